@@ -15,6 +15,10 @@ call (the multi-token form x[N, D, T] the page reserves).  ``causal_conv1d`` is 
 full-sequence prefill the page names at its top, returning the final state the
 update continues (batch or packed variable-length sequences).
 
+``selective_scan``, ``selective_update`` and ``causal_conv1d_selective_update`` (module
+``selective``) are the state-space recurrence that the convolution feeds, for prompts
+and for single tokens.
+
 There is no fallback: if the HIP library is missing, every call raises.
 """
 from __future__ import annotations
@@ -22,6 +26,9 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+
+from . import _binding, selective
+from .selective import *  # noqa: F401,F403
 
 __all__ = [
     "DCCONV_OK", "DCCONV_EINVAL", "DCCONV_EUNSUPPORTED", "DCCONV_EHIP",
@@ -31,7 +38,7 @@ __all__ = [
     "causal_conv1d_update_tokens", "dcconv_prefill", "causal_conv1d", "library_path", "DcconvError",
     "DCCONV_DEV_BAD_SEQ", "DCCONV_DEV_BAD_SEQLEN", "dcconv_stream_copy", "stream_copy",
     "dcconv_busy_spin", "busy_spin",
-]
+] + selective.__all__
 
 DCCONV_OK, DCCONV_EINVAL, DCCONV_EUNSUPPORTED, DCCONV_EHIP = 0, 1, 2, 3
 DCCONV_ACT_IDENTITY, DCCONV_ACT_SILU = 0, 1
@@ -99,6 +106,7 @@ def _load() -> ctypes.CDLL:
             lib.dcconv_stream_copy.argtypes = [vp, vp, i64, vp]      # dst, src, bytes, stream
             lib.dcconv_busy_spin.restype = i32
             lib.dcconv_busy_spin.argtypes = [ctypes.c_double, vp]     # microseconds, stream
+            selective.declare(lib)
             _lib = lib
     return _lib
 
@@ -112,6 +120,9 @@ def _raise_for(rc: int) -> None:
     if rc == DCCONV_EUNSUPPORTED:
         raise NotImplementedError(msg)
     raise DcconvError(msg or f"dcconv error {rc}")
+
+
+_binding.load, _binding.raise_for, _binding.ACTIVATIONS = _load, _raise_for, _ACTIVATIONS
 
 
 # ----------------------------------------------------------------- raw C ABI

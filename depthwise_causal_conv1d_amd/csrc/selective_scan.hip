@@ -1,0 +1,643 @@
+// The selective state-space recurrence over whole sequences for gfx950.
+//
+// Per head, with d_t = softplus(dt_t + dt_bias), a_t = d_t * a and the head's group
+// holding B and C:
+//
+//     h_t = e^{a_t} h_{t-1} + d_t x_t B_t^T,   y_t = h_t C_t + D x_t,   out_t = y_t * silu(z_t)
+//
+// Chunks of Q = 64 tokens turn this into matrix products.  With c_t the prefix sum of
+// a_t inside the chunk and H the state ahead of it,
+//
+//     Y  = (L o C B^T) X + e^{c} C H^T      L_tu = e^{c_t - c_u} d_u for u <= t, else 0
+//     H' = e^{c_Q} H + (e^{c_Q - c_u} d_u X)^T B
+//
+// so a token and head cost about 64 (k + p) + 4 p k operations on the matrix cores
+// instead of 5 p k on the vector units, and x, z and out move once.
+//
+// A wave owns 32 of a head's p and all of the state's k: H stays in its FP32
+// accumulators for the whole sequence, already in the lane order that the next
+// product reads it in (below).  A block is four such waves of one group (two heads
+// at p = 64), which share the chunk's B and C in LDS and the products C B^T, each
+// wave computing a quarter of the lower triangle and scaling it for every head of
+// the block.
+//
+// Layouts.  v_mfma_f32_16x16x32_bf16 takes, in lane l with r = l & 15 and g = l >> 4,
+// row (column) r of an operand at inner indices 8 g .. 8 g + 7, and leaves column r,
+// rows 4 g .. 4 g + 3 of the result.  The inner index may be permuted if both operands
+// agree, and the order of rows is free: state columns are numbered so that the two
+// result tiles 2 m and 2 m + 1 of H, four values each, are the eight values of one
+// operand (LDS keeps B and C with each 32 state columns permuted that way), and the p
+// of a wave's two tiles interleave by four so that a lane ends with eight consecutive
+// p of a token: one 16-byte store.  B and x, needed with tokens as the inner index
+// too, are read from LDS through the transposing load.
+//
+// Precision: B, C and x are BF16 as given; sums, prefix sums, exponentials and H are
+// FP32.  The scaled products L o C B^T and the copy of H that C reads are rounded to
+// BF16 (each about as much as the BF16 output's own rounding).  The scaled x that
+// enters H is split into SPLIT BF16 parts whose products are added up: three carry all
+// 24 bits, for states that are handed out in FP32.
+#include "selective_common.h"
+
+namespace dcconv {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kChunk = 64;
+constexpr int kScanWaves = 4;
+constexpr int kScanBlock = kWave * kScanWaves;
+constexpr int kUnitP = 32;               // p of a wave
+constexpr int kXPitch = kUnitP + 8;      // LDS row pitches, elements: rows start on
+constexpr int kPPitch = kChunk + 8;      // different banks, 16-byte aligned
+constexpr int kMaxHeads = 4;             // heads of a block (p <= 32)
+
+// How a call is cut up; the same on the host and in every kernel.
+struct ScanPlan {
+    int32_t seg;     // tokens of a segment (a multiple of kChunk)
+    int32_t nseg;    // segments of a sequence (batch form)
+    int32_t slots;   // segments in all; packed: an upper bound, some empty
+    int32_t np;      // waves a head takes: ceil(p / 32)
+    int32_t quads;   // blocks a group takes
+    int32_t heads;   // most heads of one block
+    bool split;      // some sequence may have more than one segment
+};
+
+__device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+}
+
+// Eight values of one column, from two 4-row pieces of LDS: lane 4 q + j of a
+// 16-lane row gives the address of row q, columns 4 j .. 4 j + 3, and gets
+// rows 0 .. 3 of column 4 q + j.
+__device__ __forceinline__ u32x4 load_transposed(const uint16_t *lo, const uint16_t *hi) {
+    typedef __attribute__((address_space(3))) s16x4_t *Lds;
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4_t *)lo));
+    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4_t *)hi));
+    return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+__device__ __forceinline__ u32x4 lds16(const uint16_t *p) { return *reinterpret_cast<const u32x4 *>(p); }
+
+// Up to eight consecutive BF16 values at s, of which `count` exist: zeros behind.
+template <bool WIDE>
+__device__ __forceinline__ u32x4 load8(const uint16_t *s, int count) {
+    u32x4 v = {0, 0, 0, 0};
+    if (WIDE) {
+        if (count > 0) v = *reinterpret_cast<const u32x4 *>(s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < count) v[i >> 1] |= (uint32_t)s[i] << (16 * (i & 1));
+    }
+    return v;
+}
+
+constexpr float kHuge = 3.0e38f;
+__device__ __forceinline__ bool is_finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
+
+// acc + the two BF16 values of w.
+__device__ __forceinline__ float sum_pair(uint32_t w, float acc) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 ones = __builtin_bit_cast(bf16x2, 0x3f803f80u);
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), ones, acc, false);
+}
+
+// w with a value that is no number, or infinite, replaced by zero.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+    if (!is_finite(lo_f32(w))) w &= 0xffff0000u;
+    if (!is_finite(hi_f32(w))) w &= 0x0000ffffu;
+    return w;
+}
+
+struct Segment {
+    int seq, first, last, index, count;  // tokens [first, last) of sequence seq; segment `index` of `count`
+    int64_t token0;                      // the sequence's first token on the t axis
+    bool ok;
+};
+
+// The segment at position u: sequence i has positions i * nseg .. in the batch
+// form, and starts[i] / seg + i .. in the packed form (which leaves room for every
+// sequence's last, partial segment).
+__device__ __forceinline__ Segment find_segment(const SelectiveScanParams &p, const ScanPlan &plan, int u) {
+    Segment s;
+    int len;
+    if (p.starts == nullptr) {
+        s.seq = u / plan.nseg;
+        s.index = u - s.seq * plan.nseg;
+        s.token0 = 0;
+        len = p.t;
+    } else {
+        int lo = 0, hi = p.n;  // the last i with starts[i] / seg + i <= u
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((int64_t)load_uniform(p.starts, mid) / plan.seg + mid <= u)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s.seq = lo;
+        const int a = load_uniform(p.starts, lo), e = load_uniform(p.starts, lo + 1);
+        len = (a >= 0 && a <= e && e <= p.t) ? e - a : -1;
+        s.token0 = len >= 0 ? a : 0;
+        s.index = u - (int)(s.token0 / plan.seg) - lo;
+    }
+    s.count = len > 0 ? (len + plan.seg - 1) / plan.seg : 1;
+    s.ok = len >= 0 && s.index >= 0 && s.index < s.count;
+    s.first = s.ok ? s.index * plan.seg : 0;
+    s.last = s.ok ? s.first + min(len - s.first, plan.seg) : 0;
+    return s;
+}
+
+// Reports a sequence table that is not 0 = starts[0] <= ... <= starts[n] = t.
+__device__ __forceinline__ void check_table(const SelectiveScanParams &p) {
+    if (p.starts == nullptr || p.status == nullptr) return;
+    bool bad = false;
+    for (int i = threadIdx.x; i <= p.n; i += kScanBlock) {
+        const int a = p.starts[i];
+        bad |= a < 0 || a > p.t || (i == 0 && a != 0) || (i == p.n ? a != p.t : p.starts[i + 1] < a);
+    }
+    if (bad) atomicOr(p.status, DCCONV_DEV_BAD_SEQ);
+}
+
+// OUT: the outputs and final states.  Otherwise the state that each segment but a
+// sequence's last builds up from zero, and its decay, for the join.
+template <int KS, int SPLIT, bool OUT, bool WIDE>
+__global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_kernel(const SelectiveScanParams p,
+                                                                                      const ScanPlan plan) {
+    constexpr int kPitch = KS + 8;
+    constexpr int kTiles = KS / 16;
+    constexpr int kPieces = KS / 32;  // 16-byte pieces of B (of C) a thread stages
+    extern __shared__ u32x4 smem[];
+    uint16_t *sb = reinterpret_cast<uint16_t *>(smem);
+    uint16_t *sc = sb + kChunk * kPitch;
+    uint16_t *sx_all = sc + (OUT ? kChunk * kPitch : 0);
+    float *ss_all = reinterpret_cast<float *>(sx_all + kScanWaves * kChunk * kXPitch);
+    uint16_t *sp = reinterpret_cast<uint16_t *>(ss_all + kScanWaves * 4 * kChunk);
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    uint16_t *sx = sx_all + wave * kChunk * kXPitch;
+    float *ss = ss_all + wave * 4 * kChunk;  // c, d, the weight into H, e^c; 64 tokens each
+    const int per_group = p.h / p.g, units = per_group * plan.np;
+
+    if (OUT && blockIdx.x == 0) check_table(p);
+    // result tiles above the diagonal that a product over 32 tokens reads: zeros for good
+    if (OUT)
+        for (int i = tid; i < plan.heads * 2 * 16 * 16; i += kScanBlock) {
+            const int head = i >> 9, tile = (i >> 8) & 1, row = (i >> 4) & 15, col = i & 15;
+            sp[(head * kChunk + 32 * tile + row) * kPPitch + 32 * tile + 16 + col] = 0;
+        }
+
+    for_each_unit((int64_t)plan.slots * p.g * plan.quads, [&](int64_t unit) {
+        const int quad = (int)(unit % plan.quads);
+        const int64_t ug = unit / plan.quads;
+        const int group = (int)(ug % p.g), u = (int)(ug / p.g);
+        const Segment seg = find_segment(p, plan, u);
+        if (!seg.ok || (!OUT && seg.index == seg.count - 1)) return;
+
+        const int un = quad * kScanWaves + wave;
+        const bool valid = un < units;
+        const int mine = min(un, units - 1);
+        const int first_head = quad * kScanWaves / plan.np;
+        const int heads = min(quad * kScanWaves + kScanWaves - 1, units - 1) / plan.np - first_head + 1;
+        const int head_slot = mine / plan.np - first_head;
+        const int head = group * per_group + mine / plan.np;
+        const int p0 = (mine % plan.np) * kUnitP;
+        const int pcount = valid ? min(kUnitP, p.p - p0) : 0;
+
+        const int slot = route_row(p.idx, p.status, p.n, p.s, seg.seq, lane);
+        if (slot < 0) {  // a padding sequence: zeros, and no state moves
+            if (OUT)
+                for (int t = seg.first; t < seg.last; ++t)
+                    if (lane < pcount)
+                        p.out[seg.seq * p.os_n + (seg.token0 + t) * p.os_t + head * p.os_h + p0 + lane] = 0;
+            return;
+        }
+
+        // ---- the state ahead of the segment: tile m of tile pair f, rows k = 16 m + 4 g + i, column p
+        f32x4_t hs[kTiles][2];
+        const int64_t hpk = (int64_t)p.h * p.p * p.k;
+        const int64_t in_state = ((int64_t)head * p.p + p0) * p.k;
+        const bool pool_init = p.state != nullptr && p.has_init != nullptr && p.has_init[seg.seq] != 0;
+        const bool from_ws = OUT && seg.count > 1;
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = 16 * m + 4 * g + i, pc = 8 * (r >> 2) + 4 * f + (r & 3);
+                    float v = 0.0f;
+                    if (k < p.k && pc < pcount) {
+                        const int64_t at = in_state + (int64_t)pc * p.k + k;
+                        if (from_ws)
+                            v = p.workspace[u * hpk + at];
+                        else if (OUT && pool_init)
+                            v = p.state_f32 ? static_cast<const float *>(p.state)[slot * p.ss_s + at]
+                                            : bf16_bits_to_f32(static_cast<const uint16_t *>(p.state)[slot * p.ss_s + at]);
+                    }
+                    hs[m][f][i] = v;
+                }
+
+        const uint16_t *xb = p.x + seg.seq * p.xs_n + seg.token0 * p.xs_t + head * p.xs_h + p0;
+        const uint16_t *bb = p.b + seg.seq * p.bs_n + seg.token0 * p.bs_t + group * p.bs_g;
+        const uint16_t *cb = p.c + seg.seq * p.cs_n + seg.token0 * p.cs_t + group * p.cs_g;
+        const int64_t dtb = seg.seq * p.ds_n + seg.token0 * p.ds_t + head;
+        const float a2 = p.a[head] * kLog2e;
+        const float skip = OUT && p.d_skip != nullptr ? p.d_skip[head] : 0.0f;
+        float decay_sum = 0.0f;
+
+        // ---- a chunk on its way from memory
+        u32x4 nb[kPieces], nc[kPieces], nx[4];
+        float nd = 0.0f;
+        auto fetch = [&](int t0) {
+            const int rows = seg.last - t0;
+#pragma unroll
+            for (int q = 0; q < kPieces; ++q) {
+                const int i = q * kScanBlock + tid, row = i / (KS / 8), col = i % (KS / 8) * 8;
+                const int n = row < rows ? p.k - col : 0;
+                nb[q] = load8<WIDE>(bb + (int64_t)(t0 + row) * p.bs_t + col, n);
+                if (OUT) nc[q] = load8<WIDE>(cb + (int64_t)(t0 + row) * p.cs_t + col, n);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = q * 16 + (lane >> 2), col = (lane & 3) * 8;
+                nx[q] = load8<WIDE>(xb + (int64_t)(t0 + row) * p.xs_t + col, row < rows ? pcount - col : 0);
+            }
+            nd = lane < rows ? load_step(p, dtb + (int64_t)(t0 + lane) * p.ds_t, head) : 0.0f;
+        };
+
+        fetch(seg.first);
+        for (int t0 = seg.first; t0 < seg.last; t0 += kChunk) {
+            // ---- the chunk into LDS.  A 16-byte piece of B or C is two runs of four state
+            // columns of its 32: column 16 m + 4 q + i goes to 8 q + 4 m + i.
+#pragma unroll
+            for (int q = 0; q < kPieces; ++q) {
+                const int i = q * kScanBlock + tid, row = i / (KS / 8), col = i % (KS / 8) * 8;
+                const int to = row * kPitch + (col & ~31) + ((col & 8) << 1) + ((col & 16) >> 2);
+                *reinterpret_cast<u32x2 *>(sb + to) = u32x2{nb[q][0], nb[q][1]};
+                *reinterpret_cast<u32x2 *>(sb + to + 8) = u32x2{nb[q][2], nb[q][3]};
+                if (OUT) {
+                    *reinterpret_cast<u32x2 *>(sc + to) = u32x2{nc[q][0], nc[q][1]};
+                    *reinterpret_cast<u32x2 *>(sc + to + 8) = u32x2{nc[q][2], nc[q][3]};
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<u32x4 *>(sx + (q * 16 + (lane >> 2)) * kXPitch + (lane & 3) * 8) = nx[q];
+            const float d = nd, a = d * a2;
+            float before = a, behind = a;  // prefix and suffix sums over the 64 tokens
+#pragma unroll
+            for (int o = 1; o < kWave; o <<= 1) {
+                const float u1 = __shfl_up(before, o), u2 = __shfl_down(behind, o);
+                if (lane >= o) before += u1;
+                if (lane < kWave - o) behind += u2;
+            }
+            const float total = __shfl(before, kWave - 1);
+            float rest = __shfl_down(behind, 1);  // of the tokens behind this one
+            if (lane == kWave - 1) rest = 0.0f;
+            ss[lane] = before;
+            ss[kChunk + lane] = d;
+            ss[2 * kChunk + lane] = d * __builtin_amdgcn_exp2f(rest);
+            ss[3 * kChunk + lane] = __builtin_amdgcn_exp2f(before);
+            decay_sum += total;
+            __syncthreads();
+            if (t0 + kChunk < seg.last) fetch(t0 + kChunk);
+
+            f32x4_t y[4][2];
+            u32x4 xf[2][2];  // x with tokens inside: [32-token half][tile]
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const uint16_t *at = sx + (32 * s + 8 * g + (r >> 2)) * kXPitch + 8 * (r & 3) + 4 * f;
+                    xf[s][f] = load_transposed(at, at + 4 * kXPitch);
+                }
+            // An infinity or NaN of a later token must not meet the zeros of L: it is taken
+            // out of the matrix products and its terms are added one by one.
+            float probe = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) probe = sum_pair(xf[i >> 3][(i >> 2) & 1][i & 3], probe);
+            const bool bad = __any(!(__builtin_fabsf(probe) < kHuge));
+            if (bad) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) xf[i >> 3][(i >> 2) & 1][i & 3] = finite_pair(xf[i >> 3][(i >> 2) & 1][i & 3]);
+            }
+            if constexpr (OUT) {
+                // ---- C B^T of this wave's tiles, scaled for each head of the block
+#pragma unroll
+                for (int q = 0; q < 3; ++q) {
+                    const int e = q * kScanWaves + wave;  // tile (tt, ut) of the lower triangle, row by row
+                    if (e >= 10) continue;
+                    const int tt = e >= 6 ? 3 : e >= 3 ? 2 : e >= 1 ? 1 : 0, ut = e - tt * (tt + 1) / 2;
+                    f32x4_t acc = {0, 0, 0, 0};
+#pragma unroll
+                    for (int m = 0; m < KS / 32; ++m)
+                        acc = mfma(lds16(sb + (16 * ut + r) * kPitch + 32 * m + 8 * g),
+                                   lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g), acc);
+                    const int t = 16 * tt + r, u0 = 16 * ut + 4 * g;
+                    for (int hd = 0; hd < heads; ++hd) {
+                        const int owner = max((first_head + hd) * plan.np, quad * kScanWaves) - quad * kScanWaves;
+                        const float *hs4 = ss_all + owner * 4 * kChunk;
+                        const f32x4_t cu = *reinterpret_cast<const f32x4_t *>(hs4 + u0);
+                        const f32x4_t du = *reinterpret_cast<const f32x4_t *>(hs4 + kChunk + u0);
+                        const float ct = hs4[t];
+                        float v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = u0 + i <= t ? acc[i] * __builtin_amdgcn_exp2f(ct - cu[i]) * du[i] : 0.0f;
+                        *reinterpret_cast<u32x2 *>(sp + (hd * kChunk + t) * kPPitch + u0) =
+                            u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    }
+                }
+                // ---- e^c C H^T
+                u32x4 hb[KS / 32][2];
+#pragma unroll
+                for (int m = 0; m < KS / 32; ++m)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const f32x4_t h0 = hs[2 * m][f], h1 = hs[2 * m + 1][f];
+                        hb[m][f] = u32x4{pack_bf16x2(h0[0], h0[1]), pack_bf16x2(h0[2], h0[3]),
+                                         pack_bf16x2(h1[0], h1[1]), pack_bf16x2(h1[2], h1[3])};
+                    }
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {
+                    y[tt][0] = y[tt][1] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+                    for (int m = 0; m < KS / 32; ++m) {
+                        const u32x4 cf = lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g);
+                        y[tt][0] = mfma(hb[m][0], cf, y[tt][0]);
+                        y[tt][1] = mfma(hb[m][1], cf, y[tt][1]);
+                    }
+                    const float e = ss[3 * kChunk + 16 * tt + r];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[tt][0][i] *= e;
+                        y[tt][1][i] *= e;
+                    }
+                }
+                __syncthreads();
+                // ---- (L o C B^T) X
+                const uint16_t *mp = sp + head_slot * kChunk * kPPitch;
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                    for (int s = 0; s <= tt / 2; ++s) {
+                        const u32x4 pf = lds16(mp + (16 * tt + r) * kPPitch + 32 * s + 8 * g);
+                        y[tt][0] = mfma(xf[s][0], pf, y[tt][0]);
+                        y[tt][1] = mfma(xf[s][1], pf, y[tt][1]);
+                    }
+                if (bad) {
+#pragma unroll
+                    for (int tt = 0; tt < 4; ++tt)
+                        for (int q = 0; q <= 16 * tt + r; ++q)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float v = bf16_bits_to_f32(sx[q * kXPitch + 8 * g + i]);
+                                if (!is_finite(v))
+                                    y[tt][i >> 2][i & 3] += bf16_bits_to_f32(mp[(16 * tt + r) * kPPitch + q]) * v;
+                            }
+                }
+            }
+
+            // ---- H' = e^{c_Q} H + (scaled x)^T B
+            const float dec = __builtin_amdgcn_exp2f(total);
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) hs[m][f][i] *= dec;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const float *w = ss + 2 * kChunk + 32 * s + 8 * g;
+                u32x4 xw[SPLIT][2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v0 = lo_f32(xf[s][f][i]) * w[2 * i], v1 = hi_f32(xf[s][f][i]) * w[2 * i + 1];
+#pragma unroll
+                        for (int part = 0; part < SPLIT; ++part) {
+                            const uint32_t h = pack_bf16x2(v0, v1);
+                            xw[part][f][i] = h;
+                            v0 -= lo_f32(h);
+                            v1 -= hi_f32(h);
+                        }
+                    }
+#pragma unroll
+                for (int m = 0; m < kTiles; ++m) {
+                    const uint16_t *at = sb + (32 * s + 8 * g + (r >> 2)) * kPitch + 32 * (m >> 1) + 8 * (r & 3) + 4 * (m & 1);
+                    const u32x4 bt = load_transposed(at, at + 4 * kPitch);
+#pragma unroll
+                    for (int part = SPLIT - 1; part >= 0; --part) {
+                        hs[m][0] = mfma(bt, xw[part][0], hs[m][0]);
+                        hs[m][1] = mfma(bt, xw[part][1], hs[m][1]);
+                    }
+                }
+            }
+
+            if (bad) {
+                for (int q = 0; q < kChunk; ++q)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const float v = bf16_bits_to_f32(sx[q * kXPitch + 8 * (r >> 2) + 4 * f + (r & 3)]);
+                        if (is_finite(v)) continue;
+                        const float w = ss[2 * kChunk + q] * v;
+#pragma unroll
+                        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                hs[m][f][i] += w * bf16_bits_to_f32(sb[q * kPitch + 32 * (m >> 1) + 8 * g + 4 * (m & 1) + i]);
+                    }
+            }
+
+            // ---- skip, gate and store: eight consecutive p of a token a lane
+            if constexpr (OUT) {
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {
+                    const int row = 16 * tt + r, t = t0 + row, n = pcount - 8 * g;
+                    if (t >= seg.last || n <= 0) continue;
+                    const u32x4 xv = lds16(sx + row * kXPitch + 8 * g);
+                    const int64_t tok = seg.token0 + t;
+                    float o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(skip, (i & 1) ? hi_f32(xv[i >> 1]) : lo_f32(xv[i >> 1]), y[tt][i >> 2][i & 3]);
+                    if (p.z != nullptr) {
+                        const u32x4 zv = load8<WIDE>(p.z + seg.seq * p.zs_n + tok * p.zs_t + head * p.zs_h + p0 + 8 * g, n);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] *= silu((i & 1) ? hi_f32(zv[i >> 1]) : lo_f32(zv[i >> 1]));
+                    }
+                    uint16_t *to = p.out + seg.seq * p.os_n + tok * p.os_t + head * p.os_h + p0 + 8 * g;
+                    const u32x4 ov = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+                    if (WIDE) {
+                        *reinterpret_cast<u32x4 *>(to) = ov;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i < n) to[i] = (uint16_t)(ov[i >> 1] >> (16 * (i & 1)));
+                    }
+                }
+            }
+            __syncthreads();
+        }
+
+        // ---- the state behind the segment
+        const bool to_pool = OUT && p.state != nullptr && seg.index == seg.count - 1;
+        if (OUT && !to_pool) return;
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = 16 * m + 4 * g + i, pc = 8 * (r >> 2) + 4 * f + (r & 3);
+                    if (k >= p.k || pc >= pcount) continue;
+                    const int64_t at = in_state + (int64_t)pc * p.k + k;
+                    if (!OUT)
+                        p.workspace[(u + 1) * hpk + at] = hs[m][f][i];
+                    else if (p.state_f32)
+                        static_cast<float *>(p.state)[slot * p.ss_s + at] = hs[m][f][i];
+                    else
+                        static_cast<uint16_t *>(p.state)[slot * p.ss_s + at] = f32_to_bf16_bits(hs[m][f][i]);
+                }
+        if (!OUT && valid && p0 == 0 && lane == 0)
+            p.workspace[plan.slots * hpk + (int64_t)(u + 1) * p.h + head] = __builtin_amdgcn_exp2f(decay_sum);
+    });
+}
+
+// The states ahead of every segment, in place: position u + 1 of the workspace
+// holds what segment u built up from zero and its decay.
+__global__ __launch_bounds__(256) void selective_join_kernel(const SelectiveScanParams p, const ScanPlan plan,
+                                                             int blocks_per_seq) {
+    const int64_t hpk = (int64_t)p.h * p.p * p.k;
+    for_each_unit((int64_t)p.n * blocks_per_seq, [&](int64_t unit) {
+        const int seq = (int)(unit / blocks_per_seq);
+        const int64_t e = (unit % blocks_per_seq) * 256 + threadIdx.x;
+        int u0 = seq * plan.nseg;
+        if (p.starts != nullptr) {
+            const int a = load_uniform(p.starts, seq);
+            if (a < 0 || a > p.t) return;
+            u0 = a / plan.seg + seq;
+        }
+        const Segment seg = find_segment(p, plan, u0);
+        if (!seg.ok || seg.seq != seq || seg.count < 2) return;
+        const int slot = route_row(p.idx, nullptr, p.n, p.s, seq, threadIdx.x & 63);
+        if (e >= hpk) return;
+        const int head = (int)(e / ((int64_t)p.p * p.k));
+        float run = 0.0f;
+        if (slot >= 0 && p.state != nullptr && p.has_init != nullptr && p.has_init[seq] != 0)
+            run = p.state_f32 ? static_cast<const float *>(p.state)[slot * p.ss_s + e]
+                              : bf16_bits_to_f32(static_cast<const uint16_t *>(p.state)[slot * p.ss_s + e]);
+        float *ws = p.workspace + u0 * hpk + e;
+        const float *dec = p.workspace + plan.slots * hpk + (int64_t)u0 * p.h + head;
+        ws[0] = run;
+        for (int j = 1; j < seg.count; ++j) {
+            run = __builtin_fmaf(run, dec[(int64_t)j * p.h], ws[j * hpk]);
+            ws[j * hpk] = run;
+        }
+    });
+}
+
+// Two blocks a CU fill the card.  Sequences are cut into segments only while
+// there are fewer blocks than that, and not below kMinSegment tokens: a segment
+// costs another pass over its x and B, and a state's round trip through memory.
+constexpr int64_t kFullGrid = 512;
+constexpr int64_t kMinSegment = 256;
+
+ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, bool packed) {
+    ScanPlan plan;
+    plan.np = (int32_t)((p + kUnitP - 1) / kUnitP);
+    plan.quads = (int32_t)((h / g * plan.np + kScanWaves - 1) / kScanWaves);
+    plan.heads = plan.np == 1 ? kMaxHeads : 2;
+    const int64_t per_slot = g * plan.quads;
+    const int64_t tokens = packed ? t : n * t;  // the whole call's
+    int64_t seg = tokens * per_slot / kFullGrid;
+    seg = (seg + kChunk - 1) / kChunk * kChunk;
+    if (seg < kMinSegment) seg = kMinSegment;
+    if (seg >= t) seg = (t + kChunk - 1) / kChunk * kChunk;
+    if (seg < kChunk) seg = kChunk;
+    plan.seg = (int32_t)seg;
+    plan.nseg = (int32_t)(t > 0 ? (t + seg - 1) / seg : 1);
+    plan.split = plan.nseg > 1;
+    plan.slots = (int32_t)(packed ? t / seg + n : n * plan.nseg);
+    return plan;
+}
+
+// Lets a kernel use a CU's whole LDS; once for each device, whose bit of *done is
+// then set.
+hipError_t allow_lds(const void *kernel, uint64_t *done) {
+    int dev = 0;
+    const hipError_t err = hipGetDevice(&dev);
+    if (err != hipSuccess) return err;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (__atomic_load_n(done, __ATOMIC_RELAXED) & bit) return hipSuccess;
+    const hipError_t set = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (set == hipSuccess) __atomic_fetch_or(done, bit, __ATOMIC_RELAXED);
+    return set;
+}
+
+template <int KS, int SPLIT, bool OUT, bool WIDE>
+uint64_t lds_allowed = 0;
+
+template <int KS, int SPLIT, bool OUT, bool WIDE>
+hipError_t launch_pass(const SelectiveScanParams &p, const ScanPlan &plan, hipStream_t stream) {
+    const int64_t units = (int64_t)plan.slots * p.g * plan.quads;
+    const size_t lds = (size_t)(OUT ? 2 : 1) * kChunk * (KS + 8) * 2 + (size_t)kScanWaves * kChunk * kXPitch * 2 +
+                       (size_t)kScanWaves * 4 * kChunk * 4 + (OUT ? (size_t)plan.heads * kChunk * kPPitch * 2 : 0);
+    auto kernel = selective_scan_kernel<KS, SPLIT, OUT, WIDE>;
+    const hipError_t allowed = allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, SPLIT, OUT, WIDE>);
+    if (allowed != hipSuccess) return allowed;
+    kernel<<<dim3((unsigned)(units < kMaxBlocks ? units : kMaxBlocks)), kScanBlock, lds, stream>>>(p, plan);
+    return hipGetLastError();
+}
+
+template <int KS, int SPLIT, bool WIDE>
+hipError_t launch_passes(const SelectiveScanParams &p, const ScanPlan &plan, hipStream_t stream) {
+    if (plan.split) {
+        hipError_t err = launch_pass<KS, SPLIT, false, WIDE>(p, plan, stream);
+        if (err != hipSuccess) return err;
+        const int64_t per_seq = ((int64_t)p.h * p.p * p.k + 255) / 256, units = per_seq * p.n;
+        selective_join_kernel<<<dim3((unsigned)(units < kMaxBlocks ? units : kMaxBlocks)), 256, 0, stream>>>(
+            p, plan, (int)per_seq);
+        err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return launch_pass<KS, SPLIT, true, WIDE>(p, plan, stream);
+}
+
+template <int KS>
+hipError_t launch_ks(const SelectiveScanParams &p, const ScanPlan &plan, bool wide, hipStream_t stream) {
+    const bool exact = p.state != nullptr && p.state_f32;
+    if (wide) return exact ? launch_passes<KS, 3, true>(p, plan, stream) : launch_passes<KS, 1, true>(p, plan, stream);
+    return exact ? launch_passes<KS, 3, false>(p, plan, stream) : launch_passes<KS, 1, false>(p, plan, stream);
+}
+
+// Whether rows at p with the given element strides start on 16 bytes.
+bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
+}
+
+}  // namespace
+
+int64_t selective_scan_workspace_floats(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k, bool packed) {
+    const ScanPlan plan = make_plan(n, t, h, p, g, packed);
+    return plan.split ? plan.slots * (h * p * k + h) : 0;
+}
+
+hipError_t launch_selective_scan(const SelectiveScanParams &p, hipStream_t stream, const char **kernel_name) {
+    const ScanPlan plan = make_plan(p.n, p.t, p.h, p.p, p.g, p.starts != nullptr);
+    const bool wide = p.p % 8 == 0 && p.k % 8 == 0 && rows16(p.x, p.xs_n, p.xs_t, p.xs_h) &&
+                      rows16(p.b, p.bs_n, p.bs_t, p.bs_g) && rows16(p.c, p.cs_n, p.cs_t, p.cs_g) &&
+                      (p.z == nullptr || rows16(p.z, p.zs_n, p.zs_t, p.zs_h)) &&
+                      rows16(p.out, p.os_n, p.os_t, p.os_h);
+    *kernel_name = plan.split ? (wide ? "selective_scan_split" : "selective_scan_split_scalar")
+                              : (wide ? "selective_scan" : "selective_scan_scalar");
+    if (p.k <= 64) return launch_ks<64>(p, plan, wide, stream);
+    if (p.k <= 128) return launch_ks<128>(p, plan, wide, stream);
+    return launch_ks<256>(p, plan, wide, stream);
+}
+
+}  // namespace dcconv

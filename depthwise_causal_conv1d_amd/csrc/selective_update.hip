@@ -1,0 +1,290 @@
+// One token of the selective state-space recurrence for gfx950, with or without
+// the causal convolution ahead of it.
+//
+// For row n, head i (its B and C belong to group i / (h/g)) and the slot the row
+// selects, with d = softplus(dt + dt_bias):
+//
+//     state[p, k] = exp(d * a[i]) * state[p, k] + d * x[p] * B[k]
+//     out[p]      = (sum_k state[p, k] * C[k] + D[i] * x[p]) * silu(z[p])
+//
+// The state is read and written once and everything else is a few percent of it:
+// HBM bounds the call.  A block takes up to 64 rows p of one head.  Sixteen lanes
+// share a row, so the sum over k is four DPP steps, and each lane has all of its
+// state vectors in flight before the small operands (x, B, C: 2 bytes each, any
+// strides) pass through LDS.  All arithmetic is FP32; a BF16 state is rounded
+// when it is stored, after C has read the unrounded value.
+//
+// The fused form computes x, B and C as the width-4 convolution of its channels
+// (kept in FP32, not rounded to BF16 between the two operators).  Every block of
+// a group needs the group's B and C channels, and the convolution state of those
+// is advanced in place: each block counts itself in `arrivals[row, group]` once
+// it has read them, and the block that completes the count writes their state
+// and sets the count back to zero.  Nothing waits on the count.
+#include "selective_common.h"
+
+namespace dcconv {
+namespace {
+
+constexpr int kUpdateBlock = 256;
+constexpr int kRowLanes = 16;                        // lanes that share a state row
+constexpr int kGroups = kUpdateBlock / kRowLanes;    // rows a block holds at a time
+constexpr int kMaxK = 256;
+
+template <bool F32, int VEC>
+struct StateVec;
+template <>
+struct StateVec<true, 4> {
+    u32x4 w;
+    __device__ __forceinline__ void load(const void *s, int64_t at) {
+        w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(static_cast<const float *>(s) + at));
+    }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(w[i]); }
+    __device__ __forceinline__ void set(int i, float v) { w[i] = __float_as_uint(v); }
+    __device__ __forceinline__ void store(void *s, int64_t at) const {
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(static_cast<float *>(s) + at));
+    }
+};
+template <>
+struct StateVec<false, 8> {
+    u32x4 w;
+    float v[8];
+    __device__ __forceinline__ void load(const void *s, int64_t at) {
+        w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(s) + at));
+    }
+    __device__ __forceinline__ float get(int i) const { return (i & 1) ? hi_f32(w[i >> 1]) : lo_f32(w[i >> 1]); }
+    __device__ __forceinline__ void set(int i, float x) { v[i] = x; }
+    __device__ __forceinline__ void store(void *s, int64_t at) const {
+        const u32x4 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7])};
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(s) + at));
+    }
+};
+template <bool F32>
+struct StateVec<F32, 1> {
+    float v;
+    __device__ __forceinline__ void load(const void *s, int64_t at) {
+        v = F32 ? static_cast<const float *>(s)[at] : bf16_bits_to_f32(static_cast<const uint16_t *>(s)[at]);
+    }
+    __device__ __forceinline__ float get(int) const { return v; }
+    __device__ __forceinline__ void set(int, float x) { v = x; }
+    __device__ __forceinline__ void store(void *s, int64_t at) const {
+        if (F32)
+            static_cast<float *>(s)[at] = v;
+        else
+            static_cast<uint16_t *>(s)[at] = f32_to_bf16_bits(v);
+    }
+};
+
+// The sum over the 16 lanes of a row, in all of them.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_sum(float v) {
+    v = dpp_add<0x128>(v);  // rotations of the row by 8, 4, 2 and 1
+    v = dpp_add<0x124>(v);
+    v = dpp_add<0x122>(v);
+    return dpp_add<0x121>(v);
+}
+
+// Channel `ch` of the fused form: the convolution of its history and this token.
+// The three newest values and x are left in `taps` for the state's advance.
+__device__ __forceinline__ float conv_channel(const SelectiveUpdateParams &p, int row, int64_t base, int seen, int ch,
+                                              uint16_t (&taps)[4]) {
+    const uint16_t *st = p.conv_state + base + (int64_t)ch * p.st_d;
+    if (p.seqlens == nullptr) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) taps[j] = st[(int64_t)(p.l - 3 + j) * p.st_l];
+    } else {
+        const int at = seen % p.l;
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            int q = at - 3 + j;
+            if (q < 0) q += p.l;
+            taps[j] = st[(int64_t)q * p.st_l];
+        }
+    }
+    taps[3] = p.xbc[(int64_t)row * p.xbcs_n + ch];
+    float acc = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        acc = __builtin_fmaf(bf16_bits_to_f32(taps[j]), bf16_bits_to_f32(p.weight[(int64_t)ch * 4 + j]), acc);
+    if (p.bias != nullptr) acc += bf16_bits_to_f32(p.bias[ch]);
+    return p.silu ? silu(acc) : acc;
+}
+
+// Advances channel ch's convolution state by the token in taps[3].
+__device__ __forceinline__ void conv_advance(const SelectiveUpdateParams &p, int64_t base, int seen, int ch,
+                                             const uint16_t (&taps)[4]) {
+    uint16_t *st = p.conv_state + base + (int64_t)ch * p.st_d;
+    if (p.seqlens != nullptr) {
+        st[(int64_t)(seen % p.l) * p.st_l] = taps[3];
+        return;
+    }
+    for (int j = 0; j < p.l - 3; ++j) st[j * p.st_l] = st[(j + 1) * p.st_l];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) st[(int64_t)(p.l - 3 + j) * p.st_l] = taps[j + 1];
+}
+
+// ROWS rows of the state per 16-lane group, NV vectors of VEC elements per lane
+// and row (16 * VEC * NV >= k).
+template <bool F32, int VEC, int NV, int ROWS, bool CONV>
+__global__ __launch_bounds__(kUpdateBlock) void selective_update_kernel(const SelectiveUpdateParams p) {
+    __shared__ float s_x[ROWS * kGroups], s_b[kMaxK], s_c[kMaxK];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 63, sub = tid & (kRowLanes - 1), grp = tid / kRowLanes;
+    const int ptiles = (p.p + ROWS * kGroups - 1) / (ROWS * kGroups);
+    const int per_group = p.h / p.g;
+    for_each_unit((int64_t)p.n * p.h * ptiles, [&](int64_t u) {
+        const int pt = (int)(u % ptiles);
+        const int64_t rh = u / ptiles;
+        const int head = (int)(rh % p.h), row = (int)(rh / p.h);
+        const int group = head / per_group;
+        const int p0 = pt * ROWS * kGroups;
+        int slot = route_row(p.idx, p.status, p.n, p.s, row, lane);
+        int seen = 0;
+        if (CONV && p.seqlens != nullptr) {
+            seen = p.seqlens[row];
+            if (seen < 0) {
+                if (p.status != nullptr && tid == 0) atomicOr(p.status, DCCONV_DEV_BAD_SEQLEN);
+                slot = -1;
+            }
+        }
+        uint16_t *out = p.out + (int64_t)row * p.os_n + (int64_t)head * p.os_h;
+        if (slot < 0) {  // a padding row: zeros, and no state moves
+            for (int q = p0 + tid; q < min(p.p, p0 + ROWS * kGroups); q += kUpdateBlock) out[q] = 0;
+            return;
+        }
+
+        // the state rows, all in flight at once
+        const int64_t base = (int64_t)slot * p.ss_s + (int64_t)head * p.p * p.k;
+        StateVec<F32, VEC> st[ROWS][NV];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int pr = p0 + r * kGroups + grp, k0 = (v * kRowLanes + sub) * VEC;
+                if (pr < p.p && k0 < p.k) st[r][v].load(p.state, base + (int64_t)pr * p.k + k0);
+            }
+
+        // the small operands, through LDS
+        const float step = load_step(p, (int64_t)row * p.ds_n + head, head);
+        const float decay = expf(step * p.a[head]);
+        if constexpr (!CONV) {
+            const uint16_t *x = p.x + (int64_t)row * p.xs_n + (int64_t)head * p.xs_h;
+            const uint16_t *b = p.b + (int64_t)row * p.bs_n + (int64_t)group * p.bs_g;
+            const uint16_t *c = p.c + (int64_t)row * p.cs_n + (int64_t)group * p.cs_g;
+            if (tid < ROWS * kGroups && p0 + tid < p.p) s_x[tid] = bf16_bits_to_f32(x[p0 + tid]);
+            if (tid < p.k) {
+                s_b[tid] = bf16_bits_to_f32(b[tid]);
+                s_c[tid] = bf16_bits_to_f32(c[tid]);
+            }
+            __syncthreads();
+        } else {
+            const int64_t cbase = (int64_t)slot * p.st_s;
+            const int hp = p.h * p.p;
+            uint16_t xt[4], bt[4], ct[4];
+            const int xch = head * p.p + p0 + tid, bch = hp + group * p.k + tid, cch = bch + p.g * p.k;
+            const bool has_x = tid < ROWS * kGroups && p0 + tid < p.p, has_bc = tid < p.k;
+            if (has_x) s_x[tid] = conv_channel(p, row, cbase, seen, xch, xt);
+            if (has_bc) {
+                s_b[tid] = conv_channel(p, row, cbase, seen, bch, bt);
+                s_c[tid] = conv_channel(p, row, cbase, seen, cch, ct);
+            }
+            __syncthreads();  // every lane has read its channels' history
+            if (tid == 0) {
+                int32_t *count = p.arrivals + (int64_t)row * p.g + group;
+                const int before = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                s_last = before == per_group * ptiles - 1;
+                if (s_last) __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+            if (has_x) conv_advance(p, cbase, seen, xch, xt);
+            __syncthreads();
+            if (s_last && has_bc) {
+                conv_advance(p, cbase, seen, bch, bt);
+                conv_advance(p, cbase, seen, cch, ct);
+            }
+        }
+
+        float bv[NV][VEC], cv[NV][VEC];
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int k0 = (v * kRowLanes + sub) * VEC;
+                bv[v][e] = k0 < p.k ? s_b[k0 + e] : 0.0f;
+                cv[v][e] = k0 < p.k ? s_c[k0 + e] : 0.0f;
+            }
+        const float skip = p.d_skip != nullptr ? p.d_skip[head] : 0.0f;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int pr = p0 + r * kGroups + grp;
+            if (pr >= p.p) continue;
+            const float xv = s_x[r * kGroups + grp], xd = step * xv;
+            float y = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int k0 = (v * kRowLanes + sub) * VEC;
+                if (k0 >= p.k) continue;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float s = __builtin_fmaf(xd, bv[v][e], st[r][v].get(e) * decay);
+                    y = __builtin_fmaf(s, cv[v][e], y);
+                    st[r][v].set(e, s);
+                }
+                st[r][v].store(p.state, base + (int64_t)pr * p.k + k0);
+            }
+            y = row_sum(y);
+            if (sub == 0) {
+                y = __builtin_fmaf(skip, xv, y);
+                if (p.z != nullptr)
+                    y *= silu(bf16_bits_to_f32(p.z[(int64_t)row * p.zs_n + (int64_t)head * p.zs_h + pr]));
+                out[pr] = f32_to_bf16_bits(y);
+            }
+        }
+        __syncthreads();  // the next unit reuses the LDS arrays
+    });
+}
+
+// Four state rows per 16-lane group while the grid still holds this many blocks.
+constexpr int64_t kMinBlocksForFourRows = 2048;
+
+template <bool F32, int VEC, int NV>
+hipError_t launch_rows(const SelectiveUpdateParams &p, hipStream_t stream) {
+    const int64_t heads = (int64_t)p.n * p.h;
+    const bool four = heads * ((p.p + 63) / 64) >= kMinBlocksForFourRows;
+    const int64_t units = heads * (four ? (p.p + 63) / 64 : (p.p + 15) / 16);
+    const dim3 grid((unsigned)(units < kMaxBlocks ? units : kMaxBlocks));
+    if (p.conv) {
+        if (four)
+            selective_update_kernel<F32, VEC, NV, 4, true><<<grid, kUpdateBlock, 0, stream>>>(p);
+        else
+            selective_update_kernel<F32, VEC, NV, 1, true><<<grid, kUpdateBlock, 0, stream>>>(p);
+    } else {
+        if (four)
+            selective_update_kernel<F32, VEC, NV, 4, false><<<grid, kUpdateBlock, 0, stream>>>(p);
+        else
+            selective_update_kernel<F32, VEC, NV, 1, false><<<grid, kUpdateBlock, 0, stream>>>(p);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_selective_update(const SelectiveUpdateParams &p, hipStream_t stream, const char **kernel_name) {
+    const int vec = p.state_f32 ? 4 : 8;
+    const bool wide = p.k % vec == 0 && p.ss_s % vec == 0 && reinterpret_cast<uintptr_t>(p.state) % 16 == 0;
+    if (!wide) {
+        *kernel_name = p.conv ? "selective_update_conv_scalar" : "selective_update_scalar";
+        return p.state_f32 ? launch_rows<true, 1, 16>(p, stream) : launch_rows<false, 1, 16>(p, stream);
+    }
+    if (p.state_f32) {
+        *kernel_name = p.conv ? "selective_update_conv<f32>" : "selective_update<f32>";
+        if (p.k <= 64) return launch_rows<true, 4, 1>(p, stream);
+        return p.k <= 128 ? launch_rows<true, 4, 2>(p, stream) : launch_rows<true, 4, 4>(p, stream);
+    }
+    *kernel_name = p.conv ? "selective_update_conv<bf16>" : "selective_update<bf16>";
+    return p.k <= 128 ? launch_rows<false, 8, 1>(p, stream) : launch_rows<false, 8, 2>(p, stream);
+}
+
+}  // namespace dcconv

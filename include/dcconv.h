@@ -53,6 +53,9 @@ enum {
  * contains no activation code. */
 enum { DCCONV_ACT_IDENTITY = 0, DCCONV_ACT_SILU = 1 };
 
+/* Element types where an operand may have either. */
+enum { DCCONV_DTYPE_BF16 = 0, DCCONV_DTYPE_F32 = 1 };
+
 /* Bits OR-ed into *dev_status by the device when a routing entry is rejected. */
 enum {
     DCCONV_DEV_BAD_INDEX = 1, /* an index below -1, or not below S           */
@@ -246,6 +249,110 @@ int dcconv_prefill(const void *x, int64_t n, int64_t d, int64_t t,
                    void *out, int64_t os_n, int64_t os_d, int64_t os_t,
                    int32_t *dev_status,
                    void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The state-space recurrence behind the convolution.
+ *
+ * Heads i = 0..h-1 of p channels each; B and C of k values belong to the head's
+ * group i / (h/g).  With d = softplus(dt + dt_bias[i]) (or dt + dt_bias[i]
+ * without dt_softplus), a head's state H [p, k] and a token's x, B and C:
+ *
+ *     H    = exp(d * a[i]) * H + d * x B^T
+ *     y    = H C + d_skip[i] * x
+ *     out  = y * SiLU(z)                        (y without z)
+ *
+ * Sums, exponentials and the recurrence are FP32; out, and a BF16 state, are
+ * rounded once.  The decay has one rate per head (a[i], usually negative).
+ *
+ * Operands of all three entry points:
+ *  x, z, out   BF16, p unit-stride channels of a head; the other strides are given
+ *              in elements, >= 0.  z may be NULL.  out must give every element its
+ *              own address.
+ *  b, c        BF16, k unit-stride values of a group.  1 <= k <= 256.
+ *  dt          BF16 or F32 (dt_dtype), h unit-stride values of a token.
+ *  dt_bias, a, d_skip  F32 [h]; dt_bias and d_skip may be NULL (zero).
+ *  ssm_state   F32 or BF16 (state_dtype) [s, h, p, k], slots ss_s elements apart
+ *              and dense inside, READ AND WRITTEN.
+ *  state_indices, dev_status, stream: as conv_state_indices, dev_status and stream
+ *              of dcconv_update: -1 is a padding row (zero output, no state moves);
+ *              a bad index, and with dev_status a duplicate one, makes a row padding.
+ * Operands are aligned to their elements; rows that start on 16 bytes (and sizes
+ * that are multiples of 8) take 16-byte accesses.  Nothing that a call writes may
+ * lie within the range another operand spans.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * dcconv_selective_update -- one token of n rows, in place.
+ * x [n, h, p] (strides xs_n, xs_h), dt [n, h] (ds_n), b and c [n, g, k], z and out
+ * [n, h, p].  n == 0 returns DCCONV_OK and enqueues nothing.
+ * Returns DCCONV_OK, DCCONV_EINVAL, DCCONV_EUNSUPPORTED (k > 256, or sizes past
+ * n, s < 2^31, h*p and g*k <= 2^26) or DCCONV_EHIP.
+ */
+int dcconv_selective_update(const void *x, int64_t n, int64_t h, int64_t p, int64_t xs_n, int64_t xs_h,
+                            const void *dt, int dt_dtype, int64_t ds_n, const float *dt_bias, int dt_softplus,
+                            const float *a, const void *b, const void *c, int64_t g, int64_t k,
+                            int64_t bs_n, int64_t bs_g, int64_t cs_n, int64_t cs_g,
+                            const float *d_skip, const void *z, int64_t zs_n, int64_t zs_h,
+                            void *ssm_state, int state_dtype, int64_t s, int64_t ss_s,
+                            const int32_t *state_indices, void *out, int64_t os_n, int64_t os_h,
+                            int32_t *dev_status, void *stream);
+
+/*
+ * dcconv_conv_selective_update -- one token through the convolution and the
+ * recurrence, both states in place, in one launch.
+ * xbc         BF16 [n, d], d = h*p + 2*g*k channels ordered x | B | C, row stride
+ *             xbcs_n.  Every channel passes the convolution of dcconv_update
+ *             (weight [d, 4], bias [d] or NULL, activation), whose result enters the
+ *             recurrence in FP32, without the rounding to BF16 between two calls.
+ * conv_state  BF16 [s, d, l] at any strides that give every element its own address,
+ *             l >= 3; with cache_seqlens (int32 [n] or NULL) a circular buffer, as
+ *             for dcconv_update.  Both states use the same slots.
+ * workspace   int32 [n*g] on the device, zero before the first call that uses it; a
+ *             call leaves it zero.  Calls that may run at the same time need one each.
+ * Returns as dcconv_selective_update; w != 4 is DCCONV_EUNSUPPORTED.
+ */
+int dcconv_conv_selective_update(const void *xbc, int64_t n, int64_t h, int64_t p, int64_t g, int64_t k,
+                                 int64_t xbcs_n, void *conv_state, int64_t l, int64_t st_s, int64_t st_d,
+                                 int64_t st_l, const void *weight, int64_t w, const void *bias,
+                                 const int32_t *cache_seqlens, int activation,
+                                 const void *dt, int dt_dtype, int64_t ds_n, const float *dt_bias, int dt_softplus,
+                                 const float *a, const float *d_skip, const void *z, int64_t zs_n, int64_t zs_h,
+                                 void *ssm_state, int state_dtype, int64_t s, int64_t ss_s,
+                                 const int32_t *state_indices, void *out, int64_t os_n, int64_t os_h,
+                                 int32_t *workspace, int32_t *dev_status, void *stream);
+
+/*
+ * dcconv_selective_scan -- whole sequences (prefill).
+ * x, z, out [n, t, h, p], dt [n, t, h], b and c [n, t, g, k]; or, with seq_starts
+ * (device int32 [n+1], as for dcconv_prefill), n packed sequences on one axis of t
+ * tokens, the _n strides unused.
+ * ssm_state   NULL (with s == 0, no indices and no has_initial_state: every sequence
+ *             starts from zero and its final state is dropped), or the pool: sequence
+ *             i starts from its slot's state where has_initial_state[i] (uint8 [n],
+ *             NULL: nowhere) is nonzero, from zero elsewhere, and leaves its final
+ *             state there.  An empty sequence leaves its initial state or zeros.
+ * workspace   dcconv_selective_scan_workspace() bytes, 16-byte aligned; its contents
+ *             need not be kept and are not read from one call to the next.
+ * A finite dt is assumed; an infinity or NaN in x, B, C or z reaches the outputs and
+ * the state that the recurrence takes it to, and no other.
+ * Returns as dcconv_selective_update.
+ */
+int dcconv_selective_scan(const void *x, int64_t n, int64_t t, int64_t h, int64_t p,
+                          int64_t xs_n, int64_t xs_t, int64_t xs_h,
+                          const void *dt, int dt_dtype, int64_t ds_n, int64_t ds_t,
+                          const float *dt_bias, int dt_softplus, const float *a,
+                          const void *b, const void *c, int64_t g, int64_t k,
+                          int64_t bs_n, int64_t bs_t, int64_t bs_g, int64_t cs_n, int64_t cs_t, int64_t cs_g,
+                          const float *d_skip, const void *z, int64_t zs_n, int64_t zs_t, int64_t zs_h,
+                          const int32_t *seq_starts, void *ssm_state, int state_dtype, int64_t s, int64_t ss_s,
+                          const int32_t *state_indices, const uint8_t *has_initial_state,
+                          void *out, int64_t os_n, int64_t os_t, int64_t os_h,
+                          void *workspace, int64_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Bytes of workspace that dcconv_selective_scan needs for these sizes (0: none, the
+ * pointer may be NULL).  `packed` is nonzero with seq_starts. */
+int64_t dcconv_selective_scan_workspace(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k,
+                                        int packed);
 
 /*
  * dcconv_stream_copy -- measurement control, not part of the operation.
