@@ -411,3 +411,81 @@ extern "C" int dcconv_selective_scan(const void *x, int64_t n, int64_t t, int64_
     if (err != hipSuccess) return fail(DCCONV_EHIP, "kernel launch failed: %s", hipGetErrorString(err));
     return succeed(name);
 }
+
+namespace {
+
+// Shapes of a 4-bit weight matrix.
+int check_w4(int64_t n, int64_t k) {
+    if (n < 1 || k < 1)
+        return fail(DCCONV_EINVAL, "n and k must be >= 1, got %lld and %lld", (long long)n, (long long)k);
+    if (n > (1 << 24) || k > (1 << 24))
+        return fail(DCCONV_EUNSUPPORTED, "n and k above 2^24 are not served, got %lld and %lld", (long long)n,
+                    (long long)k);
+    return DCCONV_OK;
+}
+
+int64_t w4_bytes(int64_t n, int64_t k) { return (n + 15) / 16 * ((k + 127) / 128) * 1024; }
+
+}  // namespace
+
+extern "C" int dcconv_w4_matvec(const void *x, int64_t m, int64_t k, int64_t xs_m, const void *qweight, int64_t n,
+                                const void *scales, const uint8_t *zeros, int64_t group_size, const void *bias,
+                                void *out, int64_t os_m, void *stream) {
+    int rc = check_w4(n, k);
+    if (rc != DCCONV_OK) return rc;
+    if (m < 0) return fail(DCCONV_EINVAL, "m must be >= 0, got %lld", (long long)m);
+    if (group_size < 1) return fail(DCCONV_EINVAL, "group_size must be >= 1, got %lld", (long long)group_size);
+    if (xs_m < 0 || os_m < 0) return fail(DCCONV_EINVAL, "strides must be non-negative");
+    if (group_size % 32 != 0 || group_size > (1 << 24))
+        return fail(DCCONV_EUNSUPPORTED, "group_size must be a multiple of 32 up to 2^24, got %lld",
+                    (long long)group_size);
+    if (m > (1 << 20) - 64) return fail(DCCONV_EUNSUPPORTED, "m=%lld rows are not served", (long long)m);
+    if (m == 0) return succeed("");
+    if (!x || !qweight || !scales || !out)
+        return fail(DCCONV_EINVAL, "x, qweight, scales and out must be non-NULL when m > 0");
+    if (m > 1 && os_m < n)
+        return fail(DCCONV_EINVAL, "out row stride %lld is smaller than n=%lld", (long long)os_m, (long long)n);
+    int64_t xb, ob;
+    if (!extent({m, 1, 1}, {xs_m, 0, 0}, k, 2, &xb) || !extent({m, 1, 1}, {os_m, 0, 0}, n, 2, &ob))
+        return fail(DCCONV_EINVAL, "strides span more than 2^47 bytes");
+    const int64_t groups = (k + group_size - 1) / group_size;
+    const Operand ops[] = {{"out", out, ob, 2, true},
+                           {"x", x, xb, 2, false},
+                           {"qweight", qweight, w4_bytes(n, k), 16, false},
+                           {"scales", scales, 2 * groups * n, 2, false},
+                           {"zeros", zeros, groups * n, 1, false},
+                           {"bias", bias, 2 * n, 2, false}};
+    rc = check_operands(ops);
+    if (rc != DCCONV_OK) return rc;
+
+    dcconv::W4Params q = {};
+    q.x = static_cast<const uint16_t *>(x);
+    q.xs_m = xs_m;
+    q.q = static_cast<const uint8_t *>(qweight);
+    q.scales = static_cast<const uint16_t *>(scales);
+    q.zeros = zeros;
+    q.bias = static_cast<const uint16_t *>(bias);
+    q.out = static_cast<uint16_t *>(out);
+    q.os_m = os_m;
+    q.m = (int32_t)m;
+    q.n = (int32_t)n;
+    q.k = (int32_t)k;
+    q.group = (int32_t)group_size;
+    const char *name = "";
+    const hipError_t err = dcconv::launch_w4_matvec(q, static_cast<hipStream_t>(stream), &name);
+    if (err != hipSuccess) return fail(DCCONV_EHIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return succeed(name);
+}
+
+extern "C" int dcconv_w4_pack(const uint8_t *codes, int64_t n, int64_t k, void *qweight, void *stream) {
+    int rc = check_w4(n, k);
+    if (rc != DCCONV_OK) return rc;
+    if (!codes || !qweight) return fail(DCCONV_EINVAL, "codes and qweight must be non-NULL");
+    const Operand ops[] = {{"qweight", qweight, w4_bytes(n, k), 16, true}, {"codes", codes, n * k, 1, false}};
+    rc = check_operands(ops);
+    if (rc != DCCONV_OK) return rc;
+    const hipError_t err =
+        dcconv::launch_w4_pack(codes, n, k, static_cast<uint8_t *>(qweight), static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return fail(DCCONV_EHIP, "kernel launch failed: %s", hipGetErrorString(err));
+    return succeed("w4_pack");
+}

@@ -2,7 +2,8 @@
 
 ``selective_scan`` runs whole prompts, ``selective_update`` one token a row, and
 ``causal_conv1d_selective_update`` one token through the short convolution and the
-recurrence in one launch.  Per head, with d = softplus(dt + dt_bias) and the head's
+recurrence in one launch; ``w4_matvec`` multiplies a few rows with 4-bit weights, as a
+decoding layer's projections.  Per head, with d = softplus(dt + dt_bias) and the head's
 group holding B and C::
 
     state = exp(d * A) * state + d * x B^T
@@ -23,6 +24,7 @@ __all__ = [
     "dcconv_selective_update", "dcconv_conv_selective_update", "dcconv_selective_scan",
     "dcconv_selective_scan_workspace", "selective_scan", "selective_update",
     "causal_conv1d_selective_update", "selective_update_workspace",
+    "dcconv_w4_matvec", "dcconv_w4_pack", "w4_matvec", "w4_pack",
 ]
 
 DCCONV_DTYPE_BF16, DCCONV_DTYPE_F32 = 0, 1
@@ -60,6 +62,11 @@ def declare(lib: ctypes.CDLL) -> None:
         + [vp, i64, i64, i64, vp, i64, vp, vp])       # out, os_n, os_t, os_h, workspace, bytes, status, stream
     lib.dcconv_selective_scan_workspace.restype = i64
     lib.dcconv_selective_scan_workspace.argtypes = [i64] * 6 + [i32]
+    lib.dcconv_w4_matvec.restype = i32
+    lib.dcconv_w4_matvec.argtypes = [vp, i64, i64, i64, vp, i64,       # x, m, k, xs_m, qweight, n
+                                     vp, vp, i64, vp, vp, i64, vp]     # scales, zeros, group, bias, out, os_m, stream
+    lib.dcconv_w4_pack.restype = i32
+    lib.dcconv_w4_pack.argtypes = [vp, i64, i64, vp, vp]               # codes, n, k, qweight, stream
 
 
 # ----------------------------------------------------------------- raw C ABI
@@ -83,6 +90,16 @@ def dcconv_selective_scan(*args) -> int:
 def dcconv_selective_scan_workspace(n, t, h, p, g, k, packed) -> int:
     """Bytes of workspace a scan of these sizes needs, one to one."""
     return _b.load().dcconv_selective_scan_workspace(n, t, h, p, g, k, packed)
+
+
+def dcconv_w4_matvec(*args) -> int:
+    """The 4-bit matrix-vector C entry point, one to one (pointers as ints)."""
+    return _b.load().dcconv_w4_matvec(*args)
+
+
+def dcconv_w4_pack(*args) -> int:
+    """The packing C entry point, one to one (pointers as ints)."""
+    return _b.load().dcconv_w4_pack(*args)
 
 
 # ------------------------------------------------------------ tensor front end
@@ -364,3 +381,59 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
             0 if workspace is None else workspace.numel(), _status(dev_status, dev), stream)
     _b.raise_for(rc)
     return (out, final) if final is not None else out
+
+
+def w4_pack(codes):
+    """Lay out the codes (uint8 [N, K], values 0 to 15) of a 4-bit weight matrix for
+    ``w4_matvec``: uint8 [ceil(N/16), ceil(K/128), 64, 16]."""
+    import torch
+
+    if codes.dim() != 2 or codes.dtype is not torch.uint8 or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous uint8 [N, K] tensor")
+    dev = _gpu(codes)
+    N, K = codes.shape
+    q = torch.empty(-(-N // 16), -(-K // 128), 64, 16, dtype=torch.uint8, device=dev)
+    with _b.on(dev) as stream:
+        rc = _b.load().dcconv_w4_pack(codes.data_ptr(), N, K, q.data_ptr(), stream)
+    _b.raise_for(rc)
+    return q
+
+
+def w4_matvec(x, qweight, scales, zeros=None, bias=None, *, group_size, out=None):
+    """x [M, K] (bf16) times a 4-bit weight matrix: out [M, N], with
+    out[m, n] = sum_k x[m, k] * (code[n, k] - zeros[k // group_size, n]) * scales[k // group_size, n] + bias[n].
+
+    qweight: ``w4_pack``'s tiles; scales: bf16 [ceil(K / group_size), N]; zeros: uint8 of
+    that shape or None (8); bias: bf16 [N] or None; group_size: a multiple of 32."""
+    import torch
+
+    if x.dim() != 2 or scales.dim() != 2:
+        raise ValueError(f"x must be [M, K] and scales [groups, N], got {tuple(x.shape)} and {tuple(scales.shape)}")
+    dev = _gpu(x)
+    M, K = x.shape
+    N = scales.shape[1]
+    groups = -(-K // group_size) if group_size > 0 else 0
+    _bf16("x", x, (M, K), dev)
+    _bf16("scales", scales, (groups, N), dev)
+    if not scales.is_contiguous():
+        raise ValueError("scales must be contiguous")
+    if qweight.dtype is not torch.uint8 or not qweight.is_contiguous():
+        raise ValueError("qweight must be a contiguous uint8 tensor")
+    _shaped("qweight", qweight, (-(-N // 16), -(-K // 128), 64, 16), dev)
+    if zeros is not None:
+        if zeros.dtype is not torch.uint8 or not zeros.is_contiguous():
+            raise ValueError("zeros must be a contiguous uint8 tensor")
+        _shaped("zeros", zeros, (groups, N), dev)
+    if bias is not None:
+        _bf16("bias", bias, (N,), dev)
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    else:
+        _bf16("out", out, (M, N), dev)
+    with _b.on(dev) as stream:
+        rc = _b.load().dcconv_w4_matvec(
+            x.data_ptr(), M, K, x.stride(0), qweight.data_ptr(), N, scales.data_ptr(),
+            None if zeros is None else zeros.data_ptr(), group_size, None if bias is None else bias.data_ptr(),
+            out.data_ptr(), out.stride(0) if M > 1 else N, stream)
+    _b.raise_for(rc)
+    return out

@@ -355,6 +355,39 @@ int64_t dcconv_selective_scan_workspace(int64_t n, int64_t t, int64_t h, int64_t
                                         int packed);
 
 /*
+ * dcconv_w4_matvec -- a few rows times a 4-bit weight matrix, as the projections
+ * before and after the convolution and the recurrence:
+ *
+ *     out[r, i] = sum_j x[r, j] * (code[i, j] - zero[j / group_size, i])
+ *                                * scale[j / group_size, i] + bias[i]
+ *
+ * in FP32, rounded once.
+ *
+ * x, out      BF16 [m, k] and [m, n], rows xs_m and os_m elements apart (rows of x
+ *             that start on 16 bytes, with k a multiple of 8, are read 16 bytes wide).
+ * qweight     codes 0..15 of n outputs by k inputs in tiles [ceil(n/16)][ceil(k/128)]
+ *             of 64 lanes x 16 bytes, 16-byte aligned, as dcconv_w4_pack lays them
+ *             out: byte 4q + 2u + v of lane 16j + i holds output i and inputs
+ *             32q + 8j + 4v + u (low half) and 32q + 8j + 4v + 2 + u (high half) of
+ *             the tile.  Codes past n and k are not used.
+ * scales      BF16 [ceil(k/group_size), n]; zeros: uint8 likewise, or NULL (8).
+ * group_size  a multiple of 32.
+ * bias        BF16 [n] or NULL.
+ * Any m is served; the kernel is made for decode batches (it takes 64 rows at a
+ * time, and reads the weights again for the next 64).  An infinite x gives NaN.
+ * m == 0 returns DCCONV_OK and enqueues nothing.
+ * Returns DCCONV_OK, DCCONV_EINVAL, DCCONV_EUNSUPPORTED or DCCONV_EHIP.
+ */
+int dcconv_w4_matvec(const void *x, int64_t m, int64_t k, int64_t xs_m, const void *qweight, int64_t n,
+                     const void *scales, const uint8_t *zeros, int64_t group_size, const void *bias,
+                     void *out, int64_t os_m, void *stream);
+
+/* dcconv_w4_pack -- codes (uint8 [n, k] contiguous, the low four bits of each) into
+ * the tiles of dcconv_w4_matvec, ceil(n/16) * ceil(k/128) * 1024 bytes.  Once per
+ * weight matrix, when it is loaded. */
+int dcconv_w4_pack(const uint8_t *codes, int64_t n, int64_t k, void *qweight, void *stream);
+
+/*
  * dcconv_stream_copy -- measurement control, not part of the operation.
  * The page "Composing multi-kernel blocks in Python" (section "Measuring a block
  * honestly") asks for a plain baseline timed in the same run as the block it
