@@ -82,16 +82,11 @@ __device__ __forceinline__ u32x4 load_transposed(const uint16_t *lo, const uint1
 __device__ __forceinline__ u32x4 lds16(const uint16_t *p) { return *reinterpret_cast<const u32x4 *>(p); }
 
 // Up to eight consecutive BF16 values at s, of which `count` exist: zeros behind.
-template <bool WIDE>
 __device__ __forceinline__ u32x4 load8(const uint16_t *s, int count) {
     u32x4 v = {0, 0, 0, 0};
-    if (WIDE) {
-        if (count > 0) v = *reinterpret_cast<const u32x4 *>(s);
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < count) v[i >> 1] |= (uint32_t)s[i] << (16 * (i & 1));
-    }
+    for (int i = 0; i < 8; ++i)
+        if (i < count) v[i >> 1] |= (uint32_t)s[i] << (16 * (i & 1));
     return v;
 }
 
@@ -162,6 +157,121 @@ __device__ __forceinline__ void check_table(const SelectiveScanParams &p) {
     if (bad) atomicOr(p.status, DCCONV_DEV_BAD_SEQ);
 }
 
+// Sums over the 64 lanes of a wave: of the lanes up to this one, and of the lanes
+// behind it (each formed from small to large distances, so that the decay of a
+// recent token is not the difference of two long sums).
+template <int CTRL>
+__device__ __forceinline__ float dpp_shift(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+__device__ __forceinline__ void wave_sums(float v, int lane, float *upto, float *behind, float *total) {
+    float u = v, b = v;  // inside each row of 16 lanes, by DPP shifts
+    u += dpp_shift<0x111>(u), b += dpp_shift<0x101>(b);
+    u += dpp_shift<0x112>(u), b += dpp_shift<0x102>(b);
+    u += dpp_shift<0x114>(u), b += dpp_shift<0x104>(b);
+    u += dpp_shift<0x118>(u), b += dpp_shift<0x108>(b);
+    const float r0 = lane_value(u, 15), r1 = lane_value(u, 31), r2 = lane_value(u, 47), r3 = lane_value(u, 63);
+    const int row = lane >> 4;
+    *upto = u + (row == 0 ? 0.0f : row == 1 ? r0 : row == 2 ? r0 + r1 : r0 + r1 + r2);
+    *total = r0 + r1 + r2 + r3;
+    b = dpp_shift<0x101>(b);  // the lanes behind this one; zero for a row's last
+    *behind = b + (row == 3 ? 0.0f : row == 2 ? r3 : row == 1 ? r2 + r3 : r1 + r2 + r3);
+}
+
+constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer
+
+// One operand's rows of a chunk, `stride` elements apart: a lane moves eight values
+// from column `col` (of which `count` exist) of rows row0, row0 + step, ...  WIDE moves
+// 16 bytes through a buffer that ends with the chunk's last row, so that what lies
+// behind it reads as zeros and is not written.
+template <bool WIDE>
+struct ChunkRows {
+    const uint16_t *base;  // wave-uniform: the chunk's first row
+    int64_t stride;
+    int32_t row0, col, count, step, rows;
+    uint32_t at0, hop, width;
+    Buffer buf;
+    __device__ __forceinline__ ChunkRows(const uint16_t *first, int64_t stride, int row0, int step, int col, int width)
+        : base(first), stride(stride), row0(row0), col(col), count(width - col), step(step), width(2u * (uint32_t)width) {
+        const uint32_t bytes = 2u * (uint32_t)stride;
+        at0 = count > 0 ? (uint32_t)row0 * bytes + 2u * (uint32_t)col : kNowhere;
+        hop = (uint32_t)step * bytes;
+    }
+    __device__ __forceinline__ void begin(int n) {
+        rows = n;
+        if (WIDE) buf = make_buffer(base, n > 0 ? (uint32_t)(n - 1) * 2u * (uint32_t)stride + width : 0u);
+    }
+    __device__ __forceinline__ void advance() { base += kChunk * stride; }
+    __device__ __forceinline__ u32x4 load(int q) const {
+        if (WIDE) return buffer_load<kCached>(buf, at0 + (uint32_t)q * hop);
+        const int row = row0 + q * step;
+        return load8(base + row * stride + col, row < rows ? count : 0);
+    }
+    __device__ __forceinline__ void store(u32x4 v, int q) const {
+        if (WIDE) {
+            buffer_store<kCached>(v, buf, at0 + (uint32_t)q * hop);
+            return;
+        }
+        const int row = row0 + q * step;
+        if (row >= rows) return;
+        uint16_t *to = const_cast<uint16_t *>(base) + row * stride + col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < count) to[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    }
+};
+
+// The kernel's arguments, read again: what is used only once a loop is done need not
+// occupy scalar registers throughout it.
+__device__ __forceinline__ const SelectiveScanParams &reread(const SelectiveScanParams &p) {
+    typedef const __attribute__((address_space(4))) SelectiveScanParams *Args;
+    Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(args));
+    return *(const SelectiveScanParams *)args;
+}
+
+// Four consecutive state values at element `at`, of which `count` exist.
+__device__ __forceinline__ f32x4_t load_state4(const void *s, bool f32, bool wide, int64_t at, int count) {
+    f32x4_t v = {0, 0, 0, 0};
+    if (wide && count >= 4) {
+        if (f32) return *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(s) + at);
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(s) + at);
+        return f32x4_t{lo_f32(w[0]), hi_f32(w[0]), lo_f32(w[1]), hi_f32(w[1])};
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < count)
+            v[i] = f32 ? static_cast<const float *>(s)[at + i]
+                       : bf16_bits_to_f32(static_cast<const uint16_t *>(s)[at + i]);
+    return v;
+}
+__device__ __forceinline__ void store_state4(void *s, bool f32, bool wide, int64_t at, int count, f32x4_t v) {
+    if (wide && count >= 4) {
+        if (f32)
+            *reinterpret_cast<f32x4_t *>(static_cast<float *>(s) + at) = v;
+        else
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(s) + at) =
+                u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < count) {
+            if (f32)
+                static_cast<float *>(s)[at + i] = v[i];
+            else
+                static_cast<uint16_t *>(s)[at + i] = f32_to_bf16_bits(v[i]);
+        }
+}
+
+// Whether the pool's rows of four state values start on whole 8 or 16 bytes.
+__device__ __forceinline__ bool wide_state(const SelectiveScanParams &p) {
+    return p.k % 4 == 0 && p.ss_s % 4 == 0 && reinterpret_cast<uintptr_t>(p.state) % 16 == 0;
+}
+
 // OUT: the outputs and final states.  Otherwise the state that each segment but a
 // sequence's last builds up from zero, and its decay, for the join.
 template <int KS, int SPLIT, bool OUT, bool WIDE>
@@ -175,14 +285,14 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_
     uint16_t *sc = sb + kChunk * kPitch;
     uint16_t *sx_all = sc + (OUT ? kChunk * kPitch : 0);
     float *ss_all = reinterpret_cast<float *>(sx_all + kScanWaves * kChunk * kXPitch);
-    uint16_t *sp = reinterpret_cast<uint16_t *>(ss_all + kScanWaves * 4 * kChunk);
+    uint16_t *sp = reinterpret_cast<uint16_t *>(ss_all + kMaxHeads * 4 * kChunk);
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     uint16_t *sx = sx_all + wave * kChunk * kXPitch;
-    float *ss = ss_all + wave * 4 * kChunk;  // c, d, the weight into H, e^c; 64 tokens each
     const int per_group = p.h / p.g, units = per_group * plan.np;
 
-    if (OUT && blockIdx.x == 0) check_table(p);
+    if (OUT && blockIdx.x == 0 && blockIdx.y == 0) check_table(p);
     // result tiles above the diagonal that a product over 32 tokens reads: zeros for good
     if (OUT)
         for (int i = tid; i < plan.heads * 2 * 16 * 16; i += kScanBlock) {
@@ -190,322 +300,322 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_
             sp[(head * kChunk + 32 * tile + row) * kPPitch + 32 * tile + 16 + col] = 0;
         }
 
-    for_each_unit((int64_t)plan.slots * p.g * plan.quads, [&](int64_t unit) {
-        const int quad = (int)(unit % plan.quads);
-        const int64_t ug = unit / plan.quads;
-        const int group = (int)(ug % p.g), u = (int)(ug / p.g);
-        const Segment seg = find_segment(p, plan, u);
-        if (!seg.ok || (!OUT && seg.index == seg.count - 1)) return;
+    const int64_t unit = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (unit >= (int64_t)plan.slots * p.g * plan.quads) return;
+    const int quad = (int)(unit % plan.quads);
+    const int64_t ug = unit / plan.quads;
+    const int group = (int)(ug % p.g), u = (int)(ug / p.g);
+    const Segment seg = find_segment(p, plan, u);
+    if (!seg.ok || (!OUT && seg.index == seg.count - 1)) return;
 
-        const int un = quad * kScanWaves + wave;
-        const bool valid = un < units;
-        const int mine = min(un, units - 1);
-        const int first_head = quad * kScanWaves / plan.np;
-        const int heads = min(quad * kScanWaves + kScanWaves - 1, units - 1) / plan.np - first_head + 1;
-        const int head_slot = mine / plan.np - first_head;
-        const int head = group * per_group + mine / plan.np;
-        const int p0 = (mine % plan.np) * kUnitP;
-        const int pcount = valid ? min(kUnitP, p.p - p0) : 0;
+    const int un = quad * kScanWaves + wave;
+    const bool valid = un < units;
+    const int mine = min(un, units - 1);
+    const int first_head = quad * kScanWaves / plan.np;
+    const int heads = min(quad * kScanWaves + kScanWaves - 1, units - 1) / plan.np - first_head + 1;
+    const int head_slot = mine / plan.np - first_head;
+    const int head = group * per_group + mine / plan.np;
+    const int p0 = (mine % plan.np) * kUnitP;
+    const int pcount = valid ? min(kUnitP, p.p - p0) : 0;
+    // the first of the block's waves that have this head computes its steps for all
+    const bool leads = un == max(mine / plan.np * plan.np, quad * kScanWaves);
+    float *ss = ss_all + head_slot * 4 * kChunk;  // c, d, the weight into H, e^c; 64 tokens each
 
-        const int slot = route_row(p.idx, p.status, p.n, p.s, seg.seq, lane);
-        if (slot < 0) {  // a padding sequence: zeros, and no state moves
-            if (OUT)
-                for (int t = seg.first; t < seg.last; ++t)
-                    if (lane < pcount)
-                        p.out[seg.seq * p.os_n + (seg.token0 + t) * p.os_t + head * p.os_h + p0 + lane] = 0;
-            return;
-        }
+    const int slot = route_row(p.idx, p.status, p.n, p.s, seg.seq, lane);
+    if (slot < 0) {  // a padding sequence: zeros, and no state moves
+        if (OUT)
+            for (int t = seg.first; t < seg.last; ++t)
+                if (lane < pcount)
+                    p.out[seg.seq * p.os_n + (seg.token0 + t) * p.os_t + head * p.os_h + p0 + lane] = 0;
+        return;
+    }
 
-        // ---- the state ahead of the segment: tile m of tile pair f, rows k = 16 m + 4 g + i, column p
-        f32x4_t hs[kTiles][2];
-        const int64_t hpk = (int64_t)p.h * p.p * p.k;
-        const int64_t in_state = ((int64_t)head * p.p + p0) * p.k;
-        const bool pool_init = p.state != nullptr && p.has_init != nullptr && p.has_init[seg.seq] != 0;
-        const bool from_ws = OUT && seg.count > 1;
+    // ---- the state ahead of the segment: tile m of p tile f, rows k = 16 m + 4 g + i, column p
+    f32x4_t hs[kTiles][2];
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) hs[m][0] = hs[m][1] = f32x4_t{0, 0, 0, 0};
+    const int64_t in_state = ((int64_t)head * p.p + p0) * p.k;
+    const bool from_ws = seg.count > 1;
+    if (OUT && (from_ws || (p.state != nullptr && p.has_init != nullptr && p.has_init[seg.seq] != 0))) {
+        const void *src = from_ws ? p.workspace + u * (int64_t)p.h * p.p * p.k : p.state;
+        const bool f32 = from_ws || p.state_f32, wide = from_ws ? p.k % 4 == 0 : wide_state(p);
+        const int64_t at = (from_ws ? 0 : slot * p.ss_s) + in_state;
 #pragma unroll
         for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = 16 * m + 4 * g + i, pc = 8 * (r >> 2) + 4 * f + (r & 3);
-                    float v = 0.0f;
-                    if (k < p.k && pc < pcount) {
-                        const int64_t at = in_state + (int64_t)pc * p.k + k;
-                        if (from_ws)
-                            v = p.workspace[u * hpk + at];
-                        else if (OUT && pool_init)
-                            v = p.state_f32 ? static_cast<const float *>(p.state)[slot * p.ss_s + at]
-                                            : bf16_bits_to_f32(static_cast<const uint16_t *>(p.state)[slot * p.ss_s + at]);
-                    }
-                    hs[m][f][i] = v;
-                }
+            for (int f = 0; f < 2; ++f) {
+                const int pc = 8 * (r >> 2) + 4 * f + (r & 3), k = 16 * m + 4 * g;
+                if (pc < pcount) hs[m][f] = load_state4(src, f32, wide, at + (int64_t)pc * p.k + k, p.k - k);
+            }
+    }
 
-        const uint16_t *xb = p.x + seg.seq * p.xs_n + seg.token0 * p.xs_t + head * p.xs_h + p0;
-        const uint16_t *bb = p.b + seg.seq * p.bs_n + seg.token0 * p.bs_t + group * p.bs_g;
-        const uint16_t *cb = p.c + seg.seq * p.cs_n + seg.token0 * p.cs_t + group * p.cs_g;
-        const int64_t dtb = seg.seq * p.ds_n + seg.token0 * p.ds_t + head;
-        const float a2 = p.a[head] * kLog2e;
-        const float skip = OUT && p.d_skip != nullptr ? p.d_skip[head] : 0.0f;
-        float decay_sum = 0.0f;
+    // ---- the operands' rows: B and C shared out over the block, the rest a wave's own
+    const int64_t tok = seg.token0 + seg.first;
+    constexpr int kRowsPerPiece = kScanBlock * 8 / KS;
+    const int brow = tid / (KS / 8), bcol = tid % (KS / 8) * 8;
+    ChunkRows<WIDE> rb(p.b + seg.seq * p.bs_n + tok * p.bs_t + group * p.bs_g, p.bs_t, brow, kRowsPerPiece, bcol, p.k);
+    ChunkRows<WIDE> rc(p.c + seg.seq * p.cs_n + tok * p.cs_t + group * p.cs_g, p.cs_t, brow, kRowsPerPiece, bcol, p.k);
+    ChunkRows<WIDE> rx(p.x + seg.seq * p.xs_n + tok * p.xs_t + head * p.xs_h + p0, p.xs_t, lane >> 2, 16, (lane & 3) * 8, pcount);
+    ChunkRows<WIDE> rz(p.z + seg.seq * p.zs_n + tok * p.zs_t + head * p.zs_h + p0, p.zs_t, r, 16, 8 * g, pcount);
+    ChunkRows<WIDE> ro(p.out + seg.seq * p.os_n + tok * p.os_t + head * p.os_h + p0, p.os_t, r, 16, 8 * g, pcount);
+    int64_t dt_at = seg.seq * p.ds_n + (tok + lane) * p.ds_t + head;
+    const float a2 = p.a[head] * kLog2e;
+    const float dt_bias = p.dt_bias != nullptr ? p.dt_bias[head] : 0.0f;
+    const float skip = OUT && p.d_skip != nullptr ? p.d_skip[head] : 0.0f;
+    const bool gated = p.z != nullptr;
+    float decay_sum = 0.0f;
 
-        // ---- a chunk on its way from memory
-        u32x4 nb[kPieces], nc[kPieces], nx[4];
-        float nd = 0.0f;
-        auto fetch = [&](int t0) {
-            const int rows = seg.last - t0;
+    // ---- a chunk on its way from memory
+    u32x4 nb[kPieces], nc[kPieces], nx[4];
+    float nd = 0.0f;
+    auto fetch = [&](int left) {
+        const int n = min(left, kChunk);
+        rb.begin(n);
 #pragma unroll
-            for (int q = 0; q < kPieces; ++q) {
-                const int i = q * kScanBlock + tid, row = i / (KS / 8), col = i % (KS / 8) * 8;
-                const int n = row < rows ? p.k - col : 0;
-                nb[q] = load8<WIDE>(bb + (int64_t)(t0 + row) * p.bs_t + col, n);
-                if (OUT) nc[q] = load8<WIDE>(cb + (int64_t)(t0 + row) * p.cs_t + col, n);
-            }
+        for (int q = 0; q < kPieces; ++q) nb[q] = rb.load(q);
+        if (OUT) {
+            rc.begin(n);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int row = q * 16 + (lane >> 2), col = (lane & 3) * 8;
-                nx[q] = load8<WIDE>(xb + (int64_t)(t0 + row) * p.xs_t + col, row < rows ? pcount - col : 0);
-            }
-            nd = lane < rows ? load_step(p, dtb + (int64_t)(t0 + lane) * p.ds_t, head) : 0.0f;
-        };
+            for (int q = 0; q < kPieces; ++q) nc[q] = rc.load(q);
+        }
+        rx.begin(n);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) nx[q] = rx.load(q);
+        if (leads && lane < n)
+            nd = p.dt_f32 ? static_cast<const float *>(p.dt)[dt_at]
+                          : bf16_bits_to_f32(static_cast<const uint16_t *>(p.dt)[dt_at]);
+        rb.advance();
+        rc.advance();
+        rx.advance();
+        dt_at += kChunk * p.ds_t;
+    };
 
-        fetch(seg.first);
-        for (int t0 = seg.first; t0 < seg.last; t0 += kChunk) {
-            // ---- the chunk into LDS.  A 16-byte piece of B or C is two runs of four state
-            // columns of its 32: column 16 m + 4 q + i goes to 8 q + 4 m + i.
+    fetch(seg.last - seg.first);
+    for (int t0 = seg.first; t0 < seg.last; t0 += kChunk) {
+        const int rows = min(seg.last - t0, kChunk);
+        // ---- the chunk into LDS.  A 16-byte piece of B or C is two runs of four state
+        // columns of its 32: column 16 m + 4 q + i goes to 8 q + 4 m + i.
 #pragma unroll
-            for (int q = 0; q < kPieces; ++q) {
-                const int i = q * kScanBlock + tid, row = i / (KS / 8), col = i % (KS / 8) * 8;
-                const int to = row * kPitch + (col & ~31) + ((col & 8) << 1) + ((col & 16) >> 2);
-                *reinterpret_cast<u32x2 *>(sb + to) = u32x2{nb[q][0], nb[q][1]};
-                *reinterpret_cast<u32x2 *>(sb + to + 8) = u32x2{nb[q][2], nb[q][3]};
-                if (OUT) {
-                    *reinterpret_cast<u32x2 *>(sc + to) = u32x2{nc[q][0], nc[q][1]};
-                    *reinterpret_cast<u32x2 *>(sc + to + 8) = u32x2{nc[q][2], nc[q][3]};
-                }
+        for (int q = 0; q < kPieces; ++q) {
+            const int to = (q * kRowsPerPiece + brow) * kPitch + (bcol & ~31) + ((bcol & 8) << 1) +
+                           ((bcol & 16) >> 2);
+            *reinterpret_cast<u32x2 *>(sb + to) = u32x2{nb[q][0], nb[q][1]};
+            *reinterpret_cast<u32x2 *>(sb + to + 8) = u32x2{nb[q][2], nb[q][3]};
+            if (OUT) {
+                *reinterpret_cast<u32x2 *>(sc + to) = u32x2{nc[q][0], nc[q][1]};
+                *reinterpret_cast<u32x2 *>(sc + to + 8) = u32x2{nc[q][2], nc[q][3]};
             }
+        }
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<u32x4 *>(sx + (q * 16 + (lane >> 2)) * kXPitch + (lane & 3) * 8) = nx[q];
-            const float d = nd, a = d * a2;
-            float before = a, behind = a;  // prefix and suffix sums over the 64 tokens
-#pragma unroll
-            for (int o = 1; o < kWave; o <<= 1) {
-                const float u1 = __shfl_up(before, o), u2 = __shfl_down(behind, o);
-                if (lane >= o) before += u1;
-                if (lane < kWave - o) behind += u2;
-            }
-            const float total = __shfl(before, kWave - 1);
-            float rest = __shfl_down(behind, 1);  // of the tokens behind this one
-            if (lane == kWave - 1) rest = 0.0f;
-            ss[lane] = before;
+        for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<u32x4 *>(sx + (q * 16 + (lane >> 2)) * kXPitch + (lane & 3) * 8) = nx[q];
+        if (leads) {
+            float d = nd + dt_bias;
+            if (p.dt_softplus) d = softplus(d);
+            if (lane >= rows) d = 0.0f;
+            float upto, behind, total;
+            wave_sums(d * a2, lane, &upto, &behind, &total);
+            ss[lane] = upto;
             ss[kChunk + lane] = d;
-            ss[2 * kChunk + lane] = d * __builtin_amdgcn_exp2f(rest);
-            ss[3 * kChunk + lane] = __builtin_amdgcn_exp2f(before);
+            ss[2 * kChunk + lane] = d * __builtin_amdgcn_exp2f(behind);
+            ss[3 * kChunk + lane] = __builtin_amdgcn_exp2f(upto);
             decay_sum += total;
-            __syncthreads();
-            if (t0 + kChunk < seg.last) fetch(t0 + kChunk);
+        }
+        __syncthreads();
+        u32x4 zv[4];
+        if (OUT && gated) {
+            rz.begin(rows);
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) zv[tt] = rz.load(tt);
+            rz.advance();
+        }
+        if (t0 + kChunk < seg.last) fetch(seg.last - t0 - kChunk);
 
-            f32x4_t y[4][2];
-            u32x4 xf[2][2];  // x with tokens inside: [32-token half][tile]
+        f32x4_t y[4][2];
+        if constexpr (OUT) {
+            // ---- C B^T of this wave's tiles, scaled for each head of the block
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const uint16_t *at = sx + (32 * s + 8 * g + (r >> 2)) * kXPitch + 8 * (r & 3) + 4 * f;
-                    xf[s][f] = load_transposed(at, at + 4 * kXPitch);
-                }
-            // An infinity or NaN of a later token must not meet the zeros of L: it is taken
-            // out of the matrix products and its terms are added one by one.
-            float probe = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) probe = sum_pair(xf[i >> 3][(i >> 2) & 1][i & 3], probe);
-            const bool bad = __any(!(__builtin_fabsf(probe) < kHuge));
-            if (bad) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) xf[i >> 3][(i >> 2) & 1][i & 3] = finite_pair(xf[i >> 3][(i >> 2) & 1][i & 3]);
-            }
-            if constexpr (OUT) {
-                // ---- C B^T of this wave's tiles, scaled for each head of the block
-#pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    const int e = q * kScanWaves + wave;  // tile (tt, ut) of the lower triangle, row by row
-                    if (e >= 10) continue;
-                    const int tt = e >= 6 ? 3 : e >= 3 ? 2 : e >= 1 ? 1 : 0, ut = e - tt * (tt + 1) / 2;
-                    f32x4_t acc = {0, 0, 0, 0};
-#pragma unroll
-                    for (int m = 0; m < KS / 32; ++m)
-                        acc = mfma(lds16(sb + (16 * ut + r) * kPitch + 32 * m + 8 * g),
-                                   lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g), acc);
-                    const int t = 16 * tt + r, u0 = 16 * ut + 4 * g;
-                    for (int hd = 0; hd < heads; ++hd) {
-                        const int owner = max((first_head + hd) * plan.np, quad * kScanWaves) - quad * kScanWaves;
-                        const float *hs4 = ss_all + owner * 4 * kChunk;
-                        const f32x4_t cu = *reinterpret_cast<const f32x4_t *>(hs4 + u0);
-                        const f32x4_t du = *reinterpret_cast<const f32x4_t *>(hs4 + kChunk + u0);
-                        const float ct = hs4[t];
-                        float v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = u0 + i <= t ? acc[i] * __builtin_amdgcn_exp2f(ct - cu[i]) * du[i] : 0.0f;
-                        *reinterpret_cast<u32x2 *>(sp + (hd * kChunk + t) * kPPitch + u0) =
-                            u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                    }
-                }
-                // ---- e^c C H^T
-                u32x4 hb[KS / 32][2];
+            for (int q = 0; q < 3; ++q) {
+                const int e = q * kScanWaves + wave;  // tile (tt, ut) of the lower triangle, row by row
+                if (e >= 10) continue;
+                const int tt = e >= 6 ? 3 : e >= 3 ? 2 : e >= 1 ? 1 : 0, ut = e - tt * (tt + 1) / 2;
+                f32x4_t acc = {0, 0, 0, 0};
 #pragma unroll
                 for (int m = 0; m < KS / 32; ++m)
+                    acc = mfma(lds16(sb + (16 * ut + r) * kPitch + 32 * m + 8 * g),
+                               lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g), acc);
+                const int t = 16 * tt + r, u0 = 16 * ut + 4 * g;
+                for (int hd = 0; hd < heads; ++hd) {
+                    const float *hs4 = ss_all + hd * 4 * kChunk;
+                    const f32x4_t cu = *reinterpret_cast<const f32x4_t *>(hs4 + u0);
+                    const f32x4_t du = *reinterpret_cast<const f32x4_t *>(hs4 + kChunk + u0);
+                    const float ct = hs4[t];
+                    float v[4];
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const f32x4_t h0 = hs[2 * m][f], h1 = hs[2 * m + 1][f];
-                        hb[m][f] = u32x4{pack_bf16x2(h0[0], h0[1]), pack_bf16x2(h0[2], h0[3]),
-                                         pack_bf16x2(h1[0], h1[1]), pack_bf16x2(h1[2], h1[3])};
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = u0 + i <= t ? acc[i] * __builtin_amdgcn_exp2f(ct - cu[i]) * du[i] : 0.0f;
+                    *reinterpret_cast<u32x2 *>(sp + (hd * kChunk + t) * kPPitch + u0) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                }
+            }
+            // ---- e^c C H^T
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) y[tt][0] = y[tt][1] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < KS / 32; ++m) {
+                u32x4 hb[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const f32x4_t h0 = hs[2 * m][f], h1 = hs[2 * m + 1][f];
+                    hb[f] = u32x4{pack_bf16x2(h0[0], h0[1]), pack_bf16x2(h0[2], h0[3]), pack_bf16x2(h1[0], h1[1]),
+                                  pack_bf16x2(h1[2], h1[3])};
+                }
 #pragma unroll
                 for (int tt = 0; tt < 4; ++tt) {
-                    y[tt][0] = y[tt][1] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-                    for (int m = 0; m < KS / 32; ++m) {
-                        const u32x4 cf = lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g);
-                        y[tt][0] = mfma(hb[m][0], cf, y[tt][0]);
-                        y[tt][1] = mfma(hb[m][1], cf, y[tt][1]);
-                    }
-                    const float e = ss[3 * kChunk + 16 * tt + r];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[tt][0][i] *= e;
-                        y[tt][1][i] *= e;
-                    }
-                }
-                __syncthreads();
-                // ---- (L o C B^T) X
-                const uint16_t *mp = sp + head_slot * kChunk * kPPitch;
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                    for (int s = 0; s <= tt / 2; ++s) {
-                        const u32x4 pf = lds16(mp + (16 * tt + r) * kPPitch + 32 * s + 8 * g);
-                        y[tt][0] = mfma(xf[s][0], pf, y[tt][0]);
-                        y[tt][1] = mfma(xf[s][1], pf, y[tt][1]);
-                    }
-                if (bad) {
-#pragma unroll
-                    for (int tt = 0; tt < 4; ++tt)
-                        for (int q = 0; q <= 16 * tt + r; ++q)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float v = bf16_bits_to_f32(sx[q * kXPitch + 8 * g + i]);
-                                if (!is_finite(v))
-                                    y[tt][i >> 2][i & 3] += bf16_bits_to_f32(mp[(16 * tt + r) * kPPitch + q]) * v;
-                            }
+                    const u32x4 cf = lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g);
+                    y[tt][0] = mfma(hb[0], cf, y[tt][0]);
+                    y[tt][1] = mfma(hb[1], cf, y[tt][1]);
                 }
             }
-
-            // ---- H' = e^{c_Q} H + (scaled x)^T B
-            const float dec = __builtin_amdgcn_exp2f(total);
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) hs[m][f][i] *= dec;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const float *w = ss + 2 * kChunk + 32 * s + 8 * g;
-                u32x4 xw[SPLIT][2];
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float v0 = lo_f32(xf[s][f][i]) * w[2 * i], v1 = hi_f32(xf[s][f][i]) * w[2 * i + 1];
-#pragma unroll
-                        for (int part = 0; part < SPLIT; ++part) {
-                            const uint32_t h = pack_bf16x2(v0, v1);
-                            xw[part][f][i] = h;
-                            v0 -= lo_f32(h);
-                            v1 -= hi_f32(h);
-                        }
-                    }
-#pragma unroll
-                for (int m = 0; m < kTiles; ++m) {
-                    const uint16_t *at = sb + (32 * s + 8 * g + (r >> 2)) * kPitch + 32 * (m >> 1) + 8 * (r & 3) + 4 * (m & 1);
-                    const u32x4 bt = load_transposed(at, at + 4 * kPitch);
-#pragma unroll
-                    for (int part = SPLIT - 1; part >= 0; --part) {
-                        hs[m][0] = mfma(bt, xw[part][0], hs[m][0]);
-                        hs[m][1] = mfma(bt, xw[part][1], hs[m][1]);
-                    }
-                }
-            }
-
-            if (bad) {
-                for (int q = 0; q < kChunk; ++q)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const float v = bf16_bits_to_f32(sx[q * kXPitch + 8 * (r >> 2) + 4 * f + (r & 3)]);
-                        if (is_finite(v)) continue;
-                        const float w = ss[2 * kChunk + q] * v;
-#pragma unroll
-                        for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                hs[m][f][i] += w * bf16_bits_to_f32(sb[q * kPitch + 32 * (m >> 1) + 8 * g + 4 * (m & 1) + i]);
-                    }
-            }
-
-            // ---- skip, gate and store: eight consecutive p of a token a lane
-            if constexpr (OUT) {
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt) {
-                    const int row = 16 * tt + r, t = t0 + row, n = pcount - 8 * g;
-                    if (t >= seg.last || n <= 0) continue;
-                    const u32x4 xv = lds16(sx + row * kXPitch + 8 * g);
-                    const int64_t tok = seg.token0 + t;
-                    float o[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(skip, (i & 1) ? hi_f32(xv[i >> 1]) : lo_f32(xv[i >> 1]), y[tt][i >> 2][i & 3]);
-                    if (p.z != nullptr) {
-                        const u32x4 zv = load8<WIDE>(p.z + seg.seq * p.zs_n + tok * p.zs_t + head * p.zs_h + p0 + 8 * g, n);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] *= silu((i & 1) ? hi_f32(zv[i >> 1]) : lo_f32(zv[i >> 1]));
-                    }
-                    uint16_t *to = p.out + seg.seq * p.os_n + tok * p.os_t + head * p.os_h + p0 + 8 * g;
-                    const u32x4 ov = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
-                    if (WIDE) {
-                        *reinterpret_cast<u32x4 *>(to) = ov;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i < n) to[i] = (uint16_t)(ov[i >> 1] >> (16 * (i & 1)));
-                    }
-                }
+            for (int tt = 0; tt < 4; ++tt) {
+                const float e = ss[3 * kChunk + 16 * tt + r];
+                y[tt][0] *= e;
+                y[tt][1] *= e;
             }
             __syncthreads();
         }
 
-        // ---- the state behind the segment
-        const bool to_pool = OUT && p.state != nullptr && seg.index == seg.count - 1;
-        if (OUT && !to_pool) return;
+        u32x4 xf[2][2];  // x with tokens inside: [32-token half][tile]
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const uint16_t *at = sx + (32 * s + 8 * g + (r >> 2)) * kXPitch + 8 * (r & 3) + 4 * f;
+                xf[s][f] = load_transposed(at, at + 4 * kXPitch);
+            }
+        // An infinity or NaN of a later token must not meet the zeros of L: it is taken
+        // out of the matrix products and its terms are added one by one.
+        float probe = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) probe = sum_pair(xf[i >> 3][(i >> 2) & 1][i & 3], probe);
+        const bool bad = __any(!(__builtin_fabsf(probe) < kHuge));
+        if (bad) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) xf[i >> 3][(i >> 2) & 1][i & 3] = finite_pair(xf[i >> 3][(i >> 2) & 1][i & 3]);
+        }
+        if constexpr (OUT) {
+            // ---- (L o C B^T) X
+            const uint16_t *mp = sp + head_slot * kChunk * kPPitch;
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                for (int s = 0; s <= tt / 2; ++s) {
+                    const u32x4 pf = lds16(mp + (16 * tt + r) * kPPitch + 32 * s + 8 * g);
+                    y[tt][0] = mfma(xf[s][0], pf, y[tt][0]);
+                    y[tt][1] = mfma(xf[s][1], pf, y[tt][1]);
+                }
+            if (bad) {
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt)
+                    for (int q = 0; q <= 16 * tt + r; ++q)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float v = bf16_bits_to_f32(sx[q * kXPitch + 8 * g + i]);
+                            if (!is_finite(v))
+                                y[tt][i >> 2][i & 3] += bf16_bits_to_f32(mp[(16 * tt + r) * kPPitch + q]) * v;
+                        }
+            }
+        }
+
+        // ---- H' = e^{c_Q} H + (scaled x)^T B
+        const float dec = ss[3 * kChunk + kChunk - 1];
 #pragma unroll
         for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) hs[m][f] *= dec;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const float *w = ss + 2 * kChunk + 32 * s + 8 * g;
+            u32x4 xw[SPLIT][2];
 #pragma unroll
             for (int f = 0; f < 2; ++f)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int k = 16 * m + 4 * g + i, pc = 8 * (r >> 2) + 4 * f + (r & 3);
-                    if (k >= p.k || pc >= pcount) continue;
-                    const int64_t at = in_state + (int64_t)pc * p.k + k;
-                    if (!OUT)
-                        p.workspace[(u + 1) * hpk + at] = hs[m][f][i];
-                    else if (p.state_f32)
-                        static_cast<float *>(p.state)[slot * p.ss_s + at] = hs[m][f][i];
-                    else
-                        static_cast<uint16_t *>(p.state)[slot * p.ss_s + at] = f32_to_bf16_bits(hs[m][f][i]);
+                    float v0 = lo_f32(xf[s][f][i]) * w[2 * i], v1 = hi_f32(xf[s][f][i]) * w[2 * i + 1];
+#pragma unroll
+                    for (int part = 0; part < SPLIT; ++part) {
+                        const uint32_t h = pack_bf16x2(v0, v1);
+                        xw[part][f][i] = h;
+                        v0 -= lo_f32(h);
+                        v1 -= hi_f32(h);
+                    }
                 }
-        if (!OUT && valid && p0 == 0 && lane == 0)
-            p.workspace[plan.slots * hpk + (int64_t)(u + 1) * p.h + head] = __builtin_amdgcn_exp2f(decay_sum);
-    });
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m) {
+                const uint16_t *at = sb + (32 * s + 8 * g + (r >> 2)) * kPitch + 32 * (m >> 1) + 8 * (r & 3) + 4 * (m & 1);
+                const u32x4 bt = load_transposed(at, at + 4 * kPitch);
+#pragma unroll
+                for (int part = SPLIT - 1; part >= 0; --part) {
+                    hs[m][0] = mfma(bt, xw[part][0], hs[m][0]);
+                    hs[m][1] = mfma(bt, xw[part][1], hs[m][1]);
+                }
+            }
+        }
+        if (bad) {
+            for (int q = 0; q < kChunk; ++q)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const float v = bf16_bits_to_f32(sx[q * kXPitch + 8 * (r >> 2) + 4 * f + (r & 3)]);
+                    if (is_finite(v)) continue;
+                    const float w = ss[2 * kChunk + q] * v;
+#pragma unroll
+                    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            hs[m][f][i] += w * bf16_bits_to_f32(sb[q * kPitch + 32 * (m >> 1) + 8 * g + 4 * (m & 1) + i]);
+                }
+        }
+
+        // ---- skip, gate and store: eight consecutive p of a token a lane
+        if constexpr (OUT) {
+            ro.begin(rows);
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) {
+                const u32x4 xv = lds16(sx + (16 * tt + r) * kXPitch + 8 * g);
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = __builtin_fmaf(skip, (i & 1) ? hi_f32(xv[i >> 1]) : lo_f32(xv[i >> 1]), y[tt][i >> 2][i & 3]);
+                if (gated) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] *= silu((i & 1) ? hi_f32(zv[tt][i >> 1]) : lo_f32(zv[tt][i >> 1]));
+                }
+                ro.store(u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                               pack_bf16x2(o[6], o[7])},
+                         tt);
+            }
+            ro.advance();
+        }
+        __syncthreads();
+    }
+
+    // ---- the state behind the segment
+    const SelectiveScanParams &late = reread(p);
+    if (OUT && (late.state == nullptr || seg.index != seg.count - 1)) return;
+    const int64_t hpk = (int64_t)late.h * late.p * late.k;
+    void *to = OUT ? late.state : late.workspace;
+    const bool f32 = !OUT || late.state_f32, wide = OUT ? wide_state(late) : late.k % 4 == 0;
+    const int64_t at = (OUT ? slot * late.ss_s : (u + 1) * hpk) + in_state;
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const int pc = 8 * (r >> 2) + 4 * f + (r & 3), k = 16 * m + 4 * g;
+            if (pc < pcount) store_state4(to, f32, wide, at + (int64_t)pc * late.k + k, late.k - k, hs[m][f]);
+        }
+    if (!OUT && valid && leads && p0 == 0 && lane == 0)
+        late.workspace[plan.slots * hpk + (int64_t)(u + 1) * late.h + head] = __builtin_amdgcn_exp2f(decay_sum);
 }
 
 // The states ahead of every segment, in place: position u + 1 of the workspace
@@ -586,11 +696,13 @@ template <int KS, int SPLIT, bool OUT, bool WIDE>
 hipError_t launch_pass(const SelectiveScanParams &p, const ScanPlan &plan, hipStream_t stream) {
     const int64_t units = (int64_t)plan.slots * p.g * plan.quads;
     const size_t lds = (size_t)(OUT ? 2 : 1) * kChunk * (KS + 8) * 2 + (size_t)kScanWaves * kChunk * kXPitch * 2 +
-                       (size_t)kScanWaves * 4 * kChunk * 4 + (OUT ? (size_t)plan.heads * kChunk * kPPitch * 2 : 0);
+                       (size_t)kMaxHeads * 4 * kChunk * 4 + (OUT ? (size_t)plan.heads * kChunk * kPPitch * 2 : 0);
     auto kernel = selective_scan_kernel<KS, SPLIT, OUT, WIDE>;
     const hipError_t allowed = allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, SPLIT, OUT, WIDE>);
     if (allowed != hipSuccess) return allowed;
-    kernel<<<dim3((unsigned)(units < kMaxBlocks ? units : kMaxBlocks)), kScanBlock, lds, stream>>>(p, plan);
+    const int64_t across = units < kMaxBlocks ? units : kMaxBlocks, deep = (units + across - 1) / across;
+    if (deep > 65535) return hipErrorInvalidConfiguration;
+    kernel<<<dim3((unsigned)across, (unsigned)deep), kScanBlock, lds, stream>>>(p, plan);
     return hipGetLastError();
 }
 
@@ -615,9 +727,10 @@ hipError_t launch_ks(const SelectiveScanParams &p, const ScanPlan &plan, bool wi
     return exact ? launch_passes<KS, 3, false>(p, plan, stream) : launch_passes<KS, 1, false>(p, plan, stream);
 }
 
-// Whether rows at p with the given element strides start on 16 bytes.
+// Whether rows at p with the given element strides start on 16 bytes,
+// and 64 of them (b elements apart) span less than 2^31 bytes.
 bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0 && b < (1 << 23);
 }
 
 }  // namespace
