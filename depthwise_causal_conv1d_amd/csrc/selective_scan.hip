@@ -14,22 +14,26 @@
 // so a token and head cost about 64 (k + p) + 4 p k operations on the matrix cores
 // instead of 5 p k on the vector units, and x, z and out move once.
 //
-// A wave owns 32 of a head's p and all of the state's k: H stays in its FP32
+// A wave owns 16 of a head's p and all of the state's k: H stays in its FP32
 // accumulators for the whole sequence, already in the lane order that the next
-// product reads it in (below).  A block is four such waves of one group (two heads
-// at p = 64), which share the chunk's B and C in LDS and the products C B^T, each
-// wave computing a quarter of the lower triangle and scaling it for every head of
-// the block.
+// product reads it in (below).  A block is eight such waves of one group (two heads
+// at p = 64), which share the chunk's B and C in LDS and the products C B^T: the
+// lower triangle's ten tiles, scaled for each head of the block, are shared out.
+// (With 32 p a wave reads half as much LDS, but needs more than the 256 registers
+// that leave two waves a SIMD; 16 p need fewer than 128 and leave four.)
 //
 // Layouts.  v_mfma_f32_16x16x32_bf16 takes, in lane l with r = l & 15 and g = l >> 4,
 // row (column) r of an operand at inner indices 8 g .. 8 g + 7, and leaves column r,
-// rows 4 g .. 4 g + 3 of the result.  The inner index may be permuted if both operands
-// agree, and the order of rows is free: state columns are numbered so that the two
-// result tiles 2 m and 2 m + 1 of H, four values each, are the eight values of one
-// operand (LDS keeps B and C with each 32 state columns permuted that way), and the p
-// of a wave's two tiles interleave by four so that a lane ends with eight consecutive
-// p of a token: one 16-byte store.  B and x, needed with tokens as the inner index
-// too, are read from LDS through the transposing load.
+// rows 4 g .. 4 g + 3 of the result.  The order of an operand's rows is free, and so is
+// the inner indices' if both operands agree.  So the state columns of result tiles 2 m
+// and 2 m + 1 interleave by four (tile 2 m + f, row 4 g + i is column 32 m + 8 g + 4 f
+// + i): together the two tiles of H are an operand as they are, against C's rows read
+// 16 bytes at a time.  B and x, needed with tokens as the inner index too, are read
+// through the transposing load, four rows (tokens) at a time: there the inner order is
+// 4 g .. of the first and of the second 16 of 32 tokens, and L o C B^T is written in
+// that order.  LDS rows are 32 bytes longer than a multiple of 64: measured with
+// sixteen waves, 16-byte row reads then take 4.5 cycles (32 at a pitch of 256 bytes)
+// and transposing loads 4.2 (16).
 //
 // Precision: B, C and x are BF16 as given; sums, prefix sums, exponentials and H are
 // FP32.  The scaled products L o C B^T and the copy of H that C reads are rounded to
@@ -46,19 +50,19 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kChunk = 64;
-constexpr int kScanWaves = 4;
+constexpr int kScanWaves = 8;
 constexpr int kScanBlock = kWave * kScanWaves;
-constexpr int kUnitP = 32;               // p of a wave
-constexpr int kXPitch = kUnitP + 8;      // LDS row pitches, elements: rows start on
-constexpr int kPPitch = kChunk + 8;      // different banks, 16-byte aligned
-constexpr int kMaxHeads = 4;             // heads of a block (p <= 32)
+constexpr int kUnitP = 16;           // p of a wave
+constexpr int kPPitch = kChunk + 16;  // LDS row pitch of L o C B^T
+constexpr int kStepRows = 4;         // per token and head: c, d, the weight into H, e^c
 
 // How a call is cut up; the same on the host and in every kernel.
 struct ScanPlan {
     int32_t seg;     // tokens of a segment (a multiple of kChunk)
     int32_t nseg;    // segments of a sequence (batch form)
     int32_t slots;   // segments in all; packed: an upper bound, some empty
-    int32_t np;      // waves a head takes: ceil(p / 32)
+    int32_t np;      // waves a head takes: ceil(p / 16)
+    int32_t waves;   // of a block that own p
     int32_t quads;   // blocks a group takes
     int32_t heads;   // most heads of one block
     bool split;      // some sequence may have more than one segment
@@ -69,25 +73,16 @@ __device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
                                                    0, 0, 0);
 }
 
-// Eight values of one column, from two 4-row pieces of LDS: lane 4 q + j of a
-// 16-lane row gives the address of row q, columns 4 j .. 4 j + 3, and gets
-// rows 0 .. 3 of column 4 q + j.
-__device__ __forceinline__ u32x4 load_transposed(const uint16_t *lo, const uint16_t *hi) {
-    typedef __attribute__((address_space(3))) s16x4_t *Lds;
-    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4_t *)lo));
-    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4_t *)hi));
-    return u32x4{a[0], a[1], b[0], b[1]};
-}
-
 __device__ __forceinline__ u32x4 lds16(const uint16_t *p) { return *reinterpret_cast<const u32x4 *>(p); }
 
-// Up to eight consecutive BF16 values at s, of which `count` exist: zeros behind.
-__device__ __forceinline__ u32x4 load8(const uint16_t *s, int count) {
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < count) v[i >> 1] |= (uint32_t)s[i] << (16 * (i & 1));
-    return v;
+// An operand whose inner index runs over rows in LDS: lane 4 q + j of the 16 that
+// share g gives the address of its columns' piece j (four of them) in row 4 g + q, and
+// gets column 4 q + j of rows 4 g .. 4 g + 3, and of the 16 rows further down.
+__device__ __forceinline__ u32x4 load_columns(const uint16_t *at, int pitch) {
+    typedef __attribute__((address_space(3))) s16x4_t *Lds;
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4_t *)at));
+    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(s16x4_t *)(at + 16 * pitch)));
+    return u32x4{a[0], a[1], b[0], b[1]};
 }
 
 constexpr float kHuge = 3.0e38f;
@@ -183,46 +178,66 @@ __device__ __forceinline__ void wave_sums(float v, int lane, float *upto, float 
 
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer
 
-// One operand's rows of a chunk, `stride` elements apart: a lane moves eight values
-// from column `col` (of which `count` exist) of rows row0, row0 + step, ...  WIDE moves
-// 16 bytes through a buffer that ends with the chunk's last row, so that what lies
+// One operand's rows of a chunk, `stride` elements apart: a lane moves a few values
+// from column `col` on (there are `width`) of rows row0, row0 + step, ...  WIDE moves
+// them at once through a buffer that ends with the chunk's last row, so that what lies
 // behind it reads as zeros and is not written.
 template <bool WIDE>
 struct ChunkRows {
     const uint16_t *base;  // wave-uniform: the chunk's first row
     int64_t stride;
-    int32_t row0, col, count, step, rows;
-    uint32_t at0, hop, width;
+    int32_t step, width, row0, col, rows;
+    uint32_t at0, hop;
     Buffer buf;
-    __device__ __forceinline__ ChunkRows(const uint16_t *first, int64_t stride, int row0, int step, int col, int width)
-        : base(first), stride(stride), row0(row0), col(col), count(width - col), step(step), width(2u * (uint32_t)width) {
-        const uint32_t bytes = 2u * (uint32_t)stride;
-        at0 = count > 0 ? (uint32_t)row0 * bytes + 2u * (uint32_t)col : kNowhere;
-        hop = (uint32_t)step * bytes;
-    }
-    __device__ __forceinline__ void begin(int n) {
+    __device__ __forceinline__ ChunkRows(const uint16_t *first, int64_t stride, int step, int width)
+        : base(first), stride(stride), step(step), width(width) {}
+    __device__ __forceinline__ void begin(int n, int row, int column) {
         rows = n;
-        if (WIDE) buf = make_buffer(base, n > 0 ? (uint32_t)(n - 1) * 2u * (uint32_t)stride + width : 0u);
+        row0 = row;
+        col = column;
+        const uint32_t bytes = 2u * (uint32_t)stride;
+        if (WIDE) {
+            buf = make_buffer(base, n > 0 ? (uint32_t)(n - 1) * bytes + 2u * (uint32_t)width : 0u);
+            at0 = col < width ? (uint32_t)row0 * bytes + 2u * (uint32_t)col : kNowhere;
+            hop = (uint32_t)step * bytes;
+        }
     }
     __device__ __forceinline__ void advance() { base += kChunk * stride; }
-    __device__ __forceinline__ u32x4 load(int q) const {
-        if (WIDE) return buffer_load<kCached>(buf, at0 + (uint32_t)q * hop);
-        const int row = row0 + q * step;
-        return load8(base + row * stride + col, row < rows ? count : 0);
-    }
-    __device__ __forceinline__ void store(u32x4 v, int q) const {
+    // N values (8 or 4) of row row0 + q * step
+    template <int N>
+    __device__ __forceinline__ void load(uint32_t (&w)[N / 2], int q) const {
         if (WIDE) {
-            buffer_store<kCached>(v, buf, at0 + (uint32_t)q * hop);
+            buffer_load_words<N / 2, kCached>(buf, at0 + (uint32_t)q * hop, w);
+            return;
+        }
+        const int row = row0 + q * step;
+        const uint16_t *from = base + row * stride + col;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (row < rows && col + i < width) w[i >> 1] |= (uint32_t)from[i] << (16 * (i & 1));
+    }
+    __device__ __forceinline__ void store(uint32_t (&w)[2], int q) const {
+        if (WIDE) {
+            buffer_store_words<2, kCached>(w, buf, at0 + (uint32_t)q * hop);
             return;
         }
         const int row = row0 + q * step;
         if (row >= rows) return;
         uint16_t *to = const_cast<uint16_t *>(base) + row * stride + col;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < count) to[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+        for (int i = 0; i < 4; ++i)
+            if (col + i < width) to[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
     }
 };
+
+// v, not known to be the same as anywhere else: addresses formed from it are formed
+// where they are used, instead of being kept in registers from outside of a loop.
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
 // The kernel's arguments, read again: what is used only once a loop is done need not
 // occupy scalar registers throughout it.
@@ -267,6 +282,9 @@ __device__ __forceinline__ void store_state4(void *s, bool f32, bool wide, int64
         }
 }
 
+// The state column of row 4 g of H's tile m.
+__device__ __forceinline__ int column(int m, int g) { return 32 * (m >> 1) + 8 * g + 4 * (m & 1); }
+
 // Whether the pool's rows of four state values start on whole 8 or 16 bytes.
 __device__ __forceinline__ bool wide_state(const SelectiveScanParams &p) {
     return p.k % 4 == 0 && p.ss_s % 4 == 0 && reinterpret_cast<uintptr_t>(p.state) % 16 == 0;
@@ -275,21 +293,21 @@ __device__ __forceinline__ bool wide_state(const SelectiveScanParams &p) {
 // OUT: the outputs and final states.  Otherwise the state that each segment but a
 // sequence's last builds up from zero, and its decay, for the join.
 template <int KS, int SPLIT, bool OUT, bool WIDE>
-__global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_kernel(const SelectiveScanParams p,
+__global__ __launch_bounds__(kScanBlock, KS <= 128 ? 4 : 2) void selective_scan_kernel(const SelectiveScanParams p,
                                                                                       const ScanPlan plan) {
-    constexpr int kPitch = KS + 8;
+    constexpr int kPitch = KS + 16;
     constexpr int kTiles = KS / 16;
-    constexpr int kPieces = KS / 32;  // 16-byte pieces of B (of C) a thread stages
+    constexpr int kPieces = KS / 64;  // 16-byte pieces of B (of C) a thread stages
     extern __shared__ u32x4 smem[];
     uint16_t *sb = reinterpret_cast<uint16_t *>(smem);
     uint16_t *sc = sb + kChunk * kPitch;
     uint16_t *sx_all = sc + (OUT ? kChunk * kPitch : 0);
-    float *ss_all = reinterpret_cast<float *>(sx_all + kScanWaves * kChunk * kXPitch);
-    uint16_t *sp = reinterpret_cast<uint16_t *>(ss_all + kMaxHeads * 4 * kChunk);
+    float *steps = reinterpret_cast<float *>(sx_all + kScanWaves * kChunk * kUnitP);  // [2][heads][kStepRows][64]
+    uint16_t *sp = reinterpret_cast<uint16_t *>(steps + 2 * plan.heads * kStepRows * kChunk);
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    uint16_t *sx = sx_all + wave * kChunk * kXPitch;
+    uint16_t *sx = sx_all + wave * kChunk * kUnitP;
     const int per_group = p.h / p.g, units = per_group * plan.np;
 
     if (OUT && blockIdx.x == 0 && blockIdx.y == 0) check_table(p);
@@ -297,7 +315,7 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_
     if (OUT)
         for (int i = tid; i < plan.heads * 2 * 16 * 16; i += kScanBlock) {
             const int head = i >> 9, tile = (i >> 8) & 1, row = (i >> 4) & 15, col = i & 15;
-            sp[(head * kChunk + 32 * tile + row) * kPPitch + 32 * tile + 16 + col] = 0;
+            sp[(head * kChunk + 32 * tile + row) * kPPitch + 32 * tile + 8 * (col >> 2) + 4 + (col & 3)] = 0;
         }
 
     const int64_t unit = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
@@ -308,18 +326,15 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_
     const Segment seg = find_segment(p, plan, u);
     if (!seg.ok || (!OUT && seg.index == seg.count - 1)) return;
 
-    const int un = quad * kScanWaves + wave;
-    const bool valid = un < units;
-    const int mine = min(un, units - 1);
-    const int first_head = quad * kScanWaves / plan.np;
-    const int heads = min(quad * kScanWaves + kScanWaves - 1, units - 1) / plan.np - first_head + 1;
+    const int last_unit = min(quad * plan.waves + plan.waves, units) - 1;
+    const int mine = min(quad * plan.waves + wave, last_unit);
+    const bool valid = quad * plan.waves + wave == mine;
+    const int first_head = quad * plan.waves / plan.np;
+    const int heads = last_unit / plan.np - first_head + 1;
     const int head_slot = mine / plan.np - first_head;
     const int head = group * per_group + mine / plan.np;
     const int p0 = (mine % plan.np) * kUnitP;
     const int pcount = valid ? min(kUnitP, p.p - p0) : 0;
-    // the first of the block's waves that have this head computes its steps for all
-    const bool leads = un == max(mine / plan.np * plan.np, quad * kScanWaves);
-    float *ss = ss_all + head_slot * 4 * kChunk;  // c, d, the weight into H, e^c; 64 tokens each
 
     const int slot = route_row(p.idx, p.status, p.n, p.s, seg.seq, lane);
     if (slot < 0) {  // a padding sequence: zeros, and no state moves
@@ -330,114 +345,122 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_
         return;
     }
 
-    // ---- the state ahead of the segment: tile m of p tile f, rows k = 16 m + 4 g + i, column p
-    f32x4_t hs[kTiles][2];
+    // ---- the state ahead of the segment: tile m, rows k = column(m, g) + i, column p = r
+    f32x4_t hs[kTiles];
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) hs[m][0] = hs[m][1] = f32x4_t{0, 0, 0, 0};
-    const int64_t in_state = ((int64_t)head * p.p + p0) * p.k;
+    for (int m = 0; m < kTiles; ++m) hs[m] = f32x4_t{0, 0, 0, 0};
     const bool from_ws = seg.count > 1;
     if (OUT && (from_ws || (p.state != nullptr && p.has_init != nullptr && p.has_init[seg.seq] != 0))) {
         const void *src = from_ws ? p.workspace + u * (int64_t)p.h * p.p * p.k : p.state;
         const bool f32 = from_ws || p.state_f32, wide = from_ws ? p.k % 4 == 0 : wide_state(p);
-        const int64_t at = (from_ws ? 0 : slot * p.ss_s) + in_state;
+        const int64_t at = (from_ws ? 0 : slot * p.ss_s) + ((int64_t)head * p.p + p0 + r) * p.k;
+        if (r < pcount)
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const int pc = 8 * (r >> 2) + 4 * f + (r & 3), k = 16 * m + 4 * g;
-                if (pc < pcount) hs[m][f] = load_state4(src, f32, wide, at + (int64_t)pc * p.k + k, p.k - k);
-            }
+            for (int m = 0; m < kTiles; ++m)
+                hs[m] = load_state4(src, f32, wide, at + column(m, g), p.k - column(m, g));
     }
 
     // ---- the operands' rows: B and C shared out over the block, the rest a wave's own
     const int64_t tok = seg.token0 + seg.first;
-    constexpr int kRowsPerPiece = kScanBlock * 8 / KS;
-    const int brow = tid / (KS / 8), bcol = tid % (KS / 8) * 8;
-    ChunkRows<WIDE> rb(p.b + seg.seq * p.bs_n + tok * p.bs_t + group * p.bs_g, p.bs_t, brow, kRowsPerPiece, bcol, p.k);
-    ChunkRows<WIDE> rc(p.c + seg.seq * p.cs_n + tok * p.cs_t + group * p.cs_g, p.cs_t, brow, kRowsPerPiece, bcol, p.k);
-    ChunkRows<WIDE> rx(p.x + seg.seq * p.xs_n + tok * p.xs_t + head * p.xs_h + p0, p.xs_t, lane >> 2, 16, (lane & 3) * 8, pcount);
-    ChunkRows<WIDE> rz(p.z + seg.seq * p.zs_n + tok * p.zs_t + head * p.zs_h + p0, p.zs_t, r, 16, 8 * g, pcount);
-    ChunkRows<WIDE> ro(p.out + seg.seq * p.os_n + tok * p.os_t + head * p.os_h + p0, p.os_t, r, 16, 8 * g, pcount);
-    int64_t dt_at = seg.seq * p.ds_n + (tok + lane) * p.ds_t + head;
-    const float a2 = p.a[head] * kLog2e;
-    const float dt_bias = p.dt_bias != nullptr ? p.dt_bias[head] : 0.0f;
+    constexpr int kRowsPerPiece = kScanBlock * 8 / KS, kAcross = KS / 8;
+    ChunkRows<WIDE> rb(p.b + seg.seq * p.bs_n + tok * p.bs_t + group * p.bs_g, p.bs_t, kRowsPerPiece, p.k);
+    ChunkRows<WIDE> rc(p.c + seg.seq * p.cs_n + tok * p.cs_t + group * p.cs_g, p.cs_t, kRowsPerPiece, p.k);
+    ChunkRows<WIDE> rx(p.x + seg.seq * p.xs_n + tok * p.xs_t + head * p.xs_h + p0, p.xs_t, 32, pcount);
+    ChunkRows<WIDE> rz(p.z + seg.seq * p.zs_n + tok * p.zs_t + head * p.zs_h + p0, p.zs_t, 16, pcount);
+    ChunkRows<WIDE> ro(p.out + seg.seq * p.os_n + tok * p.os_t + head * p.os_h + p0, p.os_t, 16, pcount);
     const float skip = OUT && p.d_skip != nullptr ? p.d_skip[head] : 0.0f;
     const bool gated = p.z != nullptr;
+
+    // ---- the steps of a head's chunk, one chunk ahead: the last waves (which have the
+    // fewest tiles of C B^T) take a head each
+    const int job = kScanWaves - 1 - wave;
+    const bool has_job = job < heads;
+    const int job_head = group * per_group + first_head + min(job, heads - 1);
+    const float a2 = p.a[job_head] * kLog2e;
+    const float dt_bias = p.dt_bias != nullptr ? p.dt_bias[job_head] : 0.0f;
+    int64_t dt_at = seg.seq * p.ds_n + tok * p.ds_t + job_head;
     float decay_sum = 0.0f;
+    auto fetch_step = [&](int left) {
+        float v = 0.0f;
+        const int l = here(lane);
+        if (has_job && l < left)
+            v = p.dt_f32 ? static_cast<const float *>(p.dt)[dt_at + l * p.ds_t]
+                         : bf16_bits_to_f32(static_cast<const uint16_t *>(p.dt)[dt_at + l * p.ds_t]);
+        dt_at += kChunk * p.ds_t;
+        return v;
+    };
+    auto put_steps = [&](float v, int left, int parity) {
+        float d = v + dt_bias;
+        if (p.dt_softplus) d = softplus(d);
+        if (lane >= left) d = 0.0f;
+        float upto, behind, total;
+        wave_sums(d * a2, lane, &upto, &behind, &total);
+        float *to = steps + ((parity * plan.heads + job) * kStepRows) * kChunk + lane;
+        to[0] = upto;
+        to[kChunk] = d;
+        to[2 * kChunk] = d * __builtin_amdgcn_exp2f(behind);
+        to[3 * kChunk] = __builtin_amdgcn_exp2f(upto);
+        decay_sum += total;
+    };
 
     // ---- a chunk on its way from memory
-    u32x4 nb[kPieces], nc[kPieces], nx[4];
-    float nd = 0.0f;
+    uint32_t nb[kPieces][4], nc[kPieces][4], nx[2][4];
     auto fetch = [&](int left) {
-        const int n = min(left, kChunk);
-        rb.begin(n);
+        const int n = min(left, kChunk), i = here(tid), l = i & 63;
+        rb.begin(n, i / kAcross, i % kAcross * 8);
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) nb[q] = rb.load(q);
+        for (int q = 0; q < kPieces; ++q) rb.template load<8>(nb[q], q);
         if (OUT) {
-            rc.begin(n);
+            rc.begin(n, i / kAcross, i % kAcross * 8);
 #pragma unroll
-            for (int q = 0; q < kPieces; ++q) nc[q] = rc.load(q);
+            for (int q = 0; q < kPieces; ++q) rc.template load<8>(nc[q], q);
         }
-        rx.begin(n);
+        rx.begin(n, l >> 1, (l & 1) * 8);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) nx[q] = rx.load(q);
-        if (leads && lane < n)
-            nd = p.dt_f32 ? static_cast<const float *>(p.dt)[dt_at]
-                          : bf16_bits_to_f32(static_cast<const uint16_t *>(p.dt)[dt_at]);
+        for (int q = 0; q < 2; ++q) rx.template load<8>(nx[q], q);
         rb.advance();
         rc.advance();
         rx.advance();
-        dt_at += kChunk * p.ds_t;
     };
 
-    fetch(seg.last - seg.first);
-    for (int t0 = seg.first; t0 < seg.last; t0 += kChunk) {
-        const int rows = min(seg.last - t0, kChunk);
-        // ---- the chunk into LDS.  A 16-byte piece of B or C is two runs of four state
-        // columns of its 32: column 16 m + 4 q + i goes to 8 q + 4 m + i.
+    const int length = seg.last - seg.first;
+    float step0 = fetch_step(length), step1 = fetch_step(length - kChunk);
+    fetch(length);
+    if (has_job) put_steps(step0, length, 0);
+    for (int left = length, parity = 0; left > 0; left -= kChunk, parity ^= 1) {
+        const int rows = min(left, kChunk);
+        const float *ss = steps + ((parity * plan.heads + head_slot) * kStepRows) * kChunk;
+        // ---- the chunk into LDS
 #pragma unroll
         for (int q = 0; q < kPieces; ++q) {
-            const int to = (q * kRowsPerPiece + brow) * kPitch + (bcol & ~31) + ((bcol & 8) << 1) +
-                           ((bcol & 16) >> 2);
-            *reinterpret_cast<u32x2 *>(sb + to) = u32x2{nb[q][0], nb[q][1]};
-            *reinterpret_cast<u32x2 *>(sb + to + 8) = u32x2{nb[q][2], nb[q][3]};
-            if (OUT) {
-                *reinterpret_cast<u32x2 *>(sc + to) = u32x2{nc[q][0], nc[q][1]};
-                *reinterpret_cast<u32x2 *>(sc + to + 8) = u32x2{nc[q][2], nc[q][3]};
-            }
+            const int to = (q * kRowsPerPiece + tid / kAcross) * kPitch + tid % kAcross * 8;
+            *reinterpret_cast<u32x4 *>(sb + to) = u32x4{nb[q][0], nb[q][1], nb[q][2], nb[q][3]};
+            if (OUT) *reinterpret_cast<u32x4 *>(sc + to) = u32x4{nc[q][0], nc[q][1], nc[q][2], nc[q][3]};
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<u32x4 *>(sx + (q * 16 + (lane >> 2)) * kXPitch + (lane & 3) * 8) = nx[q];
-        if (leads) {
-            float d = nd + dt_bias;
-            if (p.dt_softplus) d = softplus(d);
-            if (lane >= rows) d = 0.0f;
-            float upto, behind, total;
-            wave_sums(d * a2, lane, &upto, &behind, &total);
-            ss[lane] = upto;
-            ss[kChunk + lane] = d;
-            ss[2 * kChunk + lane] = d * __builtin_amdgcn_exp2f(behind);
-            ss[3 * kChunk + lane] = __builtin_amdgcn_exp2f(upto);
-            decay_sum += total;
-        }
+        for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<u32x4 *>(sx + (q * 32 + (lane >> 1)) * kUnitP + (lane & 1) * 8) =
+                u32x4{nx[q][0], nx[q][1], nx[q][2], nx[q][3]};
         __syncthreads();
-        u32x4 zv[4];
+        if (left > kChunk && has_job) put_steps(step1, left - kChunk, parity ^ 1);
+        uint32_t zv[4][2];
         if (OUT && gated) {
-            rz.begin(rows);
+            const int l = here(lane);
+            rz.begin(rows, l & 15, l >> 4 << 2);
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) zv[tt] = rz.load(tt);
+            for (int tt = 0; tt < 4; ++tt) rz.template load<4>(zv[tt], tt);
             rz.advance();
         }
-        if (t0 + kChunk < seg.last) fetch(seg.last - t0 - kChunk);
+        if (left > kChunk) {
+            step1 = fetch_step(left - 2 * kChunk);
+            fetch(left - kChunk);
+        }
 
-        f32x4_t y[4][2];
+        f32x4_t y[4];
         if constexpr (OUT) {
-            // ---- C B^T of this wave's tiles, scaled for each head of the block
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                const int e = q * kScanWaves + wave;  // tile (tt, ut) of the lower triangle, row by row
-                if (e >= 10) continue;
+            // ---- C B^T, a tile for a head at a time
+            for (int it = wave; it < 10 * heads; it += kScanWaves) {
+                const int hd = it / 10, e = it - 10 * hd;  // tile (tt, ut) of the lower triangle, row by row
                 const int tt = e >= 6 ? 3 : e >= 3 ? 2 : e >= 1 ? 1 : 0, ut = e - tt * (tt + 1) / 2;
                 f32x4_t acc = {0, 0, 0, 0};
 #pragma unroll
@@ -445,64 +468,47 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_
                     acc = mfma(lds16(sb + (16 * ut + r) * kPitch + 32 * m + 8 * g),
                                lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g), acc);
                 const int t = 16 * tt + r, u0 = 16 * ut + 4 * g;
-                for (int hd = 0; hd < heads; ++hd) {
-                    const float *hs4 = ss_all + hd * 4 * kChunk;
-                    const f32x4_t cu = *reinterpret_cast<const f32x4_t *>(hs4 + u0);
-                    const f32x4_t du = *reinterpret_cast<const f32x4_t *>(hs4 + kChunk + u0);
-                    const float ct = hs4[t];
-                    float v[4];
+                const float *sh = steps + ((parity * plan.heads + hd) * kStepRows) * kChunk;
+                const f32x4_t cu = *reinterpret_cast<const f32x4_t *>(sh + u0);
+                const f32x4_t du = *reinterpret_cast<const f32x4_t *>(sh + kChunk + u0);
+                const float ct = sh[t];
+                float v[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = u0 + i <= t ? acc[i] * __builtin_amdgcn_exp2f(ct - cu[i]) * du[i] : 0.0f;
-                    *reinterpret_cast<u32x2 *>(sp + (hd * kChunk + t) * kPPitch + u0) =
-                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                }
+                for (int i = 0; i < 4; ++i)
+                    v[i] = u0 + i <= t ? acc[i] * __builtin_amdgcn_exp2f(ct - cu[i]) * du[i] : 0.0f;
+                *reinterpret_cast<u32x2 *>(sp + (hd * kChunk + t) * kPPitch + 32 * (ut >> 1) + 8 * g + 4 * (ut & 1)) =
+                    u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
             }
             // ---- e^c C H^T
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) y[tt][0] = y[tt][1] = f32x4_t{0, 0, 0, 0};
+            for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int m = 0; m < KS / 32; ++m) {
-                u32x4 hb[2];
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const f32x4_t h0 = hs[2 * m][f], h1 = hs[2 * m + 1][f];
-                    hb[f] = u32x4{pack_bf16x2(h0[0], h0[1]), pack_bf16x2(h0[2], h0[3]), pack_bf16x2(h1[0], h1[1]),
+                const f32x4_t h0 = hs[2 * m], h1 = hs[2 * m + 1];
+                const u32x4 hb = {pack_bf16x2(h0[0], h0[1]), pack_bf16x2(h0[2], h0[3]), pack_bf16x2(h1[0], h1[1]),
                                   pack_bf16x2(h1[2], h1[3])};
-                }
 #pragma unroll
-                for (int tt = 0; tt < 4; ++tt) {
-                    const u32x4 cf = lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g);
-                    y[tt][0] = mfma(hb[0], cf, y[tt][0]);
-                    y[tt][1] = mfma(hb[1], cf, y[tt][1]);
-                }
+                for (int tt = 0; tt < 4; ++tt)
+                    y[tt] = mfma(hb, lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g), y[tt]);
             }
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                const float e = ss[3 * kChunk + 16 * tt + r];
-                y[tt][0] *= e;
-                y[tt][1] *= e;
-            }
+            for (int tt = 0; tt < 4; ++tt) y[tt] *= ss[3 * kChunk + 16 * tt + r];
             __syncthreads();
         }
 
-        u32x4 xf[2][2];  // x with tokens inside: [32-token half][tile]
+        u32x4 xf[2];  // x with tokens inside, 32 at a time
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const uint16_t *at = sx + (32 * s + 8 * g + (r >> 2)) * kXPitch + 8 * (r & 3) + 4 * f;
-                xf[s][f] = load_transposed(at, at + 4 * kXPitch);
-            }
+            xf[s] = load_columns(sx + (32 * s + 4 * g + (r >> 2)) * kUnitP + 4 * (r & 3), kUnitP);
         // An infinity or NaN of a later token must not meet the zeros of L: it is taken
         // out of the matrix products and its terms are added one by one.
         float probe = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) probe = sum_pair(xf[i >> 3][(i >> 2) & 1][i & 3], probe);
+        for (int i = 0; i < 8; ++i) probe = sum_pair(xf[i >> 2][i & 3], probe);
         const bool bad = __any(!(__builtin_fabsf(probe) < kHuge));
         if (bad) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) xf[i >> 3][(i >> 2) & 1][i & 3] = finite_pair(xf[i >> 3][(i >> 2) & 1][i & 3]);
+            for (int i = 0; i < 8; ++i) xf[i >> 2][i & 3] = finite_pair(xf[i >> 2][i & 3]);
         }
         if constexpr (OUT) {
             // ---- (L o C B^T) X
@@ -510,20 +516,18 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-                for (int s = 0; s <= tt / 2; ++s) {
-                    const u32x4 pf = lds16(mp + (16 * tt + r) * kPPitch + 32 * s + 8 * g);
-                    y[tt][0] = mfma(xf[s][0], pf, y[tt][0]);
-                    y[tt][1] = mfma(xf[s][1], pf, y[tt][1]);
-                }
+                for (int s = 0; s <= tt / 2; ++s)
+                    y[tt] = mfma(xf[s], lds16(mp + (16 * tt + r) * kPPitch + 32 * s + 8 * g), y[tt]);
             if (bad) {
+                const int rr = here(r), gg = here(g);
 #pragma unroll
                 for (int tt = 0; tt < 4; ++tt)
-                    for (int q = 0; q <= 16 * tt + r; ++q)
+                    for (int q = 0; q <= 16 * tt + rr; ++q)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float v = bf16_bits_to_f32(sx[q * kXPitch + 8 * g + i]);
+                        for (int i = 0; i < 4; ++i) {
+                            const float v = bf16_bits_to_f32(sx[q * kUnitP + 4 * gg + i]);
                             if (!is_finite(v))
-                                y[tt][i >> 2][i & 3] += bf16_bits_to_f32(mp[(16 * tt + r) * kPPitch + q]) * v;
+                                y[tt][i] += bf16_bits_to_f32(mp[(16 * tt + rr) * kPPitch + (q & 32) + 2 * (q & 12) + ((q & 16) >> 2) + (q & 3)]) * v;
                         }
             }
         }
@@ -531,69 +535,61 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_
         // ---- H' = e^{c_Q} H + (scaled x)^T B
         const float dec = ss[3 * kChunk + kChunk - 1];
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) hs[m][f] *= dec;
+        for (int m = 0; m < kTiles; ++m) hs[m] *= dec;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const float *w = ss + 2 * kChunk + 32 * s + 8 * g;
-            u32x4 xw[SPLIT][2];
+            const f32x4_t w0 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 32 * s + 4 * g);
+            const f32x4_t w1 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 32 * s + 16 + 4 * g);
+            u32x4 xw[SPLIT];
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
+            for (int i = 0; i < 4; ++i) {
+                float v0 = lo_f32(xf[s][i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
+                float v1 = hi_f32(xf[s][i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v0 = lo_f32(xf[s][f][i]) * w[2 * i], v1 = hi_f32(xf[s][f][i]) * w[2 * i + 1];
-#pragma unroll
-                    for (int part = 0; part < SPLIT; ++part) {
-                        const uint32_t h = pack_bf16x2(v0, v1);
-                        xw[part][f][i] = h;
-                        v0 -= lo_f32(h);
-                        v1 -= hi_f32(h);
-                    }
+                for (int part = 0; part < SPLIT; ++part) {
+                    const uint32_t h = pack_bf16x2(v0, v1);
+                    xw[part][i] = h;
+                    v0 -= lo_f32(h);
+                    v1 -= hi_f32(h);
                 }
+            }
 #pragma unroll
             for (int m = 0; m < kTiles; ++m) {
-                const uint16_t *at = sb + (32 * s + 8 * g + (r >> 2)) * kPitch + 32 * (m >> 1) + 8 * (r & 3) + 4 * (m & 1);
-                const u32x4 bt = load_transposed(at, at + 4 * kPitch);
+                const u32x4 bt = load_columns(sb + (32 * s + 4 * g + (r >> 2)) * kPitch + 32 * (m >> 1) + 8 * (r & 3) + 4 * (m & 1), kPitch);
 #pragma unroll
-                for (int part = SPLIT - 1; part >= 0; --part) {
-                    hs[m][0] = mfma(bt, xw[part][0], hs[m][0]);
-                    hs[m][1] = mfma(bt, xw[part][1], hs[m][1]);
-                }
+                for (int part = SPLIT - 1; part >= 0; --part) hs[m] = mfma(bt, xw[part], hs[m]);
             }
         }
         if (bad) {
-            for (int q = 0; q < kChunk; ++q)
+            const int rr = here(r), gg = here(g);
+            for (int q = 0; q < kChunk; ++q) {
+                const float v = bf16_bits_to_f32(sx[q * kUnitP + rr]);
+                if (is_finite(v)) continue;
+                const float w = ss[2 * kChunk + q] * v;
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const float v = bf16_bits_to_f32(sx[q * kXPitch + 8 * (r >> 2) + 4 * f + (r & 3)]);
-                    if (is_finite(v)) continue;
-                    const float w = ss[2 * kChunk + q] * v;
+                for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-                    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            hs[m][f][i] += w * bf16_bits_to_f32(sb[q * kPitch + 32 * (m >> 1) + 8 * g + 4 * (m & 1) + i]);
-                }
+                    for (int i = 0; i < 4; ++i) hs[m][i] += w * bf16_bits_to_f32(sb[q * kPitch + column(m, gg) + i]);
+            }
         }
 
-        // ---- skip, gate and store: eight consecutive p of a token a lane
+        // ---- skip, gate and store: four consecutive p of a token a lane
         if constexpr (OUT) {
-            ro.begin(rows);
+            const int l = here(lane);
+            ro.begin(rows, l & 15, l >> 4 << 2);
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt) {
-                const u32x4 xv = lds16(sx + (16 * tt + r) * kXPitch + 8 * g);
-                float o[8];
+                const u32x2 xv = *reinterpret_cast<const u32x2 *>(sx + (16 * tt + r) * kUnitP + 4 * g);
+                float o[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    o[i] = __builtin_fmaf(skip, (i & 1) ? hi_f32(xv[i >> 1]) : lo_f32(xv[i >> 1]), y[tt][i >> 2][i & 3]);
+                for (int i = 0; i < 4; ++i)
+                    o[i] = __builtin_fmaf(skip, (i & 1) ? hi_f32(xv[i >> 1]) : lo_f32(xv[i >> 1]), y[tt][i]);
                 if (gated) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] *= silu((i & 1) ? hi_f32(zv[tt][i >> 1]) : lo_f32(zv[tt][i >> 1]));
+                    for (int i = 0; i < 4; ++i) o[i] *= silu((i & 1) ? hi_f32(zv[tt][i >> 1]) : lo_f32(zv[tt][i >> 1]));
                 }
-                ro.store(u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                               pack_bf16x2(o[6], o[7])},
-                         tt);
+                uint32_t ov[2] = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+                ro.store(ov, tt);
             }
             ro.advance();
         }
@@ -606,16 +602,14 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 2 : 1) void selective_scan_
     const int64_t hpk = (int64_t)late.h * late.p * late.k;
     void *to = OUT ? late.state : late.workspace;
     const bool f32 = !OUT || late.state_f32, wide = OUT ? wide_state(late) : late.k % 4 == 0;
-    const int64_t at = (OUT ? slot * late.ss_s : (u + 1) * hpk) + in_state;
+    const int64_t at = (OUT ? slot * late.ss_s : (u + 1) * hpk) + ((int64_t)head * late.p + p0 + here(r)) * late.k;
+    const int gg = here(g);
+    if (r < pcount)
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            const int pc = 8 * (r >> 2) + 4 * f + (r & 3), k = 16 * m + 4 * g;
-            if (pc < pcount) store_state4(to, f32, wide, at + (int64_t)pc * late.k + k, late.k - k, hs[m][f]);
-        }
-    if (!OUT && valid && leads && p0 == 0 && lane == 0)
-        late.workspace[plan.slots * hpk + (int64_t)(u + 1) * late.h + head] = __builtin_amdgcn_exp2f(decay_sum);
+        for (int m = 0; m < kTiles; ++m)
+            store_state4(to, f32, wide, at + column(m, gg), late.k - column(m, gg), hs[m]);
+    if (!OUT && has_job && lane == 0)
+        late.workspace[plan.slots * hpk + (int64_t)(u + 1) * late.h + job_head] = __builtin_amdgcn_exp2f(decay_sum);
 }
 
 // The states ahead of every segment, in place: position u + 1 of the workspace
@@ -657,11 +651,14 @@ __global__ __launch_bounds__(256) void selective_join_kernel(const SelectiveScan
 constexpr int64_t kFullGrid = 512;
 constexpr int64_t kMinSegment = 256;
 
-ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, bool packed) {
+ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k, bool packed) {
     ScanPlan plan;
     plan.np = (int32_t)((p + kUnitP - 1) / kUnitP);
-    plan.quads = (int32_t)((h / g * plan.np + kScanWaves - 1) / kScanWaves);
-    plan.heads = plan.np == 1 ? kMaxHeads : 2;
+    // (eight heads and the widest state would not fit LDS)
+    plan.waves = plan.np == 1 && k > 128 ? kScanWaves / 2 : kScanWaves;
+    plan.quads = (int32_t)((h / g * plan.np + plan.waves - 1) / plan.waves);
+    // heads that successive waves of a group can belong to
+    plan.heads = plan.waves % plan.np == 0 ? plan.waves / plan.np : (plan.waves - 2) / plan.np + 2;
     const int64_t per_slot = g * plan.quads;
     const int64_t tokens = packed ? t : n * t;  // the whole call's
     int64_t seg = tokens * per_slot / kFullGrid;
@@ -695,8 +692,8 @@ uint64_t lds_allowed = 0;
 template <int KS, int SPLIT, bool OUT, bool WIDE>
 hipError_t launch_pass(const SelectiveScanParams &p, const ScanPlan &plan, hipStream_t stream) {
     const int64_t units = (int64_t)plan.slots * p.g * plan.quads;
-    const size_t lds = (size_t)(OUT ? 2 : 1) * kChunk * (KS + 8) * 2 + (size_t)kScanWaves * kChunk * kXPitch * 2 +
-                       (size_t)kMaxHeads * 4 * kChunk * 4 + (OUT ? (size_t)plan.heads * kChunk * kPPitch * 2 : 0);
+    const size_t lds = (size_t)(OUT ? 2 : 1) * kChunk * (KS + 16) * 2 + (size_t)kScanWaves * kChunk * kUnitP * 2 +
+                       (size_t)2 * plan.heads * kStepRows * kChunk * 4 + (OUT ? (size_t)plan.heads * kChunk * kPPitch * 2 : 0);
     auto kernel = selective_scan_kernel<KS, SPLIT, OUT, WIDE>;
     const hipError_t allowed = allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, SPLIT, OUT, WIDE>);
     if (allowed != hipSuccess) return allowed;
@@ -736,12 +733,12 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
 }  // namespace
 
 int64_t selective_scan_workspace_floats(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k, bool packed) {
-    const ScanPlan plan = make_plan(n, t, h, p, g, packed);
+    const ScanPlan plan = make_plan(n, t, h, p, g, k, packed);
     return plan.split ? plan.slots * (h * p * k + h) : 0;
 }
 
 hipError_t launch_selective_scan(const SelectiveScanParams &p, hipStream_t stream, const char **kernel_name) {
-    const ScanPlan plan = make_plan(p.n, p.t, p.h, p.p, p.g, p.starts != nullptr);
+    const ScanPlan plan = make_plan(p.n, p.t, p.h, p.p, p.g, p.k, p.starts != nullptr);
     const bool wide = p.p % 8 == 0 && p.k % 8 == 0 && rows16(p.x, p.xs_n, p.xs_t, p.xs_h) &&
                       rows16(p.b, p.bs_n, p.bs_t, p.bs_g) && rows16(p.c, p.cs_n, p.cs_t, p.cs_g) &&
                       (p.z == nullptr || rows16(p.z, p.zs_n, p.zs_t, p.zs_h)) &&
