@@ -5,22 +5,28 @@
 //
 //     h_t = e^{a_t} h_{t-1} + d_t x_t B_t^T,   y_t = h_t C_t + D x_t,   out_t = y_t * silu(z_t)
 //
-// Chunks of Q = 64 tokens turn this into matrix products.  With c_t the prefix sum of
+// Chunks of Q = 32 tokens turn this into matrix products.  With c_t the prefix sum of
 // a_t inside the chunk and H the state ahead of it,
 //
 //     Y  = (L o C B^T) X + e^{c} C H^T      L_tu = e^{c_t - c_u} d_u for u <= t, else 0
 //     H' = e^{c_Q} H + (e^{c_Q - c_u} d_u X)^T B
 //
-// so a token and head cost about 64 (k + p) + 4 p k operations on the matrix cores
+// so a token and head cost about 32 (k + p) + 4 p k operations on the matrix cores
 // instead of 5 p k on the vector units, and x, z and out move once.
 //
 // A wave owns 16 of a head's p and all of the state's k: H stays in its FP32
 // accumulators for the whole sequence, already in the lane order that the next
 // product reads it in (below).  A block is eight such waves of one group (two heads
 // at p = 64), which share the chunk's B and C in LDS and the products C B^T: the
-// lower triangle's ten tiles, scaled for each head of the block, are shared out.
-// (With 32 p a wave reads half as much LDS, but needs more than the 256 registers
-// that leave two waves a SIMD; 16 p need fewer than 128 and leave four.)
+// lower triangle's three tiles, scaled for each head of the block, are shared out.
+//
+// One barrier a chunk: between two of them a wave finishes chunk i (the product with
+// X, H', the outputs), starts chunk i + 1 (C H^T, its tiles of C B^T), puts chunk
+// i + 2's B and C into LDS and requests chunk i + 3's.  B is kept in three places in
+// LDS, C and L o C B^T in two, and x, which a wave reads alone, in one: 70 KiB at
+// k = 128 with two heads, so that two blocks fit a CU, and fewer than 128 registers,
+// so that all their waves run.  (Chunks of 64 tokens need more of both, and took
+// three barriers: 286 us against 2xx for 8 x 2048 tokens of 96 heads.)
 //
 // Layouts.  v_mfma_f32_16x16x32_bf16 takes, in lane l with r = l & 15 and g = l >> 4,
 // row (column) r of an operand at inner indices 8 g .. 8 g + 7, and leaves column r,
@@ -49,8 +55,8 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kChunk = 64;
-constexpr int kScanWaves = 8;
+constexpr int kChunk = 32;
+constexpr int kScanWaves = 4;
 constexpr int kScanBlock = kWave * kScanWaves;
 constexpr int kUnitP = 16;           // p of a wave
 constexpr int kPPitch = kChunk + 16;  // LDS row pitch of L o C B^T
@@ -62,7 +68,6 @@ struct ScanPlan {
     int32_t nseg;    // segments of a sequence (batch form)
     int32_t slots;   // segments in all; packed: an upper bound, some empty
     int32_t np;      // waves a head takes: ceil(p / 16)
-    int32_t waves;   // of a block that own p
     int32_t quads;   // blocks a group takes
     int32_t heads;   // most heads of one block
     bool split;      // some sequence may have more than one segment
@@ -102,9 +107,14 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
     return w;
 }
 
+// v, which all lanes of the wave agree on, in a scalar register.  What was divided by
+// a run-time number has passed through vector registers; a buffer whose base depends
+// on it would be loaded from in a loop over the lanes' bases.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 struct Segment {
     int seq, first, last, index, count;  // tokens [first, last) of sequence seq; segment `index` of `count`
-    int64_t token0;                      // the sequence's first token on the t axis
+    int token0;                          // the sequence's first token on the t axis
     bool ok;
 };
 
@@ -115,7 +125,7 @@ __device__ __forceinline__ Segment find_segment(const SelectiveScanParams &p, co
     Segment s;
     int len;
     if (p.starts == nullptr) {
-        s.seq = u / plan.nseg;
+        s.seq = uniform(u / plan.nseg);
         s.index = u - s.seq * plan.nseg;
         s.token0 = 0;
         len = p.t;
@@ -123,7 +133,7 @@ __device__ __forceinline__ Segment find_segment(const SelectiveScanParams &p, co
         int lo = 0, hi = p.n;  // the last i with starts[i] / seg + i <= u
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if ((int64_t)load_uniform(p.starts, mid) / plan.seg + mid <= u)
+            if (uniform(load_uniform(p.starts, mid) / plan.seg) + mid <= u)
                 lo = mid;
             else
                 hi = mid;
@@ -132,9 +142,9 @@ __device__ __forceinline__ Segment find_segment(const SelectiveScanParams &p, co
         const int a = load_uniform(p.starts, lo), e = load_uniform(p.starts, lo + 1);
         len = (a >= 0 && a <= e && e <= p.t) ? e - a : -1;
         s.token0 = len >= 0 ? a : 0;
-        s.index = u - (int)(s.token0 / plan.seg) - lo;
+        s.index = u - uniform(s.token0 / plan.seg) - lo;
     }
-    s.count = len > 0 ? (len + plan.seg - 1) / plan.seg : 1;
+    s.count = len > 0 ? uniform((len - 1) / plan.seg) + 1 : 1;
     s.ok = len >= 0 && s.index >= 0 && s.index < s.count;
     s.first = s.ok ? s.index * plan.seg : 0;
     s.last = s.ok ? s.first + min(len - s.first, plan.seg) : 0;
@@ -152,7 +162,7 @@ __device__ __forceinline__ void check_table(const SelectiveScanParams &p) {
     if (bad) atomicOr(p.status, DCCONV_DEV_BAD_SEQ);
 }
 
-// Sums over the 64 lanes of a wave: of the lanes up to this one, and of the lanes
+// Sums over the first 32 lanes of a wave: of the lanes up to this one, and of the lanes
 // behind it (each formed from small to large distances, so that the decay of a
 // recent token is not the difference of two long sums).
 template <int CTRL>
@@ -168,12 +178,11 @@ __device__ __forceinline__ void wave_sums(float v, int lane, float *upto, float 
     u += dpp_shift<0x112>(u), b += dpp_shift<0x102>(b);
     u += dpp_shift<0x114>(u), b += dpp_shift<0x104>(b);
     u += dpp_shift<0x118>(u), b += dpp_shift<0x108>(b);
-    const float r0 = lane_value(u, 15), r1 = lane_value(u, 31), r2 = lane_value(u, 47), r3 = lane_value(u, 63);
-    const int row = lane >> 4;
-    *upto = u + (row == 0 ? 0.0f : row == 1 ? r0 : row == 2 ? r0 + r1 : r0 + r1 + r2);
-    *total = r0 + r1 + r2 + r3;
+    const float r0 = lane_value(u, 15), r1 = lane_value(u, 31);
+    *upto = u + (lane >= 16 ? r0 : 0.0f);
+    *total = r0 + r1;
     b = dpp_shift<0x101>(b);  // the lanes behind this one; zero for a row's last
-    *behind = b + (row == 3 ? 0.0f : row == 2 ? r3 : row == 1 ? r2 + r3 : r1 + r2 + r3);
+    *behind = b + (lane < 16 ? r1 : 0.0f);
 }
 
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer
@@ -293,55 +302,57 @@ __device__ __forceinline__ bool wide_state(const SelectiveScanParams &p) {
 // OUT: the outputs and final states.  Otherwise the state that each segment but a
 // sequence's last builds up from zero, and its decay, for the join.
 template <int KS, int SPLIT, bool OUT, bool WIDE>
-__global__ __launch_bounds__(kScanBlock, KS <= 128 ? 4 : 2) void selective_scan_kernel(const SelectiveScanParams p,
+__global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_kernel(const SelectiveScanParams p,
                                                                                       const ScanPlan plan) {
     constexpr int kPitch = KS + 16;
-    constexpr int kTiles = KS / 16;
-    constexpr int kPieces = KS / 64;  // 16-byte pieces of B (of C) a thread stages
+    constexpr int kTiles = KS / 16, kSteps = KS / 32;
+    constexpr int kAcross = KS / 8;  // 16-byte pieces of a row of B (of C)
+    constexpr int kPieces = (kChunk * kAcross + kScanBlock - 1) / kScanBlock;  // of them a thread stages
     extern __shared__ u32x4 smem[];
-    uint16_t *sb = reinterpret_cast<uint16_t *>(smem);
-    uint16_t *sc = sb + kChunk * kPitch;
-    uint16_t *sx_all = sc + (OUT ? kChunk * kPitch : 0);
-    float *steps = reinterpret_cast<float *>(sx_all + kScanWaves * kChunk * kUnitP);  // [2][heads][kStepRows][64]
-    uint16_t *sp = reinterpret_cast<uint16_t *>(steps + 2 * plan.heads * kStepRows * kChunk);
+    uint16_t *sb = reinterpret_cast<uint16_t *>(smem);            // [2][kChunk][kPitch]
+    uint16_t *sc = sb + 2 * kChunk * kPitch;                      // [2][kChunk][kPitch]
+    uint16_t *sx_all = sc + (OUT ? 2 * kChunk * kPitch : 0);      // [wave][kChunk][kUnitP]
+    float *steps = reinterpret_cast<float *>(sx_all + kScanWaves * kChunk * kUnitP);  // [2][heads][kStepRows][kChunk]
+    uint16_t *sp = reinterpret_cast<uint16_t *>(steps + 2 * plan.heads * kStepRows * kChunk);  // [heads][kChunk][kPPitch]
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     uint16_t *sx = sx_all + wave * kChunk * kUnitP;
-    const int per_group = p.h / p.g, units = per_group * plan.np;
+    const int per_group = uniform(p.h / p.g), units = per_group * plan.np;
 
     if (OUT && blockIdx.x == 0 && blockIdx.y == 0) check_table(p);
-    // result tiles above the diagonal that a product over 32 tokens reads: zeros for good
+    // the tile above the diagonal that the product over 32 tokens reads: zeros for good
     if (OUT)
-        for (int i = tid; i < plan.heads * 2 * 16 * 16; i += kScanBlock) {
-            const int head = i >> 9, tile = (i >> 8) & 1, row = (i >> 4) & 15, col = i & 15;
-            sp[(head * kChunk + 32 * tile + row) * kPPitch + 32 * tile + 8 * (col >> 2) + 4 + (col & 3)] = 0;
+        for (int i = tid; i < plan.heads * 16 * 16; i += kScanBlock) {
+            const int mat = i >> 8, row = (i >> 4) & 15, col = i & 15;
+            sp[(mat * kChunk + row) * kPPitch + 8 * (col >> 2) + 4 + (col & 3)] = 0;
         }
 
     const int64_t unit = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (unit >= (int64_t)plan.slots * p.g * plan.quads) return;
-    const int quad = (int)(unit % plan.quads);
+    const int quad = uniform((int)(unit % plan.quads));
     const int64_t ug = unit / plan.quads;
-    const int group = (int)(ug % p.g), u = (int)(ug / p.g);
+    const int group = uniform((int)(ug % p.g)), u = uniform((int)(ug / p.g));
     const Segment seg = find_segment(p, plan, u);
     if (!seg.ok || (!OUT && seg.index == seg.count - 1)) return;
 
-    const int last_unit = min(quad * plan.waves + plan.waves, units) - 1;
-    const int mine = min(quad * plan.waves + wave, last_unit);
-    const bool valid = quad * plan.waves + wave == mine;
-    const int first_head = quad * plan.waves / plan.np;
-    const int heads = last_unit / plan.np - first_head + 1;
-    const int head_slot = mine / plan.np - first_head;
-    const int head = group * per_group + mine / plan.np;
-    const int p0 = (mine % plan.np) * kUnitP;
+    const int last_unit = min(quad * kScanWaves + kScanWaves, units) - 1;
+    const int mine = min(quad * kScanWaves + wave, last_unit);
+    const bool valid = quad * kScanWaves + wave == mine;
+    const int first_head = uniform(quad * kScanWaves / plan.np);
+    const int heads = uniform(last_unit / plan.np) - first_head + 1;
+    const int my_head = uniform(mine / plan.np);  // of the group
+    const int head_slot = my_head - first_head;
+    const int head = group * per_group + my_head;
+    const int p0 = (mine - my_head * plan.np) * kUnitP;
     const int pcount = valid ? min(kUnitP, p.p - p0) : 0;
 
-    const int slot = route_row(p.idx, p.status, p.n, p.s, seg.seq, lane);
+    const int slot = uniform(route_row(p.idx, p.status, p.n, p.s, seg.seq, lane));
     if (slot < 0) {  // a padding sequence: zeros, and no state moves
         if (OUT)
             for (int t = seg.first; t < seg.last; ++t)
                 if (lane < pcount)
-                    p.out[seg.seq * p.os_n + (seg.token0 + t) * p.os_t + head * p.os_h + p0 + lane] = 0;
+                    p.out[seg.seq * p.os_n + ((int64_t)seg.token0 + t) * p.os_t + head * p.os_h + p0 + lane] = 0;
         return;
     }
 
@@ -361,8 +372,8 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 4 : 2) void selective_scan_
     }
 
     // ---- the operands' rows: B and C shared out over the block, the rest a wave's own
-    const int64_t tok = seg.token0 + seg.first;
-    constexpr int kRowsPerPiece = kScanBlock * 8 / KS, kAcross = KS / 8;
+    const int64_t tok = (int64_t)seg.token0 + seg.first;
+    constexpr int kRowsPerPiece = kScanBlock / kAcross;
     ChunkRows<WIDE> rb(p.b + seg.seq * p.bs_n + tok * p.bs_t + group * p.bs_g, p.bs_t, kRowsPerPiece, p.k);
     ChunkRows<WIDE> rc(p.c + seg.seq * p.cs_n + tok * p.cs_t + group * p.cs_g, p.cs_t, kRowsPerPiece, p.k);
     ChunkRows<WIDE> rx(p.x + seg.seq * p.xs_n + tok * p.xs_t + head * p.xs_h + p0, p.xs_t, 32, pcount);
@@ -371,8 +382,51 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 4 : 2) void selective_scan_
     const float skip = OUT && p.d_skip != nullptr ? p.d_skip[head] : 0.0f;
     const bool gated = p.z != nullptr;
 
-    // ---- the steps of a head's chunk, one chunk ahead: the last waves (which have the
-    // fewest tiles of C B^T) take a head each
+    // Every fetch is unconditional (of no rows behind the last chunk): registers that only
+    // one of two paths loads are waited for where the paths join.
+    uint32_t nb[kPieces][4], nc[kPieces][4], nx[4], zv[2][2];
+    auto fetch_bc = [&](int left) {
+        const int n = max(min(left, kChunk), 0), i = here(tid);
+        rb.begin(n, i / kAcross, i % kAcross * 8);
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) rb.template load<8>(nb[q], q);
+        rb.advance();
+        if (OUT) {
+            rc.begin(n, i / kAcross, i % kAcross * 8);
+#pragma unroll
+            for (int q = 0; q < kPieces; ++q) rc.template load<8>(nc[q], q);
+            rc.advance();
+        }
+    };
+    auto stage_bc = [&](int slot2) {
+        const int row = tid / kAcross, col = tid % kAcross * 8;
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+            if (kChunk * kAcross < kScanBlock && row >= kChunk) break;
+            const int to = (q * kRowsPerPiece + row) * kPitch + col;
+            *reinterpret_cast<u32x4 *>(sb + slot2 * kChunk * kPitch + to) = u32x4{nb[q][0], nb[q][1], nb[q][2], nb[q][3]};
+            if (OUT)
+                *reinterpret_cast<u32x4 *>(sc + slot2 * kChunk * kPitch + to) = u32x4{nc[q][0], nc[q][1], nc[q][2], nc[q][3]};
+        }
+    };
+    auto fetch_x = [&](int left) {
+        const int l = here(lane);
+        rx.begin(max(min(left, kChunk), 0), l >> 1, (l & 1) * 8);
+        rx.template load<8>(nx, 0);
+        rx.advance();
+    };
+    auto stage_x = [&]() { *reinterpret_cast<u32x4 *>(sx + lane * 8) = u32x4{nx[0], nx[1], nx[2], nx[3]}; };
+    auto fetch_z = [&](int left) {
+        if (!OUT || !gated) return;
+        const int l = here(lane);
+        rz.begin(max(min(left, kChunk), 0), l & 15, l >> 4 << 2);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) rz.template load<4>(zv[tt], tt);
+        rz.advance();
+    };
+
+    // ---- the steps of a head's chunk: the last waves (which have the fewest tiles of
+    // C B^T) take a head each
     const int job = kScanWaves - 1 - wave;
     const bool has_job = job < heads;
     const int job_head = group * per_group + first_head + min(job, heads - 1);
@@ -380,185 +434,128 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 4 : 2) void selective_scan_
     const float dt_bias = p.dt_bias != nullptr ? p.dt_bias[job_head] : 0.0f;
     int64_t dt_at = seg.seq * p.ds_n + tok * p.ds_t + job_head;
     float decay_sum = 0.0f;
+    // (as it is in memory: converting it here would wait for it)
     auto fetch_step = [&](int left) {
-        float v = 0.0f;
+        uint32_t v = 0;
         const int l = here(lane);
-        if (has_job && l < left)
-            v = p.dt_f32 ? static_cast<const float *>(p.dt)[dt_at + l * p.ds_t]
-                         : bf16_bits_to_f32(static_cast<const uint16_t *>(p.dt)[dt_at + l * p.ds_t]);
+        if (has_job && l < min(left, kChunk))
+            v = p.dt_f32 ? static_cast<const uint32_t *>(p.dt)[dt_at + l * p.ds_t]
+                         : static_cast<const uint16_t *>(p.dt)[dt_at + l * p.ds_t];
         dt_at += kChunk * p.ds_t;
         return v;
     };
-    auto put_steps = [&](float v, int left, int parity) {
-        float d = v + dt_bias;
+    auto put_steps = [&](uint32_t v, int left, int s_slot) {
+        float d = __uint_as_float(p.dt_f32 ? v : v << 16) + dt_bias;
         if (p.dt_softplus) d = softplus(d);
-        if (lane >= left) d = 0.0f;
+        if (lane >= min(left, kChunk)) d = 0.0f;
         float upto, behind, total;
         wave_sums(d * a2, lane, &upto, &behind, &total);
-        float *to = steps + ((parity * plan.heads + job) * kStepRows) * kChunk + lane;
-        to[0] = upto;
-        to[kChunk] = d;
-        to[2 * kChunk] = d * __builtin_amdgcn_exp2f(behind);
-        to[3 * kChunk] = __builtin_amdgcn_exp2f(upto);
+        float *to = steps + ((s_slot * plan.heads + job) * kStepRows) * kChunk + lane;
+        if (lane < kChunk) {
+            to[0] = upto;
+            to[kChunk] = d;
+            to[2 * kChunk] = d * __builtin_amdgcn_exp2f(behind);
+            to[3 * kChunk] = __builtin_amdgcn_exp2f(upto);
+        }
         decay_sum += total;
     };
 
-    // ---- a chunk on its way from memory
-    uint32_t nb[kPieces][4], nc[kPieces][4], nx[2][4];
-    auto fetch = [&](int left) {
-        const int n = min(left, kChunk), i = here(tid), l = i & 63;
-        rb.begin(n, i / kAcross, i % kAcross * 8);
+    // ---- the first half of a chunk: y = e^c C H^T, and this wave's tiles of L o C B^T
+    f32x4_t y[2];
+    auto start = [&](int slot2) {
+        const uint16_t *bm = sb + slot2 * kChunk * kPitch, *cm = sc + slot2 * kChunk * kPitch;
+        const float *st = steps + slot2 * plan.heads * kStepRows * kChunk;
+        const uint16_t *ca = cm + r * kPitch + 8 * g;
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) rb.template load<8>(nb[q], q);
-        if (OUT) {
-            rc.begin(n, i / kAcross, i % kAcross * 8);
+        for (int tt = 0; tt < 2; ++tt) y[tt] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-            for (int q = 0; q < kPieces; ++q) rc.template load<8>(nc[q], q);
+        for (int m = 0; m < kSteps; ++m) {
+            const f32x4_t h0 = hs[2 * m], h1 = hs[2 * m + 1];
+            const u32x4 hb = {pack_bf16x2(h0[0], h0[1]), pack_bf16x2(h0[2], h0[3]), pack_bf16x2(h1[0], h1[1]),
+                              pack_bf16x2(h1[2], h1[3])};
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) y[tt] = mfma(hb, lds16(ca + 16 * tt * kPitch + 32 * m), y[tt]);
         }
-        rx.begin(n, l >> 1, (l & 1) * 8);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) rx.template load<8>(nx[q], q);
-        rb.advance();
-        rc.advance();
-        rx.advance();
+        for (int tt = 0; tt < 2; ++tt) y[tt] *= st[(head_slot * kStepRows + 3) * kChunk + 16 * tt + r];
+
+        for (int it = wave; it < 3 * heads; it += kScanWaves) {
+            const int hd = it / 3, e = it - 3 * hd;
+            const int tt = e > 0, ut = e > 1;
+            f32x4_t acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < kSteps; ++m)
+                acc = mfma(lds16(bm + (16 * ut + r) * kPitch + 32 * m + 8 * g),
+                           lds16(cm + (16 * tt + r) * kPitch + 32 * m + 8 * g), acc);
+            const int t = 16 * tt + r, u0 = 16 * ut + 4 * g;
+            const float *sh = st + hd * kStepRows * kChunk;
+            const f32x4_t cu = *reinterpret_cast<const f32x4_t *>(sh + u0);
+            const f32x4_t du = *reinterpret_cast<const f32x4_t *>(sh + kChunk + u0);
+            const float ct = sh[t];
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = u0 + i <= t ? acc[i] * __builtin_amdgcn_exp2f(ct - cu[i]) * du[i] : 0.0f;
+            *reinterpret_cast<u32x2 *>(sp + (hd * kChunk + t) * kPPitch + 8 * g + 4 * ut) =
+                u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        }
     };
 
-    const int length = seg.last - seg.first;
-    float step0 = fetch_step(length), step1 = fetch_step(length - kChunk);
-    fetch(length);
-    if (has_job) put_steps(step0, length, 0);
-    for (int left = length, parity = 0; left > 0; left -= kChunk, parity ^= 1) {
-        const int rows = min(left, kChunk);
-        const float *ss = steps + ((parity * plan.heads + head_slot) * kStepRows) * kChunk;
-        // ---- the chunk into LDS
-#pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-            const int to = (q * kRowsPerPiece + tid / kAcross) * kPitch + tid % kAcross * 8;
-            *reinterpret_cast<u32x4 *>(sb + to) = u32x4{nb[q][0], nb[q][1], nb[q][2], nb[q][3]};
-            if (OUT) *reinterpret_cast<u32x4 *>(sc + to) = u32x4{nc[q][0], nc[q][1], nc[q][2], nc[q][3]};
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<u32x4 *>(sx + (q * 32 + (lane >> 1)) * kUnitP + (lane & 1) * 8) =
-                u32x4{nx[q][0], nx[q][1], nx[q][2], nx[q][3]};
-        __syncthreads();
-        if (left > kChunk && has_job) put_steps(step1, left - kChunk, parity ^ 1);
-        uint32_t zv[4][2];
-        if (OUT && gated) {
-            const int l = here(lane);
-            rz.begin(rows, l & 15, l >> 4 << 2);
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt) rz.template load<4>(zv[tt], tt);
-            rz.advance();
-        }
-        if (left > kChunk) {
-            step1 = fetch_step(left - 2 * kChunk);
-            fetch(left - kChunk);
-        }
-
-        f32x4_t y[4];
-        if constexpr (OUT) {
-            // ---- C B^T, a tile for a head at a time
-            for (int it = wave; it < 10 * heads; it += kScanWaves) {
-                const int hd = it / 10, e = it - 10 * hd;  // tile (tt, ut) of the lower triangle, row by row
-                const int tt = e >= 6 ? 3 : e >= 3 ? 2 : e >= 1 ? 1 : 0, ut = e - tt * (tt + 1) / 2;
-                f32x4_t acc = {0, 0, 0, 0};
-#pragma unroll
-                for (int m = 0; m < KS / 32; ++m)
-                    acc = mfma(lds16(sb + (16 * ut + r) * kPitch + 32 * m + 8 * g),
-                               lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g), acc);
-                const int t = 16 * tt + r, u0 = 16 * ut + 4 * g;
-                const float *sh = steps + ((parity * plan.heads + hd) * kStepRows) * kChunk;
-                const f32x4_t cu = *reinterpret_cast<const f32x4_t *>(sh + u0);
-                const f32x4_t du = *reinterpret_cast<const f32x4_t *>(sh + kChunk + u0);
-                const float ct = sh[t];
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = u0 + i <= t ? acc[i] * __builtin_amdgcn_exp2f(ct - cu[i]) * du[i] : 0.0f;
-                *reinterpret_cast<u32x2 *>(sp + (hd * kChunk + t) * kPPitch + 32 * (ut >> 1) + 8 * g + 4 * (ut & 1)) =
-                    u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-            }
-            // ---- e^c C H^T
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt) y[tt] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-            for (int m = 0; m < KS / 32; ++m) {
-                const f32x4_t h0 = hs[2 * m], h1 = hs[2 * m + 1];
-                const u32x4 hb = {pack_bf16x2(h0[0], h0[1]), pack_bf16x2(h0[2], h0[3]), pack_bf16x2(h1[0], h1[1]),
-                                  pack_bf16x2(h1[2], h1[3])};
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
-                    y[tt] = mfma(hb, lds16(sc + (16 * tt + r) * kPitch + 32 * m + 8 * g), y[tt]);
-            }
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt) y[tt] *= ss[3 * kChunk + 16 * tt + r];
-            __syncthreads();
-        }
-
-        u32x4 xf[2];  // x with tokens inside, 32 at a time
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-            xf[s] = load_columns(sx + (32 * s + 4 * g + (r >> 2)) * kUnitP + 4 * (r & 3), kUnitP);
+    // ---- the second half: y += (L o C B^T) X, H' = e^{c_Q} H + (scaled x)^T B, and the outputs
+    auto finish = [&](int rows, int slot2) {
+        const uint16_t *bm = sb + slot2 * kChunk * kPitch;
+        const uint16_t *pm = sp + head_slot * kChunk * kPPitch;
+        const float *ss = steps + (slot2 * plan.heads + head_slot) * kStepRows * kChunk;
+        u32x4 xf = load_columns(sx + (4 * g + (r >> 2)) * kUnitP + 4 * (r & 3), kUnitP);
         // An infinity or NaN of a later token must not meet the zeros of L: it is taken
         // out of the matrix products and its terms are added one by one.
         float probe = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) probe = sum_pair(xf[i >> 2][i & 3], probe);
+        for (int i = 0; i < 4; ++i) probe = sum_pair(xf[i], probe);
         const bool bad = __any(!(__builtin_fabsf(probe) < kHuge));
         if (bad) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) xf[i >> 2][i & 3] = finite_pair(xf[i >> 2][i & 3]);
+            for (int i = 0; i < 4; ++i) xf[i] = finite_pair(xf[i]);
         }
         if constexpr (OUT) {
-            // ---- (L o C B^T) X
-            const uint16_t *mp = sp + head_slot * kChunk * kPPitch;
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                for (int s = 0; s <= tt / 2; ++s)
-                    y[tt] = mfma(xf[s], lds16(mp + (16 * tt + r) * kPPitch + 32 * s + 8 * g), y[tt]);
+            for (int tt = 0; tt < 2; ++tt) y[tt] = mfma(xf, lds16(pm + (16 * tt + r) * kPPitch + 8 * g), y[tt]);
             if (bad) {
                 const int rr = here(r), gg = here(g);
 #pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
+                for (int tt = 0; tt < 2; ++tt)
                     for (int q = 0; q <= 16 * tt + rr; ++q)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float v = bf16_bits_to_f32(sx[q * kUnitP + 4 * gg + i]);
                             if (!is_finite(v))
-                                y[tt][i] += bf16_bits_to_f32(mp[(16 * tt + rr) * kPPitch + (q & 32) + 2 * (q & 12) + ((q & 16) >> 2) + (q & 3)]) * v;
+                                y[tt][i] += bf16_bits_to_f32(pm[(16 * tt + rr) * kPPitch + 2 * (q & 12) + ((q & 16) >> 2) + (q & 3)]) * v;
                         }
             }
         }
-
-        // ---- H' = e^{c_Q} H + (scaled x)^T B
+        const f32x4_t w0 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 4 * g);
+        const f32x4_t w1 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 16 + 4 * g);
         const float dec = ss[3 * kChunk + kChunk - 1];
+        u32x4 xw[SPLIT];
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) hs[m] *= dec;
+        for (int i = 0; i < 4; ++i) {
+            float v0 = lo_f32(xf[i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
+            float v1 = hi_f32(xf[i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const f32x4_t w0 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 32 * s + 4 * g);
-            const f32x4_t w1 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 32 * s + 16 + 4 * g);
-            u32x4 xw[SPLIT];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v0 = lo_f32(xf[s][i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
-                float v1 = hi_f32(xf[s][i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
-#pragma unroll
-                for (int part = 0; part < SPLIT; ++part) {
-                    const uint32_t h = pack_bf16x2(v0, v1);
-                    xw[part][i] = h;
-                    v0 -= lo_f32(h);
-                    v1 -= hi_f32(h);
-                }
+            for (int part = 0; part < SPLIT; ++part) {
+                const uint32_t h = pack_bf16x2(v0, v1);
+                xw[part][i] = h;
+                v0 -= lo_f32(h);
+                v1 -= hi_f32(h);
             }
+        }
+        const uint16_t *ba = bm + (4 * g + (r >> 2)) * kPitch + 8 * (r & 3);
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m) {
-                const u32x4 bt = load_columns(sb + (32 * s + 4 * g + (r >> 2)) * kPitch + 32 * (m >> 1) + 8 * (r & 3) + 4 * (m & 1), kPitch);
+        for (int m = 0; m < kTiles; ++m) {
+            const u32x4 bt = load_columns(ba + 32 * (m >> 1) + 4 * (m & 1), kPitch);
+            hs[m] *= dec;
 #pragma unroll
-                for (int part = SPLIT - 1; part >= 0; --part) hs[m] = mfma(bt, xw[part], hs[m]);
-            }
+            for (int part = SPLIT - 1; part >= 0; --part) hs[m] = mfma(bt, xw[part], hs[m]);
         }
         if (bad) {
             const int rr = here(r), gg = here(g);
@@ -569,16 +566,15 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 4 : 2) void selective_scan_
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) hs[m][i] += w * bf16_bits_to_f32(sb[q * kPitch + column(m, gg) + i]);
+                    for (int i = 0; i < 4; ++i) hs[m][i] += w * bf16_bits_to_f32(bm[q * kPitch + column(m, gg) + i]);
             }
         }
-
-        // ---- skip, gate and store: four consecutive p of a token a lane
+        // skip, gate and store: four consecutive p of a token a lane
         if constexpr (OUT) {
             const int l = here(lane);
             ro.begin(rows, l & 15, l >> 4 << 2);
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
+            for (int tt = 0; tt < 2; ++tt) {
                 const u32x2 xv = *reinterpret_cast<const u32x2 *>(sx + (16 * tt + r) * kUnitP + 4 * g);
                 float o[4];
 #pragma unroll
@@ -593,6 +589,38 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 4 : 2) void selective_scan_
             }
             ro.advance();
         }
+    };
+
+    int left = seg.last - seg.first;  // tokens from the current chunk on
+    {
+        const uint32_t step0 = fetch_step(left), step1 = fetch_step(left - kChunk);
+        fetch_bc(left);
+        fetch_x(left);
+        fetch_z(left);
+        if (has_job) put_steps(step0, left, 0);
+        stage_bc(0);
+        stage_x();
+        fetch_bc(left - kChunk);
+        fetch_x(left - kChunk);
+        if (has_job) put_steps(step1, left - kChunk, 1);
+    }
+    uint32_t step = fetch_step(left - 2 * kChunk);
+    __syncthreads();
+    if constexpr (OUT) start(0);
+    stage_bc(1);
+    fetch_bc(left - 2 * kChunk);
+    __syncthreads();
+    for (int b = 0; left > 0; left -= kChunk, b ^= 1) {
+        finish(min(left, kChunk), b);
+        stage_x();
+        fetch_x(left - 2 * kChunk);
+        fetch_z(left - kChunk);
+        __syncthreads();  // chunk i's places are free for chunk i + 2
+        stage_bc(b);
+        fetch_bc(left - 3 * kChunk);
+        if constexpr (OUT) start(b ^ 1);
+        if (has_job) put_steps(step, left - 2 * kChunk, b);
+        step = fetch_step(left - 3 * kChunk);
         __syncthreads();
     }
 
@@ -645,23 +673,31 @@ __global__ __launch_bounds__(256) void selective_join_kernel(const SelectiveScan
     });
 }
 
-// Two blocks a CU fill the card.  Sequences are cut into segments only while
-// there are fewer blocks than that, and not below kMinSegment tokens: a segment
-// costs another pass over its x and B, and a state's round trip through memory.
-constexpr int64_t kFullGrid = 512;
+// Three blocks a CU fill the card.  With fewer than one a CU, sequences are cut into
+// segments, as many as fill it but not below kMinSegment tokens: a segment costs
+// another pass over its x and B, and a state's round trip through memory.  Packed
+// sequences, whose lengths the host does not know, are cut where they are longer than
+// kLongSequence even if there are enough of them, so that one does not outlast the rest.
+constexpr int64_t kFullGrid = 768;
+constexpr int64_t kEnoughBlocks = 256;
 constexpr int64_t kMinSegment = 256;
+constexpr int64_t kLongSequence = 2048;
 
-ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k, bool packed) {
+ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, bool packed) {
     ScanPlan plan;
     plan.np = (int32_t)((p + kUnitP - 1) / kUnitP);
-    // (eight heads and the widest state would not fit LDS)
-    plan.waves = plan.np == 1 && k > 128 ? kScanWaves / 2 : kScanWaves;
-    plan.quads = (int32_t)((h / g * plan.np + plan.waves - 1) / plan.waves);
+    plan.quads = (int32_t)((h / g * plan.np + kScanWaves - 1) / kScanWaves);
     // heads that successive waves of a group can belong to
-    plan.heads = plan.waves % plan.np == 0 ? plan.waves / plan.np : (plan.waves - 2) / plan.np + 2;
-    const int64_t per_slot = g * plan.quads;
+    plan.heads = kScanWaves % plan.np == 0 ? kScanWaves / plan.np : (kScanWaves - 2) / plan.np + 2;
+    const int64_t per_slot = g * plan.quads, blocks = n * per_slot;
     const int64_t tokens = packed ? t : n * t;  // the whole call's
-    int64_t seg = tokens * per_slot / kFullGrid;
+    int64_t seg;
+    if (blocks >= kEnoughBlocks) {
+        seg = packed ? (tokens * per_slot / kFullGrid > kLongSequence ? tokens * per_slot / kFullGrid : kLongSequence) : t;
+    } else {
+        const int64_t each = kFullGrid / ((packed ? 1 : n) * per_slot);  // segments of the t axis
+        seg = each > 1 ? (t + each - 1) / each : t;
+    }
     seg = (seg + kChunk - 1) / kChunk * kChunk;
     if (seg < kMinSegment) seg = kMinSegment;
     if (seg >= t) seg = (t + kChunk - 1) / kChunk * kChunk;
@@ -692,8 +728,9 @@ uint64_t lds_allowed = 0;
 template <int KS, int SPLIT, bool OUT, bool WIDE>
 hipError_t launch_pass(const SelectiveScanParams &p, const ScanPlan &plan, hipStream_t stream) {
     const int64_t units = (int64_t)plan.slots * p.g * plan.quads;
-    const size_t lds = (size_t)(OUT ? 2 : 1) * kChunk * (KS + 16) * 2 + (size_t)kScanWaves * kChunk * kUnitP * 2 +
-                       (size_t)2 * plan.heads * kStepRows * kChunk * 4 + (OUT ? (size_t)plan.heads * kChunk * kPPitch * 2 : 0);
+    const size_t lds = (size_t)(OUT ? 4 : 2) * kChunk * (KS + 16) * 2 + (size_t)kScanWaves * kChunk * kUnitP * 2 +
+                       (size_t)2 * plan.heads * kStepRows * kChunk * 4 +
+                       (OUT ? (size_t)plan.heads * kChunk * kPPitch * 2 : 0);
     auto kernel = selective_scan_kernel<KS, SPLIT, OUT, WIDE>;
     const hipError_t allowed = allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, SPLIT, OUT, WIDE>);
     if (allowed != hipSuccess) return allowed;
@@ -733,12 +770,12 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
 }  // namespace
 
 int64_t selective_scan_workspace_floats(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k, bool packed) {
-    const ScanPlan plan = make_plan(n, t, h, p, g, k, packed);
+    const ScanPlan plan = make_plan(n, t, h, p, g, packed);
     return plan.split ? plan.slots * (h * p * k + h) : 0;
 }
 
 hipError_t launch_selective_scan(const SelectiveScanParams &p, hipStream_t stream, const char **kernel_name) {
-    const ScanPlan plan = make_plan(p.n, p.t, p.h, p.p, p.g, p.k, p.starts != nullptr);
+    const ScanPlan plan = make_plan(p.n, p.t, p.h, p.p, p.g, p.starts != nullptr);
     const bool wide = p.p % 8 == 0 && p.k % 8 == 0 && rows16(p.x, p.xs_n, p.xs_t, p.xs_h) &&
                       rows16(p.b, p.bs_n, p.bs_t, p.bs_g) && rows16(p.c, p.cs_n, p.cs_t, p.cs_g) &&
                       (p.z == nullptr || rows16(p.z, p.zs_n, p.zs_t, p.zs_h)) &&
