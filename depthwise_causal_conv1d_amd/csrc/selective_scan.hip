@@ -69,6 +69,8 @@ struct ScanPlan {
     int32_t slots;   // segments in all; packed: an upper bound, some empty
     int32_t np;      // waves a head takes: ceil(p / 16)
     int32_t quads;   // blocks a group takes
+    int32_t run;     // of them that follow each other on one XCD
+    int32_t parts;   // runs a group takes
     int32_t heads;   // most heads of one block
     bool split;      // some sequence may have more than one segment
 };
@@ -198,18 +200,15 @@ struct ChunkRows {
     int32_t step, width, row0, col, rows;
     uint32_t at0, hop;
     Buffer buf;
-    __device__ __forceinline__ ChunkRows(const uint16_t *first, int64_t stride, int step, int width)
-        : base(first), stride(stride), step(step), width(width) {}
-    __device__ __forceinline__ void begin(int n, int row, int column) {
-        rows = n;
-        row0 = row;
-        col = column;
+    __device__ __forceinline__ ChunkRows(const uint16_t *first, int64_t stride, int step, int width, int row, int col)
+        : base(first), stride(stride), step(step), width(width), row0(row), col(col) {
         const uint32_t bytes = 2u * (uint32_t)stride;
-        if (WIDE) {
-            buf = make_buffer(base, n > 0 ? (uint32_t)(n - 1) * bytes + 2u * (uint32_t)width : 0u);
-            at0 = col < width ? (uint32_t)row0 * bytes + 2u * (uint32_t)col : kNowhere;
-            hop = (uint32_t)step * bytes;
-        }
+        at0 = col < width ? (uint32_t)row * bytes + 2u * (uint32_t)col : kNowhere;
+        hop = (uint32_t)step * bytes;
+    }
+    __device__ __forceinline__ void begin(int n) {
+        rows = n;
+        if (WIDE) buf = make_buffer(base, n > 0 ? (uint32_t)(n - 1) * 2u * (uint32_t)stride + 2u * (uint32_t)width : 0u);
     }
     __device__ __forceinline__ void advance() { base += kChunk * stride; }
     // N values (8 or 4) of row row0 + q * step
@@ -328,11 +327,15 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
             sp[(mat * kChunk + row) * kPPitch + 8 * (col >> 2) + 4 + (col & 3)] = 0;
         }
 
-    const int64_t unit = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    if (unit >= (int64_t)plan.slots * p.g * plan.quads) return;
-    const int quad = uniform((int)(unit % plan.quads));
-    const int64_t ug = unit / plan.quads;
-    const int group = uniform((int)(ug % p.g)), u = uniform((int)(ug / p.g));
+    // Blocks are dealt to the eight XCDs in turn: a run of a group's blocks, which read
+    // the same B and C, goes to one of them, whose L2 then fetches those once.
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int turn = uniform((int)((block >> 3) / plan.run));
+    const int64_t run = (int64_t)turn * 8 + (block & 7);
+    const int64_t ug = run / plan.parts;
+    const int quad = uniform((int)((block >> 3) - (int64_t)turn * plan.run + (run - ug * plan.parts) * plan.run));
+    const int u = uniform((int)(ug / p.g)), group = uniform((int)(ug - (int64_t)u * p.g));
+    if (u >= plan.slots || quad >= plan.quads) return;
     const Segment seg = find_segment(p, plan, u);
     if (!seg.ok || (!OUT && seg.index == seg.count - 1)) return;
 
@@ -374,11 +377,11 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
     // ---- the operands' rows: B and C shared out over the block, the rest a wave's own
     const int64_t tok = (int64_t)seg.token0 + seg.first;
     constexpr int kRowsPerPiece = kScanBlock / kAcross;
-    ChunkRows<WIDE> rb(p.b + seg.seq * p.bs_n + tok * p.bs_t + group * p.bs_g, p.bs_t, kRowsPerPiece, p.k);
-    ChunkRows<WIDE> rc(p.c + seg.seq * p.cs_n + tok * p.cs_t + group * p.cs_g, p.cs_t, kRowsPerPiece, p.k);
-    ChunkRows<WIDE> rx(p.x + seg.seq * p.xs_n + tok * p.xs_t + head * p.xs_h + p0, p.xs_t, 32, pcount);
-    ChunkRows<WIDE> rz(p.z + seg.seq * p.zs_n + tok * p.zs_t + head * p.zs_h + p0, p.zs_t, 16, pcount);
-    ChunkRows<WIDE> ro(p.out + seg.seq * p.os_n + tok * p.os_t + head * p.os_h + p0, p.os_t, 16, pcount);
+    ChunkRows<WIDE> rb(p.b + seg.seq * p.bs_n + tok * p.bs_t + group * p.bs_g, p.bs_t, kRowsPerPiece, p.k, tid / kAcross, tid % kAcross * 8);
+    ChunkRows<WIDE> rc(p.c + seg.seq * p.cs_n + tok * p.cs_t + group * p.cs_g, p.cs_t, kRowsPerPiece, p.k, tid / kAcross, tid % kAcross * 8);
+    ChunkRows<WIDE> rx(p.x + seg.seq * p.xs_n + tok * p.xs_t + head * p.xs_h + p0, p.xs_t, 32, pcount, lane >> 1, (lane & 1) * 8);
+    ChunkRows<WIDE> rz(p.z + seg.seq * p.zs_n + tok * p.zs_t + head * p.zs_h + p0, p.zs_t, 16, pcount, r, 4 * g);
+    ChunkRows<WIDE> ro(p.out + seg.seq * p.os_n + tok * p.os_t + head * p.os_h + p0, p.os_t, 16, pcount, r, 4 * g);
     const float skip = OUT && p.d_skip != nullptr ? p.d_skip[head] : 0.0f;
     const bool gated = p.z != nullptr;
 
@@ -386,13 +389,13 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
     // one of two paths loads are waited for where the paths join.
     uint32_t nb[kPieces][4], nc[kPieces][4], nx[4], zv[2][2];
     auto fetch_bc = [&](int left) {
-        const int n = max(min(left, kChunk), 0), i = here(tid);
-        rb.begin(n, i / kAcross, i % kAcross * 8);
+        const int n = max(min(left, kChunk), 0);
+        rb.begin(n);
 #pragma unroll
         for (int q = 0; q < kPieces; ++q) rb.template load<8>(nb[q], q);
         rb.advance();
         if (OUT) {
-            rc.begin(n, i / kAcross, i % kAcross * 8);
+            rc.begin(n);
 #pragma unroll
             for (int q = 0; q < kPieces; ++q) rc.template load<8>(nc[q], q);
             rc.advance();
@@ -410,16 +413,14 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
         }
     };
     auto fetch_x = [&](int left) {
-        const int l = here(lane);
-        rx.begin(max(min(left, kChunk), 0), l >> 1, (l & 1) * 8);
+        rx.begin(max(min(left, kChunk), 0));
         rx.template load<8>(nx, 0);
         rx.advance();
     };
     auto stage_x = [&]() { *reinterpret_cast<u32x4 *>(sx + lane * 8) = u32x4{nx[0], nx[1], nx[2], nx[3]}; };
     auto fetch_z = [&](int left) {
         if (!OUT || !gated) return;
-        const int l = here(lane);
-        rz.begin(max(min(left, kChunk), 0), l & 15, l >> 4 << 2);
+        rz.begin(max(min(left, kChunk), 0));
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) rz.template load<4>(zv[tt], tt);
         rz.advance();
@@ -466,32 +467,49 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
         const uint16_t *bm = sb + slot2 * kChunk * kPitch, *cm = sc + slot2 * kChunk * kPitch;
         const float *st = steps + slot2 * plan.heads * kStepRows * kChunk;
         const uint16_t *ca = cm + r * kPitch + 8 * g;
+        // (reads ahead of the products that use them: left to itself the compiler waits for
+        // each read behind the product before)
+        u32x4 cf[kSteps][2];
+        float e[2];
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) y[tt] = f32x4_t{0, 0, 0, 0};
+        for (int m = 0; m < kSteps; ++m)
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) cf[m][tt] = lds16(ca + 16 * tt * kPitch + 32 * m);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            e[tt] = st[(head_slot * kStepRows + 3) * kChunk + 16 * tt + r];
+            y[tt] = f32x4_t{0, 0, 0, 0};
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int m = 0; m < kSteps; ++m) {
             const f32x4_t h0 = hs[2 * m], h1 = hs[2 * m + 1];
             const u32x4 hb = {pack_bf16x2(h0[0], h0[1]), pack_bf16x2(h0[2], h0[3]), pack_bf16x2(h1[0], h1[1]),
                               pack_bf16x2(h1[2], h1[3])};
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) y[tt] = mfma(hb, lds16(ca + 16 * tt * kPitch + 32 * m), y[tt]);
+            for (int tt = 0; tt < 2; ++tt) y[tt] = mfma(hb, cf[m][tt], y[tt]);
         }
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) y[tt] *= st[(head_slot * kStepRows + 3) * kChunk + 16 * tt + r];
+        for (int tt = 0; tt < 2; ++tt) y[tt] *= e[tt];
 
         for (int it = wave; it < 3 * heads; it += kScanWaves) {
             const int hd = it / 3, e = it - 3 * hd;
             const int tt = e > 0, ut = e > 1;
             f32x4_t acc = {0, 0, 0, 0};
+            u32x4 bf[kSteps], cf[kSteps];
 #pragma unroll
-            for (int m = 0; m < kSteps; ++m)
-                acc = mfma(lds16(bm + (16 * ut + r) * kPitch + 32 * m + 8 * g),
-                           lds16(cm + (16 * tt + r) * kPitch + 32 * m + 8 * g), acc);
+            for (int m = 0; m < kSteps; ++m) {
+                bf[m] = lds16(bm + (16 * ut + r) * kPitch + 32 * m + 8 * g);
+                cf[m] = lds16(cm + (16 * tt + r) * kPitch + 32 * m + 8 * g);
+            }
             const int t = 16 * tt + r, u0 = 16 * ut + 4 * g;
             const float *sh = st + hd * kStepRows * kChunk;
             const f32x4_t cu = *reinterpret_cast<const f32x4_t *>(sh + u0);
             const f32x4_t du = *reinterpret_cast<const f32x4_t *>(sh + kChunk + u0);
             const float ct = sh[t];
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < kSteps; ++m) acc = mfma(bf[m], cf[m], acc);
             float v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -507,6 +525,24 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
         const uint16_t *pm = sp + head_slot * kChunk * kPPitch;
         const float *ss = steps + (slot2 * plan.heads + head_slot) * kStepRows * kChunk;
         u32x4 xf = load_columns(sx + (4 * g + (r >> 2)) * kUnitP + 4 * (r & 3), kUnitP);
+        u32x4 pf[2];
+        u32x2 xv[2];
+        if (OUT) {
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                pf[tt] = lds16(pm + (16 * tt + r) * kPPitch + 8 * g);
+                xv[tt] = *reinterpret_cast<const u32x2 *>(sx + (16 * tt + r) * kUnitP + 4 * g);
+            }
+        }
+        const f32x4_t w0 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 4 * g);
+        const f32x4_t w1 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 16 + 4 * g);
+        const float dec = ss[3 * kChunk + kChunk - 1];
+        const uint16_t *ba = bm + (4 * g + (r >> 2)) * kPitch + 8 * (r & 3);
+        constexpr int kAhead = 8;  // tiles of B read at a time
+        u32x4 bt[kAhead];
+#pragma unroll
+        for (int m = 0; m < kAhead && m < kTiles; ++m) bt[m] = load_columns(ba + 32 * (m >> 1) + 4 * (m & 1), kPitch);
+        __builtin_amdgcn_sched_barrier(0);
         // An infinity or NaN of a later token must not meet the zeros of L: it is taken
         // out of the matrix products and its terms are added one by one.
         float probe = 0.0f;
@@ -519,7 +555,7 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
         }
         if constexpr (OUT) {
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) y[tt] = mfma(xf, lds16(pm + (16 * tt + r) * kPPitch + 8 * g), y[tt]);
+            for (int tt = 0; tt < 2; ++tt) y[tt] = mfma(xf, pf[tt], y[tt]);
             if (bad) {
                 const int rr = here(r), gg = here(g);
 #pragma unroll
@@ -533,9 +569,6 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
                         }
             }
         }
-        const f32x4_t w0 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 4 * g);
-        const f32x4_t w1 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 16 + 4 * g);
-        const float dec = ss[3 * kChunk + kChunk - 1];
         u32x4 xw[SPLIT];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -549,13 +582,19 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
                 v1 -= hi_f32(h);
             }
         }
-        const uint16_t *ba = bm + (4 * g + (r >> 2)) * kPitch + 8 * (r & 3);
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-            const u32x4 bt = load_columns(ba + 32 * (m >> 1) + 4 * (m & 1), kPitch);
-            hs[m] *= dec;
+        for (int m0 = 0; m0 < kTiles; m0 += kAhead) {
+            if (m0 > 0) {
 #pragma unroll
-            for (int part = SPLIT - 1; part >= 0; --part) hs[m] = mfma(bt, xw[part], hs[m]);
+                for (int m = 0; m < kAhead; ++m) bt[m] = load_columns(ba + 32 * ((m0 + m) >> 1) + 4 * (m & 1), kPitch);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int m = m0; m < m0 + kAhead && m < kTiles; ++m) {
+                hs[m] *= dec;
+#pragma unroll
+                for (int part = SPLIT - 1; part >= 0; --part) hs[m] = mfma(bt[m - m0], xw[part], hs[m]);
+            }
         }
         if (bad) {
             const int rr = here(r), gg = here(g);
@@ -571,15 +610,13 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
         }
         // skip, gate and store: four consecutive p of a token a lane
         if constexpr (OUT) {
-            const int l = here(lane);
-            ro.begin(rows, l & 15, l >> 4 << 2);
+            ro.begin(rows);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
-                const u32x2 xv = *reinterpret_cast<const u32x2 *>(sx + (16 * tt + r) * kUnitP + 4 * g);
                 float o[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    o[i] = __builtin_fmaf(skip, (i & 1) ? hi_f32(xv[i >> 1]) : lo_f32(xv[i >> 1]), y[tt][i]);
+                    o[i] = __builtin_fmaf(skip, (i & 1) ? hi_f32(xv[tt][i >> 1]) : lo_f32(xv[tt][i >> 1]), y[tt][i]);
                 if (gated) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[i] *= silu((i & 1) ? hi_f32(zv[tt][i >> 1]) : lo_f32(zv[tt][i >> 1]));
@@ -641,34 +678,51 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
 }
 
 // The states ahead of every segment, in place: position u + 1 of the workspace
-// holds what segment u built up from zero and its decay.
-__global__ __launch_bounds__(256) void selective_join_kernel(const SelectiveScanParams p, const ScanPlan plan,
-                                                             int blocks_per_seq) {
-    const int64_t hpk = (int64_t)p.h * p.p * p.k;
+// holds what segment u built up from zero and its decay.  A thread carries VEC
+// neighbouring values along a sequence's segments.
+constexpr int kJoinBlock = 256;
+template <int VEC>
+__global__ __launch_bounds__(kJoinBlock) void selective_join_kernel(const SelectiveScanParams p, const ScanPlan plan,
+                                                                    int blocks_per_seq) {
+    const int64_t hpk = (int64_t)p.h * p.p * p.k, pk = (int64_t)p.p * p.k;
     for_each_unit((int64_t)p.n * blocks_per_seq, [&](int64_t unit) {
-        const int seq = (int)(unit / blocks_per_seq);
-        const int64_t e = (unit % blocks_per_seq) * 256 + threadIdx.x;
-        int u0 = seq * plan.nseg;
+        const int seq = uniform((int)(unit / blocks_per_seq)), part = (int)(unit - (int64_t)seq * blocks_per_seq);
+        int first = 0, len = p.t, u0 = seq * plan.nseg;
         if (p.starts != nullptr) {
-            const int a = load_uniform(p.starts, seq);
-            if (a < 0 || a > p.t) return;
-            u0 = a / plan.seg + seq;
+            first = load_uniform(p.starts, seq);
+            const int end = load_uniform(p.starts, seq + 1);
+            if (first < 0 || first > end || end > p.t) return;
+            len = end - first;
+            u0 = first / plan.seg + seq;
         }
-        const Segment seg = find_segment(p, plan, u0);
-        if (!seg.ok || seg.seq != seq || seg.count < 2) return;
+        if (len <= plan.seg) return;  // one segment
+        const int count = (len - 1) / plan.seg + 1;
         const int slot = route_row(p.idx, nullptr, p.n, p.s, seq, threadIdx.x & 63);
-        if (e >= hpk) return;
-        const int head = (int)(e / ((int64_t)p.p * p.k));
-        float run = 0.0f;
-        if (slot >= 0 && p.state != nullptr && p.has_init != nullptr && p.has_init[seq] != 0)
-            run = p.state_f32 ? static_cast<const float *>(p.state)[slot * p.ss_s + e]
-                              : bf16_bits_to_f32(static_cast<const uint16_t *>(p.state)[slot * p.ss_s + e]);
-        float *ws = p.workspace + u0 * hpk + e;
-        const float *dec = p.workspace + plan.slots * hpk + (int64_t)u0 * p.h + head;
-        ws[0] = run;
-        for (int j = 1; j < seg.count; ++j) {
-            run = __builtin_fmaf(run, dec[(int64_t)j * p.h], ws[j * hpk]);
-            ws[j * hpk] = run;
+        const bool init = slot >= 0 && p.state != nullptr && p.has_init != nullptr && p.has_init[seq] != 0;
+        for (int64_t e = ((int64_t)part * kJoinBlock + threadIdx.x) * VEC; e < hpk;
+             e += (int64_t)blocks_per_seq * kJoinBlock * VEC) {
+            float run[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                run[i] = !init ? 0.0f
+                         : p.state_f32 ? static_cast<const float *>(p.state)[slot * p.ss_s + e + i]
+                                       : bf16_bits_to_f32(static_cast<const uint16_t *>(p.state)[slot * p.ss_s + e + i]);
+            typedef float fvec __attribute__((ext_vector_type(VEC)));
+            fvec *ws = reinterpret_cast<fvec *>(p.workspace + u0 * hpk + e);
+            const float *dec = p.workspace + plan.slots * hpk + (int64_t)u0 * p.h + e / pk;
+#pragma unroll 4
+            for (int j = 0; j < count; ++j) {
+                fvec v;
+                if (j > 0) {
+                    v = ws[j * (hpk / VEC)];
+                    const float d = dec[(int64_t)j * p.h];
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) run[i] = __builtin_fmaf(run[i], d, v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[i] = run[i];
+                ws[j * (hpk / VEC)] = v;
+            }
         }
     });
 }
@@ -682,6 +736,8 @@ constexpr int64_t kFullGrid = 768;
 constexpr int64_t kEnoughBlocks = 256;
 constexpr int64_t kMinSegment = 256;
 constexpr int64_t kLongSequence = 2048;
+constexpr int64_t kRuns = 32;
+constexpr int64_t kJoinBlocks = 2048;  // of the join, over all sequences
 
 ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, bool packed) {
     ScanPlan plan;
@@ -706,6 +762,11 @@ ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, bool p
     plan.nseg = (int32_t)(t > 0 ? (t + seg - 1) / seg : 1);
     plan.split = plan.nseg > 1;
     plan.slots = (int32_t)(packed ? t / seg + n : n * plan.nseg);
+    // the longest runs of which there are still kRuns (of equal length: packed
+    // sequences would leave some XCDs with more to do than others)
+    const int64_t run = packed ? 1 : plan.slots * per_slot / kRuns;
+    plan.run = (int32_t)(run < 1 ? 1 : run > plan.quads ? plan.quads : run);
+    plan.parts = (plan.quads + plan.run - 1) / plan.run;
     return plan;
 }
 
@@ -727,7 +788,7 @@ uint64_t lds_allowed = 0;
 
 template <int KS, int SPLIT, bool OUT, bool WIDE>
 hipError_t launch_pass(const SelectiveScanParams &p, const ScanPlan &plan, hipStream_t stream) {
-    const int64_t units = (int64_t)plan.slots * p.g * plan.quads;
+    const int64_t units = ((int64_t)plan.slots * p.g * plan.parts + 7) / 8 * 8 * plan.run;
     const size_t lds = (size_t)(OUT ? 4 : 2) * kChunk * (KS + 16) * 2 + (size_t)kScanWaves * kChunk * kUnitP * 2 +
                        (size_t)2 * plan.heads * kStepRows * kChunk * 4 +
                        (OUT ? (size_t)plan.heads * kChunk * kPPitch * 2 : 0);
@@ -745,9 +806,15 @@ hipError_t launch_passes(const SelectiveScanParams &p, const ScanPlan &plan, hip
     if (plan.split) {
         hipError_t err = launch_pass<KS, SPLIT, false, WIDE>(p, plan, stream);
         if (err != hipSuccess) return err;
-        const int64_t per_seq = ((int64_t)p.h * p.p * p.k + 255) / 256, units = per_seq * p.n;
-        selective_join_kernel<<<dim3((unsigned)(units < kMaxBlocks ? units : kMaxBlocks)), 256, 0, stream>>>(
-            p, plan, (int)per_seq);
+        const bool vec = (int64_t)p.p * p.k % 4 == 0;
+        const int64_t need = ((int64_t)p.h * p.p * p.k / (vec ? 4 : 1) + kJoinBlock - 1) / kJoinBlock;
+        const int64_t spread = p.n < kJoinBlocks ? kJoinBlocks / p.n : 1, per_seq = need < spread ? need : spread;
+        const int64_t units = per_seq * p.n;
+        const dim3 grid((unsigned)(units < kMaxBlocks ? units : kMaxBlocks));
+        if (vec)
+            selective_join_kernel<4><<<grid, kJoinBlock, 0, stream>>>(p, plan, (int)per_seq);
+        else
+            selective_join_kernel<1><<<grid, kJoinBlock, 0, stream>>>(p, plan, (int)per_seq);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
