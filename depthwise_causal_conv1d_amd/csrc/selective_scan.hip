@@ -59,7 +59,9 @@ constexpr int kChunk = 32;
 constexpr int kScanWaves = 4;
 constexpr int kScanBlock = kWave * kScanWaves;
 constexpr int kUnitP = 16;           // p of a wave
-constexpr int kPPitch = kChunk + 16;  // LDS row pitch of L o C B^T
+constexpr int kBlockP = kScanWaves * kUnitP;  // p of a block
+constexpr int kPPitch = kChunk + 16;   // LDS row pitches of L o C B^T,
+constexpr int kXPitch = kBlockP + 8;   // and of x and z
 constexpr int kStepRows = 4;         // per token and head: c, d, the weight into H, e^c
 
 // How a call is cut up; the same on the host and in every kernel.
@@ -189,54 +191,53 @@ __device__ __forceinline__ void wave_sums(float v, int lane, float *upto, float 
 
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer
 
-// One operand's rows of a chunk, `stride` elements apart: a lane moves a few values
-// from column `col` on (there are `width`) of rows row0, row0 + step, ...  WIDE moves
-// them at once through a buffer that ends with the chunk's last row, so that what lies
+// One operand's rows of a chunk, `stride` elements apart and `width` long: a lane moves
+// eight values, of which `count` exist, from column `col` of rows row0, row0 + step, ...
+// WIDE moves them at once (16 bytes) through a buffer that ends with the chunk's last row, so that what lies
 // behind it reads as zeros and is not written.
 template <bool WIDE>
 struct ChunkRows {
     const uint16_t *base;  // wave-uniform: the chunk's first row
     int64_t stride;
-    int32_t step, width, row0, col, rows;
-    uint32_t at0, hop;
+    int32_t step, row0, count, rows;
+    uint32_t at0, hop, width;
     Buffer buf;
-    __device__ __forceinline__ ChunkRows(const uint16_t *first, int64_t stride, int step, int width, int row, int col)
-        : base(first), stride(stride), step(step), width(width), row0(row), col(col) {
+    __device__ __forceinline__ ChunkRows(const uint16_t *first, int64_t stride, int step, int64_t width, int row,
+                                         int64_t col, int count)
+        : base(first), stride(stride), step(step), row0(row), count(count), width(2u * (uint32_t)width) {
         const uint32_t bytes = 2u * (uint32_t)stride;
-        at0 = col < width ? (uint32_t)row * bytes + 2u * (uint32_t)col : kNowhere;
+        at0 = WIDE ? (count > 0 ? (uint32_t)row * bytes + 2u * (uint32_t)col : kNowhere) : (uint32_t)col;
         hop = (uint32_t)step * bytes;
     }
     __device__ __forceinline__ void begin(int n) {
         rows = n;
-        if (WIDE) buf = make_buffer(base, n > 0 ? (uint32_t)(n - 1) * 2u * (uint32_t)stride + 2u * (uint32_t)width : 0u);
+        if (WIDE) buf = make_buffer(base, n > 0 ? (uint32_t)(n - 1) * 2u * (uint32_t)stride + width : 0u);
     }
     __device__ __forceinline__ void advance() { base += kChunk * stride; }
-    // N values (8 or 4) of row row0 + q * step
-    template <int N>
-    __device__ __forceinline__ void load(uint32_t (&w)[N / 2], int q) const {
+    // eight values of row row0 + q * step
+    __device__ __forceinline__ void load(uint32_t (&w)[4], int q) const {
         if (WIDE) {
-            buffer_load_words<N / 2, kCached>(buf, at0 + (uint32_t)q * hop, w);
+            buffer_load_words<4, kCached>(buf, row0 + q * step < rows ? at0 + (uint32_t)q * hop : kNowhere, w);
             return;
         }
         const int row = row0 + q * step;
-        const uint16_t *from = base + row * stride + col;
+        const uint16_t *from = base + row * stride + at0;
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) w[i] = 0;
+        for (int i = 0; i < 4; ++i) w[i] = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (row < rows && col + i < width) w[i >> 1] |= (uint32_t)from[i] << (16 * (i & 1));
+        for (int i = 0; i < 8; ++i)
+            if (row < rows && i < count) w[i >> 1] |= (uint32_t)from[i] << (16 * (i & 1));
     }
-    __device__ __forceinline__ void store(uint32_t (&w)[2], int q) const {
+    __device__ __forceinline__ void store(uint32_t (&w)[4]) const {
         if (WIDE) {
-            buffer_store_words<2, kCached>(w, buf, at0 + (uint32_t)q * hop);
+            buffer_store_words<4, kCached>(w, buf, row0 < rows ? at0 : kNowhere);
             return;
         }
-        const int row = row0 + q * step;
-        if (row >= rows) return;
-        uint16_t *to = const_cast<uint16_t *>(base) + row * stride + col;
+        if (row0 >= rows) return;
+        uint16_t *to = const_cast<uint16_t *>(base) + row0 * stride + at0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (col + i < width) to[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+        for (int i = 0; i < 8; ++i)
+            if (i < count) to[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
     }
 };
 
@@ -310,13 +311,15 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
     extern __shared__ u32x4 smem[];
     uint16_t *sb = reinterpret_cast<uint16_t *>(smem);            // [2][kChunk][kPitch]
     uint16_t *sc = sb + 2 * kChunk * kPitch;                      // [2][kChunk][kPitch]
-    uint16_t *sx_all = sc + (OUT ? 2 * kChunk * kPitch : 0);      // [wave][kChunk][kUnitP]
-    float *steps = reinterpret_cast<float *>(sx_all + kScanWaves * kChunk * kUnitP);  // [2][heads][kStepRows][kChunk]
+    uint16_t *sx_all = sc + (OUT ? 2 * kChunk * kPitch : 0);      // [kChunk][kXPitch]
+    uint16_t *sz_all = sx_all + kChunk * kXPitch;                 // likewise: z, and then the outputs
+    float *steps = reinterpret_cast<float *>(sz_all + (OUT ? kChunk * kXPitch : 0));  // [2][heads][kStepRows][kChunk]
     uint16_t *sp = reinterpret_cast<uint16_t *>(steps + 2 * plan.heads * kStepRows * kChunk);  // [heads][kChunk][kPPitch]
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    uint16_t *sx = sx_all + wave * kChunk * kUnitP;
+    const uint16_t *sx = sx_all + wave * kUnitP;
+    uint16_t *sz = sz_all + wave * kUnitP;
     const int per_group = uniform(p.h / p.g), units = per_group * plan.np;
 
     if (OUT && blockIdx.x == 0 && blockIdx.y == 0) check_table(p);
@@ -374,30 +377,41 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
                 hs[m] = load_state4(src, f32, wide, at + column(m, g), p.k - column(m, g));
     }
 
-    // ---- the operands' rows: B and C shared out over the block, the rest a wave's own
+    // ---- the operands' rows, shared out over the block.  Eight threads move the 64
+    // channels of a token that the block's waves own, two for a wave's 16.
     const int64_t tok = (int64_t)seg.token0 + seg.first;
     constexpr int kRowsPerPiece = kScanBlock / kAcross;
-    ChunkRows<WIDE> rb(p.b + seg.seq * p.bs_n + tok * p.bs_t + group * p.bs_g, p.bs_t, kRowsPerPiece, p.k, tid / kAcross, tid % kAcross * 8);
-    ChunkRows<WIDE> rc(p.c + seg.seq * p.cs_n + tok * p.cs_t + group * p.cs_g, p.cs_t, kRowsPerPiece, p.k, tid / kAcross, tid % kAcross * 8);
-    ChunkRows<WIDE> rx(p.x + seg.seq * p.xs_n + tok * p.xs_t + head * p.xs_h + p0, p.xs_t, 32, pcount, lane >> 1, (lane & 1) * 8);
-    ChunkRows<WIDE> rz(p.z + seg.seq * p.zs_n + tok * p.zs_t + head * p.zs_h + p0, p.zs_t, 16, pcount, r, 4 * g);
-    ChunkRows<WIDE> ro(p.out + seg.seq * p.os_n + tok * p.os_t + head * p.os_h + p0, p.os_t, 16, pcount, r, 4 * g);
+    ChunkRows<WIDE> rb(p.b + seg.seq * p.bs_n + tok * p.bs_t + group * p.bs_g, p.bs_t, kRowsPerPiece, p.k, tid / kAcross,
+                       tid % kAcross * 8, p.k - tid % kAcross * 8);
+    ChunkRows<WIDE> rc(p.c + seg.seq * p.cs_n + tok * p.cs_t + group * p.cs_g, p.cs_t, kRowsPerPiece, p.k, tid / kAcross,
+                       tid % kAcross * 8, p.k - tid % kAcross * 8);
+    constexpr int kMoves = kBlockP / 8;
+    const int move_row = tid / kMoves, move_col = tid % kMoves * 8;
+    const int theirs = min(quad * kScanWaves + move_col / kUnitP, last_unit), their_head = theirs / plan.np;
+    const int their_p = (theirs - their_head * plan.np) * kUnitP + move_col % kUnitP;
+    const int their_count = quad * kScanWaves + move_col / kUnitP == theirs ? max(p.p - their_p, 0) : 0;
+    const auto mover = [&](const uint16_t *base, int64_t sn, int64_t st, int64_t sh) {
+        return ChunkRows<WIDE>(base + seg.seq * sn + tok * st + group * per_group * sh, st, kChunk,
+                               (per_group - 1) * sh + p.p, move_row, their_head * sh + their_p, their_count);
+    };
+    ChunkRows<WIDE> rx = mover(p.x, p.xs_n, p.xs_t, p.xs_h), rz = mover(p.z, p.zs_n, p.zs_t, p.zs_h);
+    ChunkRows<WIDE> ro = mover(p.out, p.os_n, p.os_t, p.os_h);
     const float skip = OUT && p.d_skip != nullptr ? p.d_skip[head] : 0.0f;
     const bool gated = p.z != nullptr;
 
     // Every fetch is unconditional (of no rows behind the last chunk): registers that only
     // one of two paths loads are waited for where the paths join.
-    uint32_t nb[kPieces][4], nc[kPieces][4], nx[4], zv[2][2];
+    uint32_t nb[kPieces][4], nc[kPieces][4], nx[4], nz[4];
     auto fetch_bc = [&](int left) {
         const int n = max(min(left, kChunk), 0);
         rb.begin(n);
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) rb.template load<8>(nb[q], q);
+        for (int q = 0; q < kPieces; ++q) rb.load(nb[q], q);
         rb.advance();
         if (OUT) {
             rc.begin(n);
 #pragma unroll
-            for (int q = 0; q < kPieces; ++q) rc.template load<8>(nc[q], q);
+            for (int q = 0; q < kPieces; ++q) rc.load(nc[q], q);
             rc.advance();
         }
     };
@@ -414,16 +428,30 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
     };
     auto fetch_x = [&](int left) {
         rx.begin(max(min(left, kChunk), 0));
-        rx.template load<8>(nx, 0);
+        rx.load(nx, 0);
         rx.advance();
     };
-    auto stage_x = [&]() { *reinterpret_cast<u32x4 *>(sx + lane * 8) = u32x4{nx[0], nx[1], nx[2], nx[3]}; };
+    auto stage_x = [&]() {
+        *reinterpret_cast<u32x4 *>(sx_all + move_row * kXPitch + move_col) = u32x4{nx[0], nx[1], nx[2], nx[3]};
+    };
     auto fetch_z = [&](int left) {
         if (!OUT || !gated) return;
         rz.begin(max(min(left, kChunk), 0));
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) rz.template load<4>(zv[tt], tt);
+        rz.load(nz, 0);
         rz.advance();
+    };
+    auto stage_z = [&]() {
+        if (OUT && gated)
+            *reinterpret_cast<u32x4 *>(sz_all + move_row * kXPitch + move_col) = u32x4{nz[0], nz[1], nz[2], nz[3]};
+    };
+    // the outputs that the waves have left in place of z
+    auto put_out = [&](int rows) {
+        if (!OUT) return;
+        const u32x4 v = lds16(sz_all + move_row * kXPitch + move_col);
+        uint32_t w[4] = {v[0], v[1], v[2], v[3]};
+        ro.begin(rows);
+        ro.store(w);
+        ro.advance();
     };
 
     // ---- the steps of a head's chunk: the last waves (which have the fewest tiles of
@@ -520,18 +548,19 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
     };
 
     // ---- the second half: y += (L o C B^T) X, H' = e^{c_Q} H + (scaled x)^T B, and the outputs
-    auto finish = [&](int rows, int slot2) {
+    auto finish = [&](int slot2) {
         const uint16_t *bm = sb + slot2 * kChunk * kPitch;
         const uint16_t *pm = sp + head_slot * kChunk * kPPitch;
         const float *ss = steps + (slot2 * plan.heads + head_slot) * kStepRows * kChunk;
-        u32x4 xf = load_columns(sx + (4 * g + (r >> 2)) * kUnitP + 4 * (r & 3), kUnitP);
+        u32x4 xf = load_columns(sx + (4 * g + (r >> 2)) * kXPitch + 4 * (r & 3), kXPitch);
         u32x4 pf[2];
-        u32x2 xv[2];
+        u32x2 xv[2], zv[2];
         if (OUT) {
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 pf[tt] = lds16(pm + (16 * tt + r) * kPPitch + 8 * g);
-                xv[tt] = *reinterpret_cast<const u32x2 *>(sx + (16 * tt + r) * kUnitP + 4 * g);
+                xv[tt] = *reinterpret_cast<const u32x2 *>(sx + (16 * tt + r) * kXPitch + 4 * g);
+                zv[tt] = *reinterpret_cast<const u32x2 *>(sz + (16 * tt + r) * kXPitch + 4 * g);
             }
         }
         const f32x4_t w0 = *reinterpret_cast<const f32x4_t *>(ss + 2 * kChunk + 4 * g);
@@ -563,7 +592,7 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
                     for (int q = 0; q <= 16 * tt + rr; ++q)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float v = bf16_bits_to_f32(sx[q * kUnitP + 4 * gg + i]);
+                            const float v = bf16_bits_to_f32(sx[q * kXPitch + 4 * gg + i]);
                             if (!is_finite(v))
                                 y[tt][i] += bf16_bits_to_f32(pm[(16 * tt + rr) * kPPitch + 2 * (q & 12) + ((q & 16) >> 2) + (q & 3)]) * v;
                         }
@@ -599,7 +628,7 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
         if (bad) {
             const int rr = here(r), gg = here(g);
             for (int q = 0; q < kChunk; ++q) {
-                const float v = bf16_bits_to_f32(sx[q * kUnitP + rr]);
+                const float v = bf16_bits_to_f32(sx[q * kXPitch + rr]);
                 if (is_finite(v)) continue;
                 const float w = ss[2 * kChunk + q] * v;
 #pragma unroll
@@ -608,9 +637,8 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
                     for (int i = 0; i < 4; ++i) hs[m][i] += w * bf16_bits_to_f32(bm[q * kPitch + column(m, gg) + i]);
             }
         }
-        // skip, gate and store: four consecutive p of a token a lane
+        // skip and gate: four consecutive p of a token a lane, left in LDS where its z was
         if constexpr (OUT) {
-            ro.begin(rows);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 float o[4];
@@ -621,10 +649,9 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[i] *= silu((i & 1) ? hi_f32(zv[tt][i >> 1]) : lo_f32(zv[tt][i >> 1]));
                 }
-                uint32_t ov[2] = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
-                ro.store(ov, tt);
+                *reinterpret_cast<u32x2 *>(sz + (16 * tt + r) * kXPitch + 4 * g) =
+                    u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
             }
-            ro.advance();
         }
     };
 
@@ -637,8 +664,10 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
         if (has_job) put_steps(step0, left, 0);
         stage_bc(0);
         stage_x();
+        stage_z();
         fetch_bc(left - kChunk);
         fetch_x(left - kChunk);
+        fetch_z(left - kChunk);
         if (has_job) put_steps(step1, left - kChunk, 1);
     }
     uint32_t step = fetch_step(left - 2 * kChunk);
@@ -648,12 +677,14 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
     fetch_bc(left - 2 * kChunk);
     __syncthreads();
     for (int b = 0; left > 0; left -= kChunk, b ^= 1) {
-        finish(min(left, kChunk), b);
-        stage_x();
+        finish(b);
+        __syncthreads();  // chunk i's places are free
+        put_out(min(left, kChunk));
+        stage_x();  // of chunk i + 1
+        stage_z();
+        stage_bc(b);  // of chunk i + 2
         fetch_x(left - 2 * kChunk);
-        fetch_z(left - kChunk);
-        __syncthreads();  // chunk i's places are free for chunk i + 2
-        stage_bc(b);
+        fetch_z(left - 2 * kChunk);
         fetch_bc(left - 3 * kChunk);
         if constexpr (OUT) start(b ^ 1);
         if (has_job) put_steps(step, left - 2 * kChunk, b);
@@ -789,7 +820,7 @@ uint64_t lds_allowed = 0;
 template <int KS, int SPLIT, bool OUT, bool WIDE>
 hipError_t launch_pass(const SelectiveScanParams &p, const ScanPlan &plan, hipStream_t stream) {
     const int64_t units = ((int64_t)plan.slots * p.g * plan.parts + 7) / 8 * 8 * plan.run;
-    const size_t lds = (size_t)(OUT ? 4 : 2) * kChunk * (KS + 16) * 2 + (size_t)kScanWaves * kChunk * kUnitP * 2 +
+    const size_t lds = (size_t)(OUT ? 4 : 2) * kChunk * (KS + 16) * 2 + (size_t)(OUT ? 2 : 1) * kChunk * kXPitch * 2 +
                        (size_t)2 * plan.heads * kStepRows * kChunk * 4 +
                        (OUT ? (size_t)plan.heads * kChunk * kPPitch * 2 : 0);
     auto kernel = selective_scan_kernel<KS, SPLIT, OUT, WIDE>;
@@ -828,10 +859,11 @@ hipError_t launch_ks(const SelectiveScanParams &p, const ScanPlan &plan, bool wi
     return exact ? launch_passes<KS, 3, false>(p, plan, stream) : launch_passes<KS, 1, false>(p, plan, stream);
 }
 
-// Whether rows at p with the given element strides start on 16 bytes,
-// and 64 of them (b elements apart) span less than 2^31 bytes.
-bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0 && b < (1 << 23);
+// Whether rows at p with the given element strides start on 16 bytes, and 32 tokens
+// (b elements apart) of `heads` heads (c apart) span less than 2^31 bytes.
+bool rows16(const void *p, int64_t a, int64_t b, int64_t c, int64_t heads) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0 && b < (1 << 23) &&
+           c < (1 << 28) / heads;
 }
 
 }  // namespace
@@ -843,10 +875,11 @@ int64_t selective_scan_workspace_floats(int64_t n, int64_t t, int64_t h, int64_t
 
 hipError_t launch_selective_scan(const SelectiveScanParams &p, hipStream_t stream, const char **kernel_name) {
     const ScanPlan plan = make_plan(p.n, p.t, p.h, p.p, p.g, p.starts != nullptr);
-    const bool wide = p.p % 8 == 0 && p.k % 8 == 0 && rows16(p.x, p.xs_n, p.xs_t, p.xs_h) &&
-                      rows16(p.b, p.bs_n, p.bs_t, p.bs_g) && rows16(p.c, p.cs_n, p.cs_t, p.cs_g) &&
-                      (p.z == nullptr || rows16(p.z, p.zs_n, p.zs_t, p.zs_h)) &&
-                      rows16(p.out, p.os_n, p.os_t, p.os_h);
+    const int64_t heads = p.h / p.g;
+    const bool wide = p.p % 8 == 0 && p.k % 8 == 0 && rows16(p.x, p.xs_n, p.xs_t, p.xs_h, heads) &&
+                      rows16(p.b, p.bs_n, p.bs_t, p.bs_g, 1) && rows16(p.c, p.cs_n, p.cs_t, p.cs_g, 1) &&
+                      (p.z == nullptr || rows16(p.z, p.zs_n, p.zs_t, p.zs_h, heads)) &&
+                      rows16(p.out, p.os_n, p.os_t, p.os_h, heads);
     *kernel_name = plan.split ? (wide ? "selective_scan_split" : "selective_scan_split_scalar")
                               : (wide ? "selective_scan" : "selective_scan_scalar");
     if (p.k <= 64) return launch_ks<64>(p, plan, wide, stream);

@@ -166,6 +166,23 @@ def test_scan_of_strided_and_unaligned_views():
     Scan(11, [100], 4, 64, 2, 128, state=torch.bfloat16, place=off).check()
 
 
+def test_scan_of_head_major_and_broadcast_operands():
+    """Heads further apart than tokens, so that a row past the end is another head's; and
+    rows that are one and the same."""
+    def head_major(t):
+        t = t.cuda()
+        return t.transpose(1, 2).contiguous().transpose(1, 2) if t.dim() == 4 else t
+    case = Scan(18, [75, 75], 6, 64, 2, 64, state=torch.float32, place=head_major)
+    buf = torch.full((2, 6, 90, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    case.check(out=buf[:, :, 5:80].transpose(1, 2))
+    assert bool((buf[:, :, :5] == 7).all() and (buf[:, :, 80:] == 7).all())
+    case = Scan(19, [75, 75], 4, 32, 1, 64, state=torch.float32)
+    for t in (case.x, case.z, case.B, case.C):
+        t.copy_(t[:1, :1].expand_as(t).clone())
+    case.place = lambda t: t[:1, :1].cuda().expand(t.shape) if t.dim() == 4 else t.cuda()
+    case.check()
+
+
 def test_scan_writes_only_its_output():
     case = Scan(12, [77, 77], 3, 40, 1, 24, state=torch.float32)
     buf = torch.full((2, 77, 5, 48), 7.0, dtype=torch.bfloat16, device="cuda")
