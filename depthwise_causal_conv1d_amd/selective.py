@@ -29,6 +29,21 @@ __all__ = [
 
 DCCONV_DTYPE_BF16, DCCONV_DTYPE_F32 = 0, 1
 
+_t = None  # torch, from the first call on
+
+
+def _lib():
+    """The loaded library, and torch in ``_t``."""
+    global _t
+    lib = _b.load()
+    if _t is None:
+        import torch
+
+        _b.bind_torch(torch)
+        _t = torch
+    return lib
+
+
 
 def declare(lib: ctypes.CDLL) -> None:
     """The argument types of this module's C entry points."""
@@ -106,53 +121,52 @@ def dcconv_w4_pack(*args) -> int:
 
 
 def _bf16(name, t, shape, dev):
-    """``t`` as a BF16 operand of ``shape`` whose last dimension is dense."""
-    import torch
-
-    if t.dtype is not torch.bfloat16:
+    """``t`` as a BF16 operand of ``shape`` whose last dimension is dense; its strides."""
+    if t.dtype is not _t.bfloat16:
         raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
-    _shaped(name, t, shape, dev)
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.shape != shape or t.device != dev or t.requires_grad:
+        _refuse(name, t, shape, dev)
+    stride = t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
+    return stride
 
 
 def _shaped(name, t, shape, dev):
-    if tuple(t.shape) != shape:
+    if t.shape != shape or t.device != dev or t.requires_grad:
+        _refuse(name, t, shape, dev)
+
+
+def _refuse(name, t, shape, dev):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the rest on {dev}")
-    if t.requires_grad:
-        raise NotImplementedError(f"inference only: {name} requires grad (training is not served)")
+    raise NotImplementedError(f"inference only: {name} requires grad (training is not served)")
 
 
 def _f32_vector(name, t, n, dev):
-    import torch
-
     if t is None:
         return None
-    if t.dtype is not torch.float32 or not t.is_contiguous():
+    if t.dtype is not _t.float32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 [{n}] tensor")
     _shaped(name, t, (n,), dev)
     return t.data_ptr()
 
 
 def _i32_vector(name, t, n, dev):
-    import torch
-
     if t is None:
         return None
-    if t.dtype is not torch.int32 or not t.is_contiguous():
+    if t.dtype is not _t.int32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor")
     _shaped(name, t, (n,), dev)
     return t.data_ptr()
 
 
 def _dtype(name, t):
-    import torch
-
-    if t.dtype is torch.bfloat16:
+    if t.dtype is _t.bfloat16:
         return DCCONV_DTYPE_BF16
-    if t.dtype is torch.float32:
+    if t.dtype is _t.float32:
         return DCCONV_DTYPE_F32
     raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
@@ -178,11 +192,9 @@ def _pool(state, H, P, dev, K=None):
 
 
 def _status(dev_status, dev):
-    import torch
-
     if dev_status is None:
         return None
-    if dev_status.dtype is not torch.int32 or dev_status.device != dev or dev_status.numel() < 1:
+    if dev_status.dtype is not _t.int32 or dev_status.device != dev or dev_status.numel() < 1:
         raise ValueError("dev_status must be an int32 tensor on the operands' device")
     return dev_status.data_ptr()
 
@@ -202,30 +214,24 @@ def selective_update(x, dt, A, B, C, ssm_state, *, D=None, z=None, dt_bias=None,
     [N, H]; A, D, dt_bias: float32 [H]; ssm_state: bf16 or float32 [S, H, P, K].  Any
     strides with dense last dimensions.  ``state_indices`` (int32 [N]) routes rows to
     slots, -1 being a padding row (zero output, no state moves)."""
-    import torch
-
+    lib = _lib()
     if x.dim() != 3 or B.dim() != 3:
         raise ValueError(f"x must be [N, H, P] and B [N, G, K], got {tuple(x.shape)} and {tuple(B.shape)}")
     dev = _gpu(x)
-    N, H, P = x.shape
-    G, K = B.shape[1:]
-    _bf16("x", x, (N, H, P), dev)
-    _bf16("B", B, (N, G, K), dev)
-    _bf16("C", C, (N, G, K), dev)
+    N, H, P = rows = x.shape
+    _, G, K = B.shape
+    xs = _bf16("x", x, rows, dev)
+    bs, cs = _bf16("B", B, (N, G, K), dev), _bf16("C", C, (N, G, K), dev)
     code, S, slot, _ = _pool(ssm_state, H, P, dev, K)
     dt_code = _steps(dt, (N, H), dev)
     if A is None:
         raise ValueError("A must be given")
-    if z is not None:
-        _bf16("z", z, (N, H, P), dev)
+    zs = _bf16("z", z, rows, dev) if z is not None else (0, 0)
     if out is None:
-        out = torch.empty(N, H, P, dtype=torch.bfloat16, device=dev)
-    else:
-        _bf16("out", out, (N, H, P), dev)
-    xs, bs, cs, os_ = x.stride(), B.stride(), C.stride(), out.stride()
-    zs = z.stride() if z is not None else (0, 0)
+        out = _t.empty(rows, dtype=_t.bfloat16, device=dev)
+    os_ = _bf16("out", out, rows, dev)
     with _b.on(dev) as stream:
-        rc = _b.load().dcconv_selective_update(
+        rc = lib.dcconv_selective_update(
             x.data_ptr(), N, H, P, xs[0], xs[1], dt.data_ptr(), dt_code, dt.stride(0),
             _f32_vector("dt_bias", dt_bias, H, dev), int(bool(dt_softplus)), _f32_vector("A", A, H, dev),
             B.data_ptr(), C.data_ptr(), G, K, bs[0], bs[1], cs[0], cs[1], _f32_vector("D", D, H, dev),
@@ -239,9 +245,8 @@ def selective_update(x, dt, A, B, C, ssm_state, *, D=None, z=None, dt_bias=None,
 def selective_update_workspace(rows, groups, device=None):
     """The zeroed int32 [rows * groups] counters of ``causal_conv1d_selective_update``,
     which leaves them zero: one buffer serves any number of successive calls."""
-    import torch
-
-    return torch.zeros(rows * groups, dtype=torch.int32, device="cuda" if device is None else device)
+    _lib()
+    return _t.zeros(rows * groups, dtype=_t.int32, device="cuda" if device is None else device)
 
 
 def causal_conv1d_selective_update(xbc, conv_state, weight, bias, activation, dt, A, ssm_state, *, groups,
@@ -256,8 +261,7 @@ def causal_conv1d_selective_update(xbc, conv_state, weight, bias, activation, dt
     channels are not rounded before the recurrence reads them.  ``workspace`` comes
     from ``selective_update_workspace`` (allocated and zeroed here if None).  The rest
     as for ``selective_update``."""
-    import torch
-
+    lib = _lib()
     if xbc.dim() != 2 or ssm_state.dim() != 4 or conv_state.dim() != 3 or weight.dim() != 2:
         raise ValueError(f"xbc must be [N, Dc], conv_state [S, Dc, L], weight [Dc, W] and ssm_state [S, H, P, K], got "
                          f"{tuple(xbc.shape)}, {tuple(conv_state.shape)}, {tuple(weight.shape)}, "
@@ -268,7 +272,7 @@ def causal_conv1d_selective_update(xbc, conv_state, weight, bias, activation, dt
     code, S, slot, _ = _pool(ssm_state, H, P, dev)
     Dc = H * P + 2 * groups * K
     _bf16("xbc", xbc, (N, Dc), dev)
-    if conv_state.dtype is not torch.bfloat16:
+    if conv_state.dtype is not _t.bfloat16:
         raise ValueError(f"conv_state must be bfloat16, got {conv_state.dtype}")
     _shaped("conv_state", conv_state, (S, Dc, conv_state.shape[2]), dev)
     _bf16("weight", weight, (Dc, weight.shape[1]), dev)
@@ -281,21 +285,18 @@ def causal_conv1d_selective_update(xbc, conv_state, weight, bias, activation, dt
     dt_code = _steps(dt, (N, H), dev)
     if A is None:
         raise ValueError("A must be given")
-    if z is not None:
-        _bf16("z", z, (N, H, P), dev)
+    zs = _bf16("z", z, (N, H, P), dev) if z is not None else (0, 0)
     if workspace is None:
         workspace = selective_update_workspace(N, groups, dev)
-    elif workspace.dtype is not torch.int32 or not workspace.is_contiguous() or workspace.device != dev \
+    elif workspace.dtype is not _t.int32 or not workspace.is_contiguous() or workspace.device != dev \
             or workspace.numel() < N * groups:
         raise ValueError(f"workspace must be a contiguous int32 tensor of at least {N * groups} zeros")
     if out is None:
-        out = torch.empty(N, H, P, dtype=torch.bfloat16, device=dev)
-    else:
-        _bf16("out", out, (N, H, P), dev)
-    st, os_ = conv_state.stride(), out.stride()
-    zs = z.stride() if z is not None else (0, 0)
+        out = _t.empty(N, H, P, dtype=_t.bfloat16, device=dev)
+    os_ = _bf16("out", out, (N, H, P), dev)
+    st = conv_state.stride()
     with _b.on(dev) as stream:
-        rc = _b.load().dcconv_conv_selective_update(
+        rc = lib.dcconv_conv_selective_update(
             xbc.data_ptr(), N, H, P, groups, K, xbc.stride(0), conv_state.data_ptr(), conv_state.shape[2], st[0],
             st[1], st[2], weight.data_ptr(), weight.shape[1], None if bias is None else bias.data_ptr(),
             _i32_vector("cache_seqlens", cache_seqlens, N, dev), _b.ACTIVATIONS[activation], dt.data_ptr(), dt_code,
@@ -321,21 +322,18 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
     padding.  return_final_state: without ``ssm_state``, returns ``(out, state)`` with
     a new float32 [n, H, P, K] state.  ``workspace``: a uint8 buffer of
     ``dcconv_selective_scan_workspace`` bytes (allocated here if None)."""
-    import torch
-
+    lib = _lib()
     if x.dim() != 4 or B.dim() != 4:
         raise ValueError(f"x must be [N, T, H, P] and B [N, T, G, K], got {tuple(x.shape)} and {tuple(B.shape)}")
     dev = _gpu(x)
-    N, T, H, P = x.shape
-    G, K = B.shape[2:]
-    _bf16("x", x, (N, T, H, P), dev)
-    _bf16("B", B, (N, T, G, K), dev)
-    _bf16("C", C, (N, T, G, K), dev)
+    N, T, H, P = rows = x.shape
+    _, _, G, K = B.shape
+    xs = _bf16("x", x, rows, dev)
+    bs, cs = _bf16("B", B, (N, T, G, K), dev), _bf16("C", C, (N, T, G, K), dev)
     dt_code = _steps(dt, (N, T, H), dev)
     if A is None:
         raise ValueError("A must be given")
-    if z is not None:
-        _bf16("z", z, (N, T, H, P), dev)
+    zs = _bf16("z", z, rows, dev) if z is not None else (0, 0, 0)
     n = N
     if seq_starts is not None:
         if N != 1:
@@ -346,7 +344,7 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
     starts = _i32_vector("seq_starts", seq_starts, n + 1, dev)
     init = None
     if has_initial_state is not None:
-        if has_initial_state.dtype not in (torch.bool, torch.uint8) or not has_initial_state.is_contiguous():
+        if has_initial_state.dtype not in (_t.bool, _t.uint8) or not has_initial_state.is_contiguous():
             raise ValueError("has_initial_state must be a contiguous bool/uint8 [n] tensor")
         _shaped("has_initial_state", has_initial_state, (n,), dev)
         init = has_initial_state.data_ptr()
@@ -354,24 +352,22 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
     if ssm_state is None and return_final_state:
         if has_initial_state is not None or state_indices is not None:
             raise ValueError("has_initial_state and state_indices need an ssm_state")
-        ssm_state = final = torch.empty(n, H, P, K, dtype=torch.float32, device=dev)
+        ssm_state = final = _t.empty(n, H, P, K, dtype=_t.float32, device=dev)
     code, S, slot, pool = DCCONV_DTYPE_F32, 0, 0, None
     if ssm_state is not None:
         code, S, slot, _ = _pool(ssm_state, H, P, dev, K)
         pool = ssm_state.data_ptr()
     if out is None:
-        out = torch.empty(N, T, H, P, dtype=torch.bfloat16, device=dev)
-    else:
-        _bf16("out", out, (N, T, H, P), dev)
-    need = _b.load().dcconv_selective_scan_workspace(n, T, H, P, G, K, int(starts is not None))
+        out = _t.empty(rows, dtype=_t.bfloat16, device=dev)
+    os_ = _bf16("out", out, rows, dev)
+    need = lib.dcconv_selective_scan_workspace(n, T, H, P, G, K, int(starts is not None))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        workspace = _t.empty(need, dtype=_t.uint8, device=dev) if need else None
+    elif workspace.dtype is not _t.uint8 or not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError("workspace must be a contiguous uint8 tensor on x's device")
-    xs, ds, bs, cs, os_ = x.stride(), dt.stride(), B.stride(), C.stride(), out.stride()
-    zs = z.stride() if z is not None else (0, 0, 0)
+    ds = dt.stride()
     with _b.on(dev) as stream:
-        rc = _b.load().dcconv_selective_scan(
+        rc = lib.dcconv_selective_scan(
             x.data_ptr(), n, T, H, P, xs[0], xs[1], xs[2], dt.data_ptr(), dt_code, ds[0], ds[1],
             _f32_vector("dt_bias", dt_bias, H, dev), int(bool(dt_softplus)), _f32_vector("A", A, H, dev),
             B.data_ptr(), C.data_ptr(), G, K, bs[0], bs[1], bs[2], cs[0], cs[1], cs[2],
@@ -386,15 +382,14 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
 def w4_pack(codes):
     """Lay out the codes (uint8 [N, K], values 0 to 15) of a 4-bit weight matrix for
     ``w4_matvec``: uint8 [ceil(N/16), ceil(K/128), 64, 16]."""
-    import torch
-
-    if codes.dim() != 2 or codes.dtype is not torch.uint8 or not codes.is_contiguous():
+    lib = _lib()
+    if codes.dim() != 2 or codes.dtype is not _t.uint8 or not codes.is_contiguous():
         raise ValueError("codes must be a contiguous uint8 [N, K] tensor")
     dev = _gpu(codes)
     N, K = codes.shape
-    q = torch.empty(-(-N // 16), -(-K // 128), 64, 16, dtype=torch.uint8, device=dev)
+    q = _t.empty(-(-N // 16), -(-K // 128), 64, 16, dtype=_t.uint8, device=dev)
     with _b.on(dev) as stream:
-        rc = _b.load().dcconv_w4_pack(codes.data_ptr(), N, K, q.data_ptr(), stream)
+        rc = lib.dcconv_w4_pack(codes.data_ptr(), N, K, q.data_ptr(), stream)
     _b.raise_for(rc)
     return q
 
@@ -405,8 +400,7 @@ def w4_matvec(x, qweight, scales, zeros=None, bias=None, *, group_size, out=None
 
     qweight: ``w4_pack``'s tiles; scales: bf16 [ceil(K / group_size), N]; zeros: uint8 of
     that shape or None (8); bias: bf16 [N] or None; group_size: a multiple of 32."""
-    import torch
-
+    lib = _lib()
     if x.dim() != 2 or scales.dim() != 2:
         raise ValueError(f"x must be [M, K] and scales [groups, N], got {tuple(x.shape)} and {tuple(scales.shape)}")
     dev = _gpu(x)
@@ -417,21 +411,21 @@ def w4_matvec(x, qweight, scales, zeros=None, bias=None, *, group_size, out=None
     _bf16("scales", scales, (groups, N), dev)
     if not scales.is_contiguous():
         raise ValueError("scales must be contiguous")
-    if qweight.dtype is not torch.uint8 or not qweight.is_contiguous():
+    if qweight.dtype is not _t.uint8 or not qweight.is_contiguous():
         raise ValueError("qweight must be a contiguous uint8 tensor")
     _shaped("qweight", qweight, (-(-N // 16), -(-K // 128), 64, 16), dev)
     if zeros is not None:
-        if zeros.dtype is not torch.uint8 or not zeros.is_contiguous():
+        if zeros.dtype is not _t.uint8 or not zeros.is_contiguous():
             raise ValueError("zeros must be a contiguous uint8 tensor")
         _shaped("zeros", zeros, (groups, N), dev)
     if bias is not None:
         _bf16("bias", bias, (N,), dev)
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        out = _t.empty(M, N, dtype=_t.bfloat16, device=dev)
     else:
         _bf16("out", out, (M, N), dev)
     with _b.on(dev) as stream:
-        rc = _b.load().dcconv_w4_matvec(
+        rc = lib.dcconv_w4_matvec(
             x.data_ptr(), M, K, x.stride(0), qweight.data_ptr(), N, scales.data_ptr(),
             None if zeros is None else zeros.data_ptr(), group_size, None if bias is None else bias.data_ptr(),
             out.data_ptr(), out.stride(0) if M > 1 else N, stream)
