@@ -8,18 +8,19 @@
 //     out[p]      = (sum_k state[p, k] * C[k] + D[i] * x[p]) * silu(z[p])
 //
 // The state is read and written once and everything else is a few percent of it:
-// HBM bounds the call.  A block takes up to 64 rows p of one head.  Sixteen lanes
-// share a row, so the sum over k is four DPP steps, and each lane has all of its
-// state vectors in flight before the small operands (x, B, C: 2 bytes each, any
-// strides) pass through LDS.  All arithmetic is FP32; a BF16 state is rounded
-// when it is stored, after C has read the unrounded value.
+// HBM bounds the call.  An item is up to 64 rows p of one head's state; a block takes
+// several items of a group one after the other, with the next one's rows in flight
+// while it computes.  Sixteen lanes share a row, so the sum over k is four DPP steps.
+// The small operands (x, B, C, z, dt: 2 bytes each, any strides) are brought into LDS
+// for all of the block's items at once, as FP32.  All arithmetic is FP32; a BF16 state
+// is rounded when it is stored, after C has read the unrounded value.
 //
 // The fused form computes x, B and C as the width-4 convolution of its channels
 // (kept in FP32, not rounded to BF16 between the two operators).  Every block of
-// a group needs the group's B and C channels, and the convolution state of those
-// is advanced in place: each block counts itself in `arrivals[row, group]` once
-// it has read them, and the block that completes the count writes their state
-// and sets the count back to zero.  Nothing waits on the count.
+// a group needs the group's B and C channels (several items a block make that cheap),
+// and the convolution state of those is advanced in place: each block counts itself in
+// `arrivals[row, group]` once it has read them, and the block that completes the count
+// writes their state and sets the count back to zero.  Nothing waits on the count.
 #include "selective_common.h"
 
 namespace dcconv {
@@ -105,10 +106,17 @@ __device__ __forceinline__ float conv_channel(const SelectiveUpdateParams &p, in
         }
     }
     taps[3] = p.xbc[(int64_t)row * p.xbcs_n + ch];
+    float w[4];
+    if (reinterpret_cast<uintptr_t>(p.weight) % 8 == 0) {
+        const u32x2 v = *reinterpret_cast<const u32x2 *>(p.weight + (int64_t)ch * 4);
+        w[0] = lo_f32(v[0]), w[1] = hi_f32(v[0]), w[2] = lo_f32(v[1]), w[3] = hi_f32(v[1]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = bf16_bits_to_f32(p.weight[(int64_t)ch * 4 + j]);
+    }
     float acc = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        acc = __builtin_fmaf(bf16_bits_to_f32(taps[j]), bf16_bits_to_f32(p.weight[(int64_t)ch * 4 + j]), acc);
+    for (int j = 0; j < 4; ++j) acc = __builtin_fmaf(bf16_bits_to_f32(taps[j]), w[j], acc);
     if (p.bias != nullptr) acc += bf16_bits_to_f32(p.bias[ch]);
     return p.silu ? silu(acc) : acc;
 }
@@ -126,21 +134,30 @@ __device__ __forceinline__ void conv_advance(const SelectiveUpdateParams &p, int
     for (int j = 0; j < 3; ++j) st[(int64_t)(p.l - 3 + j) * p.st_l] = taps[j + 1];
 }
 
-// ROWS rows of the state per 16-lane group, NV vectors of VEC elements per lane
-// and row (16 * VEC * NV >= k).
+constexpr int kMaxItems = 8;  // of a block
+
+// How a call is cut up: items of `16 * ROWS` rows p, `chunk` of a group's to a block.
+struct UpdatePlan {
+    int32_t ptiles;  // items of a head
+    int32_t chunk, blocks;  // items of a block; blocks of a group
+};
+
+// ROWS rows of the state per 16-lane group and item, NV vectors of VEC elements per
+// lane and row (16 * VEC * NV >= k).
 template <bool F32, int VEC, int NV, int ROWS, bool CONV>
-__global__ __launch_bounds__(kUpdateBlock) void selective_update_kernel(const SelectiveUpdateParams p) {
-    __shared__ float s_x[ROWS * kGroups], s_b[kMaxK], s_c[kMaxK];
+__global__ __launch_bounds__(kUpdateBlock) void selective_update_kernel(const SelectiveUpdateParams p,
+                                                                        const UpdatePlan plan) {
+    constexpr int kItemRows = ROWS * kGroups;
+    __shared__ float s_x[kMaxItems * kItemRows], s_gate[kMaxItems * kItemRows], s_b[kMaxK], s_c[kMaxK];
+    __shared__ float s_step[kMaxItems], s_decay[kMaxItems], s_skip[kMaxItems];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 63, sub = tid & (kRowLanes - 1), grp = tid / kRowLanes;
-    const int ptiles = (p.p + ROWS * kGroups - 1) / (ROWS * kGroups);
-    const int per_group = p.h / p.g;
-    for_each_unit((int64_t)p.n * p.h * ptiles, [&](int64_t u) {
-        const int pt = (int)(u % ptiles);
-        const int64_t rh = u / ptiles;
-        const int head = (int)(rh % p.h), row = (int)(rh / p.h);
-        const int group = head / per_group;
-        const int p0 = pt * ROWS * kGroups;
+    const int per_group = p.h / p.g, group_items = per_group * plan.ptiles;
+    for_each_unit((int64_t)p.n * p.g * plan.blocks, [&](int64_t u) {
+        const int64_t rg = u / plan.blocks;
+        const int first = (int)(u - rg * plan.blocks) * plan.chunk, items = min(plan.chunk, group_items - first);
+        const int row = __builtin_amdgcn_readfirstlane((int)(rg / p.g));
+        const int group = __builtin_amdgcn_readfirstlane((int)(rg - (int64_t)row * p.g));
         int slot = route_row(p.idx, p.status, p.n, p.s, row, lane);
         int seen = 0;
         if (CONV && p.seqlens != nullptr) {
@@ -150,44 +167,64 @@ __global__ __launch_bounds__(kUpdateBlock) void selective_update_kernel(const Se
                 slot = -1;
             }
         }
-        uint16_t *out = p.out + (int64_t)row * p.os_n + (int64_t)head * p.os_h;
+        // item i's head and first row
+        auto place = [&](int i, int *head, int *p0) {
+            const int t = __builtin_amdgcn_readfirstlane((first + i) / plan.ptiles);
+            *head = group * per_group + t;
+            *p0 = (first + i - t * plan.ptiles) * kItemRows;
+        };
+        int head, p0;
         if (slot < 0) {  // a padding row: zeros, and no state moves
-            for (int q = p0 + tid; q < min(p.p, p0 + ROWS * kGroups); q += kUpdateBlock) out[q] = 0;
+            for (int i = 0; i < items; ++i) {
+                place(i, &head, &p0);
+                for (int q = p0 + tid; q < min(p.p, p0 + kItemRows); q += kUpdateBlock)
+                    p.out[(int64_t)row * p.os_n + (int64_t)head * p.os_h + q] = 0;
+            }
             return;
         }
 
-        // the state rows, all in flight at once
-        const int64_t base = (int64_t)slot * p.ss_s + (int64_t)head * p.p * p.k;
+        // an item's state rows, all in flight at once
         StateVec<F32, VEC> st[ROWS][NV];
+        auto fetch = [&](int i) {
+            int fh, fp;
+            place(i, &fh, &fp);
+            const int64_t base = (int64_t)slot * p.ss_s + (int64_t)fh * p.p * p.k;
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r)
+            for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int pr = p0 + r * kGroups + grp, k0 = (v * kRowLanes + sub) * VEC;
-                if (pr < p.p && k0 < p.k) st[r][v].load(p.state, base + (int64_t)pr * p.k + k0);
-            }
+                for (int v = 0; v < NV; ++v) {
+                    const int pr = fp + r * kGroups + grp, k0 = (v * kRowLanes + sub) * VEC;
+                    if (pr < p.p && k0 < p.k) st[r][v].load(p.state, base + (int64_t)pr * p.k + k0);
+                }
+        };
+        fetch(0);
 
-        // the small operands, through LDS
-        const float step = load_step(p, (int64_t)row * p.ds_n + head, head);
-        const float decay = expf(step * p.a[head]);
-        if constexpr (!CONV) {
-            const uint16_t *x = p.x + (int64_t)row * p.xs_n + (int64_t)head * p.xs_h;
-            const uint16_t *b = p.b + (int64_t)row * p.bs_n + (int64_t)group * p.bs_g;
-            const uint16_t *c = p.c + (int64_t)row * p.cs_n + (int64_t)group * p.cs_g;
-            if (tid < ROWS * kGroups && p0 + tid < p.p) s_x[tid] = bf16_bits_to_f32(x[p0 + tid]);
-            if (tid < p.k) {
-                s_b[tid] = bf16_bits_to_f32(b[tid]);
-                s_c[tid] = bf16_bits_to_f32(c[tid]);
+        // the small operands of all items, through LDS
+        if (tid < items) {
+            const int h = group * per_group + (first + tid) / plan.ptiles;
+            const float step = load_step(p, (int64_t)row * p.ds_n + h, h);
+            s_step[tid] = step;
+            s_decay[tid] = expf(step * p.a[h]);
+            s_skip[tid] = p.d_skip != nullptr ? p.d_skip[h] : 0.0f;
+        }
+        const int64_t cbase = CONV ? (int64_t)slot * p.st_s : 0;
+        for (int e = tid; e < items * kItemRows; e += kUpdateBlock) {
+            const int i = e / kItemRows, t = (first + i) / plan.ptiles, h = group * per_group + t;
+            const int q = (first + i - t * plan.ptiles) * kItemRows + e % kItemRows;
+            if (q >= p.p) continue;
+            if constexpr (CONV) {
+                uint16_t taps[4];
+                s_x[e] = conv_channel(p, row, cbase, seen, h * p.p + q, taps);
+                conv_advance(p, cbase, seen, h * p.p + q, taps);  // this block's alone
+            } else {
+                s_x[e] = bf16_bits_to_f32(p.x[(int64_t)row * p.xs_n + (int64_t)h * p.xs_h + q]);
             }
-            __syncthreads();
-        } else {
-            const int64_t cbase = (int64_t)slot * p.st_s;
-            const int hp = p.h * p.p;
-            uint16_t xt[4], bt[4], ct[4];
-            const int xch = head * p.p + p0 + tid, bch = hp + group * p.k + tid, cch = bch + p.g * p.k;
-            const bool has_x = tid < ROWS * kGroups && p0 + tid < p.p, has_bc = tid < p.k;
-            if (has_x) s_x[tid] = conv_channel(p, row, cbase, seen, xch, xt);
-            if (has_bc) {
+            s_gate[e] = p.z != nullptr ? silu(bf16_bits_to_f32(p.z[(int64_t)row * p.zs_n + (int64_t)h * p.zs_h + q])) : 1.0f;
+        }
+        if constexpr (CONV) {
+            uint16_t bt[4], ct[4];
+            const int bch = p.h * p.p + group * p.k + tid, cch = bch + p.g * p.k;
+            if (tid < p.k) {
                 s_b[tid] = conv_channel(p, row, cbase, seen, bch, bt);
                 s_c[tid] = conv_channel(p, row, cbase, seen, cch, ct);
             }
@@ -195,15 +232,20 @@ __global__ __launch_bounds__(kUpdateBlock) void selective_update_kernel(const Se
             if (tid == 0) {
                 int32_t *count = p.arrivals + (int64_t)row * p.g + group;
                 const int before = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                s_last = before == per_group * ptiles - 1;
+                s_last = before == plan.blocks - 1;
                 if (s_last) __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
-            if (has_x) conv_advance(p, cbase, seen, xch, xt);
             __syncthreads();
-            if (s_last && has_bc) {
+            if (s_last && tid < p.k) {
                 conv_advance(p, cbase, seen, bch, bt);
                 conv_advance(p, cbase, seen, cch, ct);
             }
+        } else {
+            if (tid < p.k) {
+                s_b[tid] = bf16_bits_to_f32(p.b[(int64_t)row * p.bs_n + (int64_t)group * p.bs_g + tid]);
+                s_c[tid] = bf16_bits_to_f32(p.c[(int64_t)row * p.cs_n + (int64_t)group * p.cs_g + tid]);
+            }
+            __syncthreads();
         }
 
         float bv[NV][VEC], cv[NV][VEC];
@@ -215,56 +257,75 @@ __global__ __launch_bounds__(kUpdateBlock) void selective_update_kernel(const Se
                 bv[v][e] = k0 < p.k ? s_b[k0 + e] : 0.0f;
                 cv[v][e] = k0 < p.k ? s_c[k0 + e] : 0.0f;
             }
-        const float skip = p.d_skip != nullptr ? p.d_skip[head] : 0.0f;
+        for (int i = 0; i < items; ++i) {
+            StateVec<F32, VEC> now[ROWS][NV];
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            const int pr = p0 + r * kGroups + grp;
-            if (pr >= p.p) continue;
-            const float xv = s_x[r * kGroups + grp], xd = step * xv;
-            float y = 0.0f;
+            for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int k0 = (v * kRowLanes + sub) * VEC;
-                if (k0 >= p.k) continue;
+                for (int v = 0; v < NV; ++v) now[r][v] = st[r][v];
+            if (i + 1 < items) fetch(i + 1);
+            place(i, &head, &p0);
+            const int64_t base = (int64_t)slot * p.ss_s + (int64_t)head * p.p * p.k;
+            uint16_t *out = p.out + (int64_t)row * p.os_n + (int64_t)head * p.os_h;
+            const float step = s_step[i], decay = s_decay[i], skip = s_skip[i];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float s = __builtin_fmaf(xd, bv[v][e], st[r][v].get(e) * decay);
-                    y = __builtin_fmaf(s, cv[v][e], y);
-                    st[r][v].set(e, s);
+            for (int r = 0; r < ROWS; ++r) {
+                const int at = r * kGroups + grp, pr = p0 + at;
+                if (pr >= p.p) continue;
+                const float xv = s_x[i * kItemRows + at], xd = step * xv;
+                float y = 0.0f;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int k0 = (v * kRowLanes + sub) * VEC;
+                    if (k0 >= p.k) continue;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float s = __builtin_fmaf(xd, bv[v][e], now[r][v].get(e) * decay);
+                        y = __builtin_fmaf(s, cv[v][e], y);
+                        now[r][v].set(e, s);
+                    }
+                    now[r][v].store(p.state, base + (int64_t)pr * p.k + k0);
                 }
-                st[r][v].store(p.state, base + (int64_t)pr * p.k + k0);
-            }
-            y = row_sum(y);
-            if (sub == 0) {
-                y = __builtin_fmaf(skip, xv, y);
-                if (p.z != nullptr)
-                    y *= silu(bf16_bits_to_f32(p.z[(int64_t)row * p.zs_n + (int64_t)head * p.zs_h + pr]));
-                out[pr] = f32_to_bf16_bits(y);
+                y = row_sum(y);
+                if (sub == 0) {
+                    y = __builtin_fmaf(skip, xv, y);
+                    if (p.z != nullptr) y *= s_gate[i * kItemRows + at];
+                    out[pr] = f32_to_bf16_bits(y);
+                }
             }
         }
         __syncthreads();  // the next unit reuses the LDS arrays
     });
 }
 
-// Four state rows per 16-lane group while the grid still holds this many blocks.
-constexpr int64_t kMinBlocksForFourRows = 2048;
+// Items of 64 rows while there are this many, else of 16; and blocks of several items
+// while this many blocks remain.
+constexpr int64_t kMinLargeItems = 2048;
+constexpr int64_t kUpdateBlocks = 4096;
 
 template <bool F32, int VEC, int NV>
 hipError_t launch_rows(const SelectiveUpdateParams &p, hipStream_t stream) {
     const int64_t heads = (int64_t)p.n * p.h;
-    const bool four = heads * ((p.p + 63) / 64) >= kMinBlocksForFourRows;
-    const int64_t units = heads * (four ? (p.p + 63) / 64 : (p.p + 15) / 16);
+    const bool four = heads * ((p.p + 63) / 64) >= kMinLargeItems;
+    UpdatePlan plan;
+    plan.ptiles = four ? (p.p + 63) / 64 : (p.p + 15) / 16;
+    const int64_t in_group = (int64_t)(p.h / p.g) * plan.ptiles, chunk = heads * plan.ptiles / kUpdateBlocks;
+    plan.chunk = (int32_t)(chunk < 1 ? 1 : chunk > kMaxItems ? kMaxItems : chunk);
+    plan.blocks = (int32_t)((in_group + plan.chunk - 1) / plan.chunk);
+    plan.chunk = (int32_t)((in_group + plan.blocks - 1) / plan.blocks);  // even shares
+    plan.blocks = (int32_t)((in_group + plan.chunk - 1) / plan.chunk);
+    const int64_t units = (int64_t)p.n * p.g * plan.blocks;
     const dim3 grid((unsigned)(units < kMaxBlocks ? units : kMaxBlocks));
     if (p.conv) {
         if (four)
-            selective_update_kernel<F32, VEC, NV, 4, true><<<grid, kUpdateBlock, 0, stream>>>(p);
+            selective_update_kernel<F32, VEC, NV, 4, true><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
         else
-            selective_update_kernel<F32, VEC, NV, 1, true><<<grid, kUpdateBlock, 0, stream>>>(p);
+            selective_update_kernel<F32, VEC, NV, 1, true><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
     } else {
         if (four)
-            selective_update_kernel<F32, VEC, NV, 4, false><<<grid, kUpdateBlock, 0, stream>>>(p);
+            selective_update_kernel<F32, VEC, NV, 4, false><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
         else
-            selective_update_kernel<F32, VEC, NV, 1, false><<<grid, kUpdateBlock, 0, stream>>>(p);
+            selective_update_kernel<F32, VEC, NV, 1, false><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
     }
     return hipGetLastError();
 }

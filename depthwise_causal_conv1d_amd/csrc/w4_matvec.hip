@@ -17,7 +17,7 @@
 // takes the offset out again in FP32 (it costs about 5 of FP32's 24 bits, of which a
 // BF16 result keeps 8).  Products and sums are FP32 throughout; out is rounded once.
 //
-// A block owns NT tiles of outputs and its waves share out the inputs, 128 at a
+// A block owns a tile of outputs and its waves share out the inputs, 128 at a
 // time; they are joined through LDS in the order of the waves.
 #include "selective_common.h"
 
@@ -43,113 +43,127 @@ __device__ __forceinline__ u32x4 expand(uint32_t w) {
     return v;
 }
 
-// Up to eight consecutive values of a row, `count` of which exist: zeros behind.
+constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer
+
+// What a wave reads: eight values of its lanes' rows of x from input k on, and the scale
+// and zero point of group `gr` for its lanes' outputs.  WIDE goes through buffers, which
+// leaves one compare and select a load to the vector units; otherwise element by element.
 template <bool WIDE>
-__device__ __forceinline__ u32x4 load8(const uint16_t *s, int count) {
-    u32x4 v = {0, 0, 0, 0};
-    if (WIDE) {
-        if (count > 0) v = *reinterpret_cast<const u32x4 *>(s);
-    } else {
+struct Operands {
+    const W4Params &p;
+    int n, g;
+    Buffer xbuf, sbuf, zbuf;
+    __device__ __forceinline__ Operands(const W4Params &p, int n, int g) : p(p), n(n), g(g) {
+        if (!WIDE) return;
+        const int groups = (p.k + p.group - 1) / p.group;
+        xbuf = make_buffer(p.x, (uint32_t)(2 * ((p.m - 1) * p.xs_m + p.k)));
+        sbuf = make_buffer(p.scales, 2u * (uint32_t)groups * (uint32_t)p.n);
+        zbuf = make_buffer(p.zeros, p.zeros != nullptr ? (uint32_t)groups * (uint32_t)p.n : 0u);
+    }
+    // row: the byte offset of the lane's row and inner position, or kNowhere
+    __device__ __forceinline__ u32x4 x(uint32_t row, int m, int k) const {
+        if (WIDE) return buffer_load<kCached>(xbuf, k + 8 * g < p.k ? row + 2u * (uint32_t)k : kNowhere);
+        u32x4 v = {0, 0, 0, 0};
+        const uint16_t *s = p.x + (int64_t)m * p.xs_m + k + 8 * g;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < count) v[i >> 1] |= (uint32_t)s[i] << (16 * (i & 1));
+            if (m < p.m && k + 8 * g + i < p.k) v[i >> 1] |= (uint32_t)s[i] << (16 * (i & 1));
+        return v;
     }
-    return v;
-}
+    // (a scale of zero past the last output and the last group)
+    __device__ __forceinline__ uint16_t scale(int gr, bool there) const {
+        if (WIDE)
+            return __builtin_amdgcn_raw_buffer_load_b16(sbuf, there && n < p.n ? 2u * (uint32_t)n : kNowhere,
+                                                        there ? 2 * gr * p.n : 0, kCached);
+        return there && n < p.n ? p.scales[(int64_t)gr * p.n + n] : 0;
+    }
+    __device__ __forceinline__ uint8_t zero(int gr, bool there) const {
+        if (p.zeros == nullptr) return 8;
+        if (WIDE)
+            return __builtin_amdgcn_raw_buffer_load_b8(zbuf, there && n < p.n ? (uint32_t)n : kNowhere,
+                                                       there ? gr * p.n : 0, kCached);
+        return there && n < p.n ? p.zeros[(int64_t)gr * p.n + n] : 0;
+    }
+};
 
-// NT tiles of outputs, MT tiles of 16 rows of x; STEPS matrix instructions (of 32
-// inputs) share a scale.
-template <int NT, int MT, int STEPS, bool WIDE>
+// MT tiles of 16 rows of x; STEPS matrix instructions (of 32 inputs) share a scale, and
+// with ONE so many inputs are a whole group.
+template <int MT, int STEPS, bool ONE, bool WIDE>
 __global__ __launch_bounds__(kMaxW4Waves *kWave) void w4_matvec_kernel(const W4Params p) {
-    extern __shared__ float joined[];  // [wave][NT][MT][16 x 16]
+    constexpr int kScales = 4 / STEPS;
+    extern __shared__ float joined[];  // [wave][MT][16 x 16]
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const int ktiles = (p.k + kTileK - 1) / kTileK, ntiles = (p.n + kTileN - 1) / kTileN;
-    const int nt0 = blockIdx.x * NT;
-    const int m0 = blockIdx.y * MT * 16;
+    const int ktiles = (p.k + kTileK - 1) / kTileK;
+    // Blocks are dealt to the eight XCDs in turn; eight neighbouring tiles, whose scales
+    // share cache lines, go to the same one.
+    const int ntiles = (p.n + kTileN - 1) / kTileN, in64 = blockIdx.x & 63;
+    const int nt = blockIdx.x - in64 + (in64 & 7) * 8 + (in64 >> 3), m0 = blockIdx.y * MT * 16;
+    if (nt >= ntiles) return;
+    const Operands<WIDE> in(p, nt * kTileN + r, g);
 
-    f32x4_t total[NT][MT];
+    f32x4_t total[MT];
+    uint32_t row[MT];
 #pragma unroll
-    for (int a = 0; a < NT; ++a)
-#pragma unroll
-        for (int b = 0; b < MT; ++b) total[a][b] = f32x4_t{0, 0, 0, 0};
+    for (int b = 0; b < MT; ++b) {
+        total[b] = f32x4_t{0, 0, 0, 0};
+        const int m = m0 + 16 * b + r;
+        row[b] = m < p.m ? 2u * ((uint32_t)m * (uint32_t)p.xs_m + 8u * (uint32_t)g) : kNowhere;
+    }
     const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    const u32x4 *tiles = reinterpret_cast<const u32x4 *>(p.q) + (int64_t)nt * ktiles * kWave;
 
     for (int kt = wave; kt < ktiles; kt += waves) {
-        u32x4 q[NT];
+        const u32x4 q = tiles[(int64_t)kt * kWave + lane];
+        uint16_t scale[kScales];
+        uint8_t zero[kScales];
 #pragma unroll
-        for (int a = 0; a < NT; ++a)
-            q[a] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p.q) +
-                                              ((int64_t)min(nt0 + a, ntiles - 1) * ktiles + kt) * kWave + lane);
-        float scale[NT][4 / STEPS], offset[NT][4 / STEPS];
-#pragma unroll
-        for (int a = 0; a < NT; ++a)
-#pragma unroll
-            for (int s = 0; s < 4 / STEPS; ++s) {
-                const int n = (nt0 + a) * kTileN + r, k = kt * kTileK + s * STEPS * 32;
-                float sc = 0.0f, zero = 8.0f;
-                if (n < p.n && k < p.k) {
-                    const int64_t at = (int64_t)(k / p.group) * p.n + n;
-                    sc = bf16_bits_to_f32(p.scales[at]);
-                    if (p.zeros != nullptr) zero = (float)p.zeros[at];
-                }
-                scale[a][s] = sc;
-                offset[a][s] = -sc * (128.0f + zero);
-            }
+        for (int s = 0; s < kScales; ++s) {
+            const int block = kt * kScales + s;
+            const int gr = ONE ? block : __builtin_amdgcn_readfirstlane(block * (STEPS * 32) / p.group);
+            scale[s] = in.scale(gr, block * (STEPS * 32) < p.k);
+            zero[s] = in.zero(gr, block * (STEPS * 32) < p.k);
+        }
         u32x4 x[MT][4];
 #pragma unroll
         for (int b = 0; b < MT; ++b)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int m = m0 + 16 * b + r, k = kt * kTileK + 32 * s + 8 * g;
-                x[b][s] = load8<WIDE>(p.x + (int64_t)m * p.xs_m + k, m < p.m ? p.k - k : 0);
-            }
+            for (int s = 0; s < 4; ++s) x[b][s] = in.x(row[b], m0 + 16 * b + r, kt * kTileK + 32 * s);
 #pragma unroll
-        for (int s = 0; s < 4 / STEPS; ++s) {
-            f32x4_t sum[MT], acc[NT][MT];
+        for (int s = 0; s < kScales; ++s) {
+            f32x4_t sum[MT], acc[MT];
 #pragma unroll
-            for (int b = 0; b < MT; ++b) {
-                sum[b] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-                for (int a = 0; a < NT; ++a) acc[a][b] = f32x4_t{0, 0, 0, 0};
-            }
+            for (int b = 0; b < MT; ++b) sum[b] = acc[b] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
+                const u32x4 w = expand(q[s * STEPS + i]);
 #pragma unroll
-                for (int b = 0; b < MT; ++b) sum[b] = mfma(x[b][s * STEPS + i], ones, sum[b]);
-#pragma unroll
-                for (int a = 0; a < NT; ++a) {
-                    const u32x4 w = expand(q[a][s * STEPS + i]);
-#pragma unroll
-                    for (int b = 0; b < MT; ++b) acc[a][b] = mfma(x[b][s * STEPS + i], w, acc[a][b]);
+                for (int b = 0; b < MT; ++b) {
+                    sum[b] = mfma(x[b][s * STEPS + i], ones, sum[b]);
+                    acc[b] = mfma(x[b][s * STEPS + i], w, acc[b]);
                 }
             }
+            const float sc = bf16_bits_to_f32(scale[s]), offset = -sc * (128.0f + (float)zero[s]);
 #pragma unroll
-            for (int a = 0; a < NT; ++a)
+            for (int b = 0; b < MT; ++b)
 #pragma unroll
-                for (int b = 0; b < MT; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        total[a][b][i] = __builtin_fmaf(offset[a][s], sum[b][i],
-                                                        __builtin_fmaf(scale[a][s], acc[a][b][i], total[a][b][i]));
+                for (int i = 0; i < 4; ++i)
+                    total[b][i] = __builtin_fmaf(offset, sum[b][i], __builtin_fmaf(sc, acc[b][i], total[b][i]));
         }
     }
 
     // lane (r, g) holds output r, rows 4 g .. 4 g + 3 of each tile
 #pragma unroll
-    for (int a = 0; a < NT; ++a)
+    for (int b = 0; b < MT; ++b)
 #pragma unroll
-        for (int b = 0; b < MT; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                joined[((wave * NT + a) * MT + b) * 256 + (4 * g + i) * 16 + r] = total[a][b][i];
+        for (int i = 0; i < 4; ++i) joined[(wave * MT + b) * 256 + (4 * g + i) * 16 + r] = total[b][i];
     __syncthreads();
-    for (int e = threadIdx.x; e < NT * MT * 256; e += blockDim.x) {
-        const int n = (nt0 + (e >> 8) / MT) * kTileN + (e & 15), m = m0 + ((e >> 8) % MT) * 16 + ((e >> 4) & 15);
-        if (n >= p.n || m >= p.m) continue;
-        float v = p.bias != nullptr ? bf16_bits_to_f32(p.bias[n]) : 0.0f;
-        for (int w = 0; w < waves; ++w) v += joined[w * NT * MT * 256 + e];
-        p.out[(int64_t)m * p.os_m + n] = f32_to_bf16_bits(v);
+    for (int e = threadIdx.x; e < MT * 256; e += blockDim.x) {
+        const int col = nt * kTileN + (e & 15), m = m0 + (e >> 4);
+        if (col >= p.n || m >= p.m) continue;
+        float v = p.bias != nullptr ? bf16_bits_to_f32(p.bias[col]) : 0.0f;
+        for (int w = 0; w < waves; ++w) v += joined[w * MT * 256 + e];
+        p.out[(int64_t)m * p.os_m + col] = f32_to_bf16_bits(v);
     }
 }
 
@@ -173,38 +187,45 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const uint8_t *codes, int6
 // Waves of a block: as many as keep about this many on the card, with an input tile each.
 constexpr int64_t kW4Waves = 4096;
 
-template <int NT, int MT, int STEPS>
+template <int MT, int STEPS, bool ONE>
 hipError_t launch_tiles(const W4Params &p, bool wide, hipStream_t stream) {
     const int64_t ktiles = (p.k + kTileK - 1) / kTileK;
-    const int64_t blocks = ((p.n + kTileN - 1) / kTileN + NT - 1) / NT, rows = (p.m + 16 * MT - 1) / (16 * MT);
+    const int64_t blocks = (p.n + kTileN - 1) / kTileN, rows = (p.m + 16 * MT - 1) / (16 * MT);
     int waves = 4;
     while (waves < kMaxW4Waves && blocks * rows * waves < kW4Waves) waves *= 2;
     while (waves > 1 && waves > ktiles) waves /= 2;
     if (rows > 65535) return hipErrorInvalidConfiguration;
-    const size_t lds = (size_t)waves * NT * MT * 256 * 4;
-    const dim3 grid((unsigned)blocks, (unsigned)rows);
+    const size_t lds = (size_t)waves * MT * 256 * 4;
+    const dim3 grid((unsigned)((blocks + 63) / 64 * 64), (unsigned)rows);
     if (wide)
-        w4_matvec_kernel<NT, MT, STEPS, true><<<grid, waves * kWave, lds, stream>>>(p);
+        w4_matvec_kernel<MT, STEPS, ONE, true><<<grid, waves * kWave, lds, stream>>>(p);
     else
-        w4_matvec_kernel<NT, MT, STEPS, false><<<grid, waves * kWave, lds, stream>>>(p);
+        w4_matvec_kernel<MT, STEPS, ONE, false><<<grid, waves * kWave, lds, stream>>>(p);
     return hipGetLastError();
 }
 
-template <int STEPS>
+template <int STEPS, bool ONE>
 hipError_t launch_steps(const W4Params &p, bool wide, hipStream_t stream) {
-    if (p.m <= 16) return launch_tiles<1, 1, STEPS>(p, wide, stream);
-    if (p.m <= 32) return launch_tiles<1, 2, STEPS>(p, wide, stream);
-    return launch_tiles<1, 4, STEPS>(p, wide, stream);
+    if (p.m <= 16) return launch_tiles<1, STEPS, ONE>(p, wide, stream);
+    if (p.m <= 32) return launch_tiles<2, STEPS, ONE>(p, wide, stream);
+    return launch_tiles<4, STEPS, ONE>(p, wide, stream);
 }
 
 }  // namespace
 
 hipError_t launch_w4_matvec(const W4Params &p, hipStream_t stream, const char **kernel_name) {
-    const bool wide = p.k % 8 == 0 && p.xs_m % 8 == 0 && reinterpret_cast<uintptr_t>(p.x) % 16 == 0;
+    // 16-byte rows, and offsets of 32 bits
+    const int64_t groups = (p.k + p.group - 1) / p.group, most = (int64_t)1 << 31;
+    const bool wide = p.k % 8 == 0 && p.xs_m % 8 == 0 && reinterpret_cast<uintptr_t>(p.x) % 16 == 0 &&
+                      p.xs_m < most / 2 && 2 * ((p.m - 1) * p.xs_m + p.k) < most && 2 * groups * p.n < most;
     *kernel_name = wide ? "w4_matvec" : "w4_matvec_scalar";
-    if (p.group % 128 == 0) return launch_steps<4>(p, wide, stream);
-    if (p.group % 64 == 0) return launch_steps<2>(p, wide, stream);
-    return launch_steps<1>(p, wide, stream);
+    switch (p.group) {
+        case 128: return launch_steps<4, true>(p, wide, stream);
+        case 64: return launch_steps<2, true>(p, wide, stream);
+        case 32: return launch_steps<1, true>(p, wide, stream);
+    }
+    if (p.group % 128 == 0) return launch_steps<4, false>(p, wide, stream);
+    return launch_steps<1, false>(p, wide, stream);
 }
 
 hipError_t launch_w4_pack(const uint8_t *codes, int64_t n, int64_t k, uint8_t *q, hipStream_t stream) {
