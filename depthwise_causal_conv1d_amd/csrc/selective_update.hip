@@ -8,7 +8,7 @@
 //     out[p]      = (sum_k state[p, k] * C[k] + D[i] * x[p]) * silu(z[p])
 //
 // The state is read and written once and everything else is a few percent of it:
-// HBM bounds the call.  An item is up to 64 rows p of one head's state; a block takes
+// HBM bounds the call.  An item is up to 32 rows p of one head's state; a block takes
 // several items of a group one after the other, with the next one's rows in flight
 // while it computes.  Sixteen lanes share a row, so the sum over k is four DPP steps.
 // The small operands (x, B, C, z, dt: 2 bytes each, any strides) are brought into LDS
@@ -298,18 +298,26 @@ __global__ __launch_bounds__(kUpdateBlock) void selective_update_kernel(const Se
     });
 }
 
-// Items of 64 rows while there are this many, else of 16; and blocks of several items
-// while this many blocks remain.
+// Items of 32 rows while there are this many, else of 16.  A block takes items worth
+// kBlockState bytes of state, or kFusedBlockState in the fused form, where each block
+// convolves its group's B and C; but no more than leave kUpdateBlocks blocks.  (256 rows
+// of 96 heads, 64 x 128: F32 states with 16, 32 and 64 KiB a block 295, 257 and 285 us,
+// BF16 147 at 16 and 136 at 32 KiB; fused, BF16 states, 201, 160 and 154 us at 16, 32
+// and 64 KiB.)
 constexpr int64_t kMinLargeItems = 2048;
-constexpr int64_t kUpdateBlocks = 4096;
+constexpr int64_t kUpdateBlocks = 768;
+constexpr int64_t kBlockState = 32 * 1024, kFusedBlockState = 64 * 1024;
 
 template <bool F32, int VEC, int NV>
 hipError_t launch_rows(const SelectiveUpdateParams &p, hipStream_t stream) {
     const int64_t heads = (int64_t)p.n * p.h;
-    const bool four = heads * ((p.p + 63) / 64) >= kMinLargeItems;
+    const bool large = heads * ((p.p + 31) / 32) >= kMinLargeItems;
+    const int rows = large ? 32 : 16;
     UpdatePlan plan;
-    plan.ptiles = four ? (p.p + 63) / 64 : (p.p + 15) / 16;
-    const int64_t in_group = (int64_t)(p.h / p.g) * plan.ptiles, chunk = heads * plan.ptiles / kUpdateBlocks;
+    plan.ptiles = (p.p + rows - 1) / rows;
+    const int64_t in_group = (int64_t)(p.h / p.g) * plan.ptiles;
+    int64_t chunk = (p.conv ? kFusedBlockState : kBlockState) / ((int64_t)rows * p.k * (F32 ? 4 : 2));
+    if (chunk > heads * plan.ptiles / kUpdateBlocks) chunk = heads * plan.ptiles / kUpdateBlocks;
     plan.chunk = (int32_t)(chunk < 1 ? 1 : chunk > kMaxItems ? kMaxItems : chunk);
     plan.blocks = (int32_t)((in_group + plan.chunk - 1) / plan.chunk);
     plan.chunk = (int32_t)((in_group + plan.blocks - 1) / plan.blocks);  // even shares
@@ -317,13 +325,13 @@ hipError_t launch_rows(const SelectiveUpdateParams &p, hipStream_t stream) {
     const int64_t units = (int64_t)p.n * p.g * plan.blocks;
     const dim3 grid((unsigned)(units < kMaxBlocks ? units : kMaxBlocks));
     if (p.conv) {
-        if (four)
-            selective_update_kernel<F32, VEC, NV, 4, true><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
+        if (large)
+            selective_update_kernel<F32, VEC, NV, 2, true><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
         else
             selective_update_kernel<F32, VEC, NV, 1, true><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
     } else {
-        if (four)
-            selective_update_kernel<F32, VEC, NV, 4, false><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
+        if (large)
+            selective_update_kernel<F32, VEC, NV, 2, false><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
         else
             selective_update_kernel<F32, VEC, NV, 1, false><<<grid, kUpdateBlock, 0, stream>>>(p, plan);
     }
