@@ -321,7 +321,8 @@ extern "C" int dcconv_selective_scan(const void *x, int64_t n, int64_t t, int64_
     int rc = check_shapes(n, h, p, g, k, dt_dtype, state_dtype, s, ss_s, state_indices != nullptr, stateless);
     if (rc != DCCONV_OK) return rc;
     if (t < 0) return fail(DCCONV_EINVAL, "t (tokens) must be >= 0, got %lld", (long long)t);
-    if (t > kI32Max - 1024) return fail(DCCONV_EUNSUPPORTED, "t >= 2^31 - 1024 tokens is not served");
+    if (t > kI32Max - 1024 || n > kI32Max - (1 << 24))
+        return fail(DCCONV_EUNSUPPORTED, "t >= 2^31 - 1024 tokens or n >= 2^31 - 2^24 sequences is not served");
     if (any_negative({xs_n, xs_t, xs_h, ds_n, ds_t, bs_n, bs_t, bs_g, cs_n, cs_t, cs_g, zs_n, zs_t, zs_h, os_n, os_t,
                       os_h, workspace_bytes}))
         return fail(DCCONV_EINVAL, "strides and workspace_bytes must be non-negative");

@@ -198,15 +198,15 @@ constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer
 template <bool WIDE>
 struct ChunkRows {
     const uint16_t *base;  // wave-uniform: the chunk's first row
-    int64_t stride;
+    int64_t stride, col;
     int32_t step, row0, count, rows;
     uint32_t at0, hop, width;
     Buffer buf;
     __device__ __forceinline__ ChunkRows(const uint16_t *first, int64_t stride, int step, int64_t width, int row,
                                          int64_t col, int count)
-        : base(first), stride(stride), step(step), row0(row), count(count), width(2u * (uint32_t)width) {
+        : base(first), stride(stride), col(col), step(step), row0(row), count(count), width(2u * (uint32_t)width) {
         const uint32_t bytes = 2u * (uint32_t)stride;
-        at0 = WIDE ? (count > 0 ? (uint32_t)row * bytes + 2u * (uint32_t)col : kNowhere) : (uint32_t)col;
+        at0 = count > 0 ? (uint32_t)row * bytes + 2u * (uint32_t)col : kNowhere;
         hop = (uint32_t)step * bytes;
     }
     __device__ __forceinline__ void begin(int n) {
@@ -221,7 +221,7 @@ struct ChunkRows {
             return;
         }
         const int row = row0 + q * step;
-        const uint16_t *from = base + row * stride + at0;
+        const uint16_t *from = base + row * stride + col;
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = 0;
 #pragma unroll
@@ -234,7 +234,7 @@ struct ChunkRows {
             return;
         }
         if (row0 >= rows) return;
-        uint16_t *to = const_cast<uint16_t *>(base) + row0 * stride + at0;
+        uint16_t *to = const_cast<uint16_t *>(base) + row0 * stride + col;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < count) to[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));

@@ -489,3 +489,57 @@ def test_offsets_past_32_bits():
                                       h0=f64(start[i]))
             close(out[i], y[0], U * y[0].abs() + (U + 2.0 ** -13) * ya[0], "out")
             close(view[i], h, 2.0 ** -17 * ha, "state")
+
+
+def test_scan_heads_past_32_bits():
+    """Heads 2^31 elements apart, read and written element by element."""
+    apart, T, H, P = (1 << 31) + 8, 40, 2, 32
+    case = Scan(21, [T], H, P, 1, 64, state=torch.float32, z=False)
+    buf = torch.empty(apart + 2 * T * P, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((1, T, H, P), (0, P, apart, 1))
+    x.copy_(case.x)
+    want = case.call()
+    state = case.pool.clone()
+    case.place = lambda t: x if t is case.x else t.cuda()
+    big = torch.empty(apart + T * P, dtype=torch.bfloat16, device="cuda")
+    out = big.as_strided((1, T, H, P), (0, P, apart, 1))
+    got = case.call(out=out)
+    assert torch.equal(got, want) and torch.equal(case.pool, state)
+
+
+def test_refusals():
+    case = Update(20, 3, 4, 64, 2, 128, torch.float32)
+    x, dt, A, B, C, state = (t.cuda() for t in (case.x, case.dt, case.A, case.B, case.C, case.state))
+
+    def update(**over):
+        a = dict(x=x, dt=dt, A=A, B=B, C=C, ssm_state=state)
+        a.update(over)
+        return dc.selective_update(a.pop("x"), a.pop("dt"), a.pop("A"), a.pop("B"), a.pop("C"), a.pop("ssm_state"), **a)
+    for over, what in ((dict(x=x.float()), "bfloat16"), (dict(dt=dt.half()), "dt must be"), (dict(A=A.bfloat16()), "A must"),
+                       (dict(A=None), "A must"), (dict(B=B[:, :, :64]), "C must"), (dict(C=C[:2]), "C must"),
+                       (dict(ssm_state=state.half()), "ssm_state"), (dict(ssm_state=state[:, :, :, ::2]), "ssm_state"),
+                       (dict(ssm_state=state.transpose(1, 2).contiguous().transpose(1, 2)), "dense"),
+                       (dict(x=x.transpose(1, 2).contiguous().transpose(1, 2)), "unit stride"),
+                       (dict(z=x[:, :2]), "z must"), (dict(D=A[:2]), "D must"), (dict(out=x), "overlap"),
+                       (dict(state_indices=torch.zeros(3, dtype=torch.int64, device="cuda")), "int32"),
+                       (dict(ssm_state=state[:2]), "slot"), (dict(dt=dt.cpu()), "on cpu")):
+        before = state.clone()
+        with pytest.raises(ValueError, match=what):
+            update(**over)
+        assert torch.equal(state, before)
+    with pytest.raises(NotImplementedError, match="training"):
+        update(x=x.clone().requires_grad_())
+    big = torch.zeros(3, 2, 300, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(NotImplementedError, match="256"):
+        update(B=big, C=big, ssm_state=torch.zeros(3, 4, 64, 300, device="cuda"))
+    with pytest.raises(ValueError, match="workspace"):
+        dc.causal_conv1d_selective_update(torch.zeros(3, 768, dtype=torch.bfloat16, device="cuda"),
+                                          torch.zeros(3, 768, 3, dtype=torch.bfloat16, device="cuda"),
+                                          torch.zeros(768, 4, dtype=torch.bfloat16, device="cuda"), None, None, dt, A, state,
+                                          groups=2, workspace=torch.zeros(5, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="packed"):
+        dc.selective_scan(x[:, None], dt[:, None], A, B[:, None], C[:, None],
+                          seq_starts=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="need an ssm_state"):
+        dc.selective_scan(x[:, None], dt[:, None], A, B[:, None], C[:, None], return_final_state=True,
+                          has_initial_state=torch.ones(3, dtype=torch.bool, device="cuda"))
