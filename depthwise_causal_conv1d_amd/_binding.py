@@ -9,40 +9,31 @@ ACTIVATIONS: dict = {}
 
 
 class on:
-    """``with on(device) as stream``: the device is current inside, ``stream`` its
-    current stream's handle."""
+    """``with on(device index):`` that device is current inside."""
 
-    __slots__ = ("index", "guard")
+    __slots__ = ("guard",)
 
-    def __init__(self, dev):
-        self.index = dev.index
+    def __init__(self, index):
+        # most calls are for the device that is current already
+        self.guard = None if index == _torch.cuda.current_device() else _torch.cuda.device(index)
 
     def __enter__(self):
-        current = _torch.cuda.current_device()
-        index = current if self.index is None else self.index
-        self.guard = None
-        if index != current:
-            self.guard = _torch.cuda.device(index)
+        if self.guard is not None:
             self.guard.__enter__()
-        return _stream(index)
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
 
-def _raw_stream():
-    """The handle of a device's current stream: without a stream object where this torch
-    has that (1.7 us less a call)."""
-    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
-    return raw or (lambda index: _torch.cuda.current_stream(index).cuda_stream)
-
-
-_torch = _stream = None
+_torch = stream = None
 
 
 def bind_torch(torch):
-    """Called when the library is loaded, so that importing the package does not import torch."""
-    global _torch, _stream
+    """Called when the library is first used, so that importing the package does not
+    import torch.  ``stream(index)`` is the handle of a device's current stream: without
+    a stream object where this torch has that (1.7 us less a call)."""
+    global _torch, stream
     _torch = torch
-    _stream = _raw_stream()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)

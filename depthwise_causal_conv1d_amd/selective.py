@@ -29,20 +29,22 @@ __all__ = [
 
 DCCONV_DTYPE_BF16, DCCONV_DTYPE_F32 = 0, 1
 
-_t = None  # torch, from the first call on
+_t = _BF16 = _F32 = _I32 = None  # torch and three of its types, from the first call on
 
 
 def _lib():
     """The loaded library, and torch in ``_t``."""
-    global _t
-    lib = _b.load()
     if _t is None:
-        import torch
+        _import_torch()
+    return _b.load()
 
-        _b.bind_torch(torch)
-        _t = torch
-    return lib
 
+def _import_torch():
+    global _t, _BF16, _F32, _I32
+    import torch
+
+    _b.bind_torch(torch)
+    _t, _BF16, _F32, _I32 = torch, torch.bfloat16, torch.float32, torch.int32
 
 
 def declare(lib: ctypes.CDLL) -> None:
@@ -120,89 +122,86 @@ def dcconv_w4_pack(*args) -> int:
 # ------------------------------------------------------------ tensor front end
 
 
+# A call's checks cost more than its launch if written carelessly: each of these reads an
+# attribute once, compares the device by its index, and leaves the wording to _refuse.
+
+
 def _bf16(name, t, shape, dev):
     """``t`` as a BF16 operand of ``shape`` whose last dimension is dense; its strides."""
-    if t.dtype is not _t.bfloat16:
-        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.shape != shape or t.device != dev or t.requires_grad:
-        _refuse(name, t, shape, dev)
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev or t.requires_grad:
+        _refuse(name, t, _BF16, shape, dev)
     stride = t.stride()
     if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
     return stride
 
 
-def _shaped(name, t, shape, dev):
-    if t.shape != shape or t.device != dev or t.requires_grad:
-        _refuse(name, t, shape, dev)
+def _vector(name, t, kind, n, dev):
+    """The address of a contiguous [n] operand, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not kind or t.shape != (n,) or t.get_device() != dev or t.requires_grad or not t.is_contiguous():
+        _refuse(name, t, kind, (n,), dev)
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _refuse(name, t, shape, dev):
+def _refuse(name, t, kind, shape, dev):
+    if kind is not None and t.dtype is not kind:
+        raise ValueError(f"{name} must be {str(kind)[6:]}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the rest on {dev}")
-    raise NotImplementedError(f"inference only: {name} requires grad (training is not served)")
-
-
-def _f32_vector(name, t, n, dev):
-    if t is None:
-        return None
-    if t.dtype is not _t.float32 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 [{n}] tensor")
-    _shaped(name, t, (n,), dev)
-    return t.data_ptr()
-
-
-def _i32_vector(name, t, n, dev):
-    if t is None:
-        return None
-    if t.dtype is not _t.int32 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor")
-    _shaped(name, t, (n,), dev)
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the rest on GPU {dev}")
+    if t.requires_grad:
+        raise NotImplementedError(f"inference only: {name} requires grad (training is not served)")
 
 
 def _dtype(name, t):
-    if t.dtype is _t.bfloat16:
+    kind = t.dtype
+    if kind is _BF16:
         return DCCONV_DTYPE_BF16
-    if t.dtype is _t.float32:
+    if kind is _F32:
         return DCCONV_DTYPE_F32
-    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    raise ValueError(f"{name} must be bfloat16 or float32, got {kind}")
 
 
 def _steps(dt, shape, dev):
+    """(dtype code, strides) of dt."""
     code = _dtype("dt", dt)
-    _shaped("dt", dt, shape, dev)
-    if dt.stride(-1) != 1 and dt.shape[-1] > 1:
+    if dt.shape != shape or dt.get_device() != dev or dt.requires_grad:
+        _refuse("dt", dt, None, shape, dev)
+    stride = dt.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError("dt must have unit stride along its heads")
-    return code
+    return code, stride
 
 
-def _pool(state, H, P, dev, K=None):
-    """(dtype code, S, slot stride, K) of an ssm_state [S, H, P, K]."""
+def _pool(state, H, P, K, dev):
+    """(dtype code, S, slot stride) of an ssm_state [S, H, P, K]."""
     code = _dtype("ssm_state", state)
-    if state.dim() != 4:
-        raise ValueError(f"ssm_state must be [S, H, P, K], got shape {tuple(state.shape)}")
-    S, K = state.shape[0], state.shape[3] if K is None else K
-    _shaped("ssm_state", state, (S, H, P, K), dev)
-    if S > 0 and not state[0].is_contiguous():
+    shape = state.shape
+    if shape[1:] != (H, P, K) or state.get_device() != dev or state.requires_grad:
+        _refuse("ssm_state", state, None, (shape[0], H, P, K), dev)
+    S, stride = shape[0], state.stride()
+    if stride[1:] != (P * K, K, 1) and S > 0 and not state[0].is_contiguous():
         raise ValueError("ssm_state must be dense inside a slot")
-    return code, S, (state.stride(0) if S > 1 else H * P * K), K
+    return code, S, (stride[0] if S > 1 else H * P * K)
 
 
 def _status(dev_status, dev):
     if dev_status is None:
         return None
-    if dev_status.dtype is not _t.int32 or dev_status.device != dev or dev_status.numel() < 1:
+    if dev_status.dtype is not _I32 or dev_status.get_device() != dev or dev_status.numel() < 1:
         raise ValueError("dev_status must be an int32 tensor on the operands' device")
     return dev_status.data_ptr()
 
 
 def _gpu(t):
-    if t.device.type != "cuda":
+    """The index of the GPU that holds ``t``."""
+    if not t.is_cuda:
         raise ValueError(f"tensors must be on a GPU, got {t.device}")
-    return t.device
+    return t.get_device()
 
 
 def selective_update(x, dt, A, B, C, ssm_state, *, D=None, z=None, dt_bias=None, dt_softplus=False,
@@ -222,22 +221,25 @@ def selective_update(x, dt, A, B, C, ssm_state, *, D=None, z=None, dt_bias=None,
     _, G, K = B.shape
     xs = _bf16("x", x, rows, dev)
     bs, cs = _bf16("B", B, (N, G, K), dev), _bf16("C", C, (N, G, K), dev)
-    code, S, slot, _ = _pool(ssm_state, H, P, dev, K)
-    dt_code = _steps(dt, (N, H), dev)
+    if ssm_state.dim() != 4:
+        raise ValueError(f"ssm_state must be [S, H, P, K], got shape {tuple(ssm_state.shape)}")
+    code, S, slot = _pool(ssm_state, H, P, K, dev)
+    dt_code, ds = _steps(dt, (N, H), dev)
     if A is None:
         raise ValueError("A must be given")
     zs = _bf16("z", z, rows, dev) if z is not None else (0, 0)
     if out is None:
-        out = _t.empty(rows, dtype=_t.bfloat16, device=dev)
-    os_ = _bf16("out", out, rows, dev)
-    with _b.on(dev) as stream:
+        out, os_ = _t.empty(rows, dtype=_BF16, device=x.device), (H * P, P)
+    else:
+        os_ = _bf16("out", out, rows, dev)
+    with _b.on(dev):
         rc = lib.dcconv_selective_update(
-            x.data_ptr(), N, H, P, xs[0], xs[1], dt.data_ptr(), dt_code, dt.stride(0),
-            _f32_vector("dt_bias", dt_bias, H, dev), int(bool(dt_softplus)), _f32_vector("A", A, H, dev),
-            B.data_ptr(), C.data_ptr(), G, K, bs[0], bs[1], cs[0], cs[1], _f32_vector("D", D, H, dev),
+            x.data_ptr(), N, H, P, xs[0], xs[1], dt.data_ptr(), dt_code, ds[0],
+            _vector("dt_bias", dt_bias, _F32, H, dev), int(bool(dt_softplus)), _vector("A", A, _F32, H, dev),
+            B.data_ptr(), C.data_ptr(), G, K, bs[0], bs[1], cs[0], cs[1], _vector("D", D, _F32, H, dev),
             None if z is None else z.data_ptr(), zs[0], zs[1], ssm_state.data_ptr(), code, S, slot,
-            _i32_vector("state_indices", state_indices, N, dev), out.data_ptr(), os_[0], os_[1],
-            _status(dev_status, dev), stream)
+            _vector("state_indices", state_indices, _I32, N, dev), out.data_ptr(), os_[0], os_[1],
+            _status(dev_status, dev), _b.stream(dev))
     _b.raise_for(rc)
     return out
 
@@ -246,7 +248,7 @@ def selective_update_workspace(rows, groups, device=None):
     """The zeroed int32 [rows * groups] counters of ``causal_conv1d_selective_update``,
     which leaves them zero: one buffer serves any number of successive calls."""
     _lib()
-    return _t.zeros(rows * groups, dtype=_t.int32, device="cuda" if device is None else device)
+    return _t.zeros(rows * groups, dtype=_I32, device="cuda" if device is None else device)
 
 
 def causal_conv1d_selective_update(xbc, conv_state, weight, bias, activation, dt, A, ssm_state, *, groups,
@@ -269,41 +271,42 @@ def causal_conv1d_selective_update(xbc, conv_state, weight, bias, activation, dt
     dev = _gpu(xbc)
     N = xbc.shape[0]
     _, H, P, K = ssm_state.shape
-    code, S, slot, _ = _pool(ssm_state, H, P, dev)
+    code, S, slot = _pool(ssm_state, H, P, K, dev)
     Dc = H * P + 2 * groups * K
-    _bf16("xbc", xbc, (N, Dc), dev)
-    if conv_state.dtype is not _t.bfloat16:
-        raise ValueError(f"conv_state must be bfloat16, got {conv_state.dtype}")
-    _shaped("conv_state", conv_state, (S, Dc, conv_state.shape[2]), dev)
-    _bf16("weight", weight, (Dc, weight.shape[1]), dev)
-    if not weight.is_contiguous():
+    xs = _bf16("xbc", xbc, (N, Dc), dev)
+    L, W = conv_state.shape[2], weight.shape[1]
+    if conv_state.dtype is not _BF16 or conv_state.shape != (S, Dc, L) or conv_state.get_device() != dev \
+            or conv_state.requires_grad:
+        _refuse("conv_state", conv_state, _BF16, (S, Dc, L), dev)
+    if _bf16("weight", weight, (Dc, W), dev)[0] != W and Dc > 1:
         raise ValueError("weight must be contiguous [Dc, W]")
     if bias is not None:
         _bf16("bias", bias, (Dc,), dev)
     if activation not in _b.ACTIVATIONS:
         raise ValueError(f"activation must be None, 'identity', 'silu' or 'swish', got {activation!r}")
-    dt_code = _steps(dt, (N, H), dev)
+    dt_code, ds = _steps(dt, (N, H), dev)
     if A is None:
         raise ValueError("A must be given")
     zs = _bf16("z", z, (N, H, P), dev) if z is not None else (0, 0)
     if workspace is None:
-        workspace = selective_update_workspace(N, groups, dev)
-    elif workspace.dtype is not _t.int32 or not workspace.is_contiguous() or workspace.device != dev \
+        workspace = selective_update_workspace(N, groups, xbc.device)
+    elif workspace.dtype is not _I32 or not workspace.is_contiguous() or workspace.get_device() != dev \
             or workspace.numel() < N * groups:
         raise ValueError(f"workspace must be a contiguous int32 tensor of at least {N * groups} zeros")
     if out is None:
-        out = _t.empty(N, H, P, dtype=_t.bfloat16, device=dev)
-    os_ = _bf16("out", out, (N, H, P), dev)
+        out, os_ = _t.empty(N, H, P, dtype=_BF16, device=xbc.device), (H * P, P)
+    else:
+        os_ = _bf16("out", out, (N, H, P), dev)
     st = conv_state.stride()
-    with _b.on(dev) as stream:
+    with _b.on(dev):
         rc = lib.dcconv_conv_selective_update(
-            xbc.data_ptr(), N, H, P, groups, K, xbc.stride(0), conv_state.data_ptr(), conv_state.shape[2], st[0],
-            st[1], st[2], weight.data_ptr(), weight.shape[1], None if bias is None else bias.data_ptr(),
-            _i32_vector("cache_seqlens", cache_seqlens, N, dev), _b.ACTIVATIONS[activation], dt.data_ptr(), dt_code,
-            dt.stride(0), _f32_vector("dt_bias", dt_bias, H, dev), int(bool(dt_softplus)),
-            _f32_vector("A", A, H, dev), _f32_vector("D", D, H, dev), None if z is None else z.data_ptr(), zs[0],
-            zs[1], ssm_state.data_ptr(), code, S, slot, _i32_vector("state_indices", state_indices, N, dev),
-            out.data_ptr(), os_[0], os_[1], workspace.data_ptr(), _status(dev_status, dev), stream)
+            xbc.data_ptr(), N, H, P, groups, K, xs[0], conv_state.data_ptr(), L, st[0],
+            st[1], st[2], weight.data_ptr(), W, None if bias is None else bias.data_ptr(),
+            _vector("cache_seqlens", cache_seqlens, _I32, N, dev), _b.ACTIVATIONS[activation], dt.data_ptr(), dt_code,
+            ds[0], _vector("dt_bias", dt_bias, _F32, H, dev), int(bool(dt_softplus)),
+            _vector("A", A, _F32, H, dev), _vector("D", D, _F32, H, dev), None if z is None else z.data_ptr(), zs[0],
+            zs[1], ssm_state.data_ptr(), code, S, slot, _vector("state_indices", state_indices, _I32, N, dev),
+            out.data_ptr(), os_[0], os_[1], workspace.data_ptr(), _status(dev_status, dev), _b.stream(dev))
     _b.raise_for(rc)
     return out
 
@@ -330,7 +333,7 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
     _, _, G, K = B.shape
     xs = _bf16("x", x, rows, dev)
     bs, cs = _bf16("B", B, (N, T, G, K), dev), _bf16("C", C, (N, T, G, K), dev)
-    dt_code = _steps(dt, (N, T, H), dev)
+    dt_code, ds = _steps(dt, (N, T, H), dev)
     if A is None:
         raise ValueError("A must be given")
     zs = _bf16("z", z, rows, dev) if z is not None else (0, 0, 0)
@@ -341,40 +344,41 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
         if seq_starts.dim() != 1 or seq_starts.shape[0] < 1:
             raise ValueError("seq_starts must be a contiguous int32 [n+1] tensor")
         n = seq_starts.shape[0] - 1
-    starts = _i32_vector("seq_starts", seq_starts, n + 1, dev)
+    starts = _vector("seq_starts", seq_starts, _I32, n + 1, dev)
     init = None
     if has_initial_state is not None:
-        if has_initial_state.dtype not in (_t.bool, _t.uint8) or not has_initial_state.is_contiguous():
+        if has_initial_state.dtype not in (_t.bool, _t.uint8):
             raise ValueError("has_initial_state must be a contiguous bool/uint8 [n] tensor")
-        _shaped("has_initial_state", has_initial_state, (n,), dev)
-        init = has_initial_state.data_ptr()
+        init = _vector("has_initial_state", has_initial_state, has_initial_state.dtype, n, dev)
     final = None
     if ssm_state is None and return_final_state:
         if has_initial_state is not None or state_indices is not None:
             raise ValueError("has_initial_state and state_indices need an ssm_state")
-        ssm_state = final = _t.empty(n, H, P, K, dtype=_t.float32, device=dev)
+        ssm_state = final = _t.empty(n, H, P, K, dtype=_F32, device=x.device)
     code, S, slot, pool = DCCONV_DTYPE_F32, 0, 0, None
     if ssm_state is not None:
-        code, S, slot, _ = _pool(ssm_state, H, P, dev, K)
+        if ssm_state.dim() != 4:
+            raise ValueError(f"ssm_state must be [S, H, P, K], got shape {tuple(ssm_state.shape)}")
+        code, S, slot = _pool(ssm_state, H, P, K, dev)
         pool = ssm_state.data_ptr()
     if out is None:
-        out = _t.empty(rows, dtype=_t.bfloat16, device=dev)
-    os_ = _bf16("out", out, rows, dev)
+        out, os_ = _t.empty(rows, dtype=_BF16, device=x.device), (T * H * P, H * P, P)
+    else:
+        os_ = _bf16("out", out, rows, dev)
     need = lib.dcconv_selective_scan_workspace(n, T, H, P, G, K, int(starts is not None))
     if workspace is None:
-        workspace = _t.empty(need, dtype=_t.uint8, device=dev) if need else None
-    elif workspace.dtype is not _t.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        workspace = _t.empty(need, dtype=_t.uint8, device=x.device) if need else None
+    elif workspace.dtype is not _t.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be a contiguous uint8 tensor on x's device")
-    ds = dt.stride()
-    with _b.on(dev) as stream:
+    with _b.on(dev):
         rc = lib.dcconv_selective_scan(
             x.data_ptr(), n, T, H, P, xs[0], xs[1], xs[2], dt.data_ptr(), dt_code, ds[0], ds[1],
-            _f32_vector("dt_bias", dt_bias, H, dev), int(bool(dt_softplus)), _f32_vector("A", A, H, dev),
+            _vector("dt_bias", dt_bias, _F32, H, dev), int(bool(dt_softplus)), _vector("A", A, _F32, H, dev),
             B.data_ptr(), C.data_ptr(), G, K, bs[0], bs[1], bs[2], cs[0], cs[1], cs[2],
-            _f32_vector("D", D, H, dev), None if z is None else z.data_ptr(), zs[0], zs[1], zs[2], starts, pool, code,
-            S, slot, _i32_vector("state_indices", state_indices, n, dev), init, out.data_ptr(), os_[0], os_[1],
+            _vector("D", D, _F32, H, dev), None if z is None else z.data_ptr(), zs[0], zs[1], zs[2], starts, pool, code,
+            S, slot, _vector("state_indices", state_indices, _I32, n, dev), init, out.data_ptr(), os_[0], os_[1],
             os_[2], None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel(), _status(dev_status, dev), stream)
+            0 if workspace is None else workspace.numel(), _status(dev_status, dev), _b.stream(dev))
     _b.raise_for(rc)
     return (out, final) if final is not None else out
 
@@ -387,9 +391,9 @@ def w4_pack(codes):
         raise ValueError("codes must be a contiguous uint8 [N, K] tensor")
     dev = _gpu(codes)
     N, K = codes.shape
-    q = _t.empty(-(-N // 16), -(-K // 128), 64, 16, dtype=_t.uint8, device=dev)
-    with _b.on(dev) as stream:
-        rc = lib.dcconv_w4_pack(codes.data_ptr(), N, K, q.data_ptr(), stream)
+    q = _t.empty(-(-N // 16), -(-K // 128), 64, 16, dtype=_t.uint8, device=codes.device)
+    with _b.on(dev):
+        rc = lib.dcconv_w4_pack(codes.data_ptr(), N, K, q.data_ptr(), _b.stream(dev))
     _b.raise_for(rc)
     return q
 
@@ -407,27 +411,31 @@ def w4_matvec(x, qweight, scales, zeros=None, bias=None, *, group_size, out=None
     M, K = x.shape
     N = scales.shape[1]
     groups = -(-K // group_size) if group_size > 0 else 0
-    _bf16("x", x, (M, K), dev)
-    _bf16("scales", scales, (groups, N), dev)
-    if not scales.is_contiguous():
+    xs = _bf16("x", x, (M, K), dev)
+    if _bf16("scales", scales, (groups, N), dev)[0] != N and groups > 1:
         raise ValueError("scales must be contiguous")
-    if qweight.dtype is not _t.uint8 or not qweight.is_contiguous():
-        raise ValueError("qweight must be a contiguous uint8 tensor")
-    _shaped("qweight", qweight, (-(-N // 16), -(-K // 128), 64, 16), dev)
+    shape = (-(-N // 16), -(-K // 128), 64, 16)
+    if qweight.dtype is not _t.uint8 or qweight.shape != shape or qweight.get_device() != dev:
+        _refuse("qweight", qweight, _t.uint8, shape, dev)
+    if not qweight.is_contiguous():
+        raise ValueError("qweight must be contiguous")
     if zeros is not None:
-        if zeros.dtype is not _t.uint8 or not zeros.is_contiguous():
-            raise ValueError("zeros must be a contiguous uint8 tensor")
-        _shaped("zeros", zeros, (groups, N), dev)
+        if zeros.dtype is not _t.uint8 or zeros.shape != (groups, N) or zeros.get_device() != dev:
+            _refuse("zeros", zeros, _t.uint8, (groups, N), dev)
+        if not zeros.is_contiguous():
+            raise ValueError("zeros must be contiguous")
     if bias is not None:
         _bf16("bias", bias, (N,), dev)
     if out is None:
-        out = _t.empty(M, N, dtype=_t.bfloat16, device=dev)
+        out, pitch = _t.empty(M, N, dtype=_BF16, device=x.device), N
     else:
-        _bf16("out", out, (M, N), dev)
-    with _b.on(dev) as stream:
+        pitch = _bf16("out", out, (M, N), dev)[0]
+        if M <= 1:
+            pitch = N
+    with _b.on(dev):
         rc = lib.dcconv_w4_matvec(
-            x.data_ptr(), M, K, x.stride(0), qweight.data_ptr(), N, scales.data_ptr(),
+            x.data_ptr(), M, K, xs[0], qweight.data_ptr(), N, scales.data_ptr(),
             None if zeros is None else zeros.data_ptr(), group_size, None if bias is None else bias.data_ptr(),
-            out.data_ptr(), out.stride(0) if M > 1 else N, stream)
+            out.data_ptr(), pitch, _b.stream(dev))
     _b.raise_for(rc)
     return out
