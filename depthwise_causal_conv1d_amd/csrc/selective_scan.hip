@@ -95,6 +95,7 @@ __device__ __forceinline__ u32x4 load_columns(const uint16_t *at, int pitch) {
 }
 
 constexpr float kHuge = 3.0e38f;
+constexpr float kNone = -160.0f;
 __device__ __forceinline__ bool is_finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
 
 // acc + the two BF16 values of w.
@@ -477,8 +478,12 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
         float d = __uint_as_float(p.dt_f32 ? v : v << 16) + dt_bias;
         if (p.dt_softplus) d = softplus(d);
         if (lane >= min(left, kChunk)) d = 0.0f;
+        // 2^kNone is zero: a step that decays more counts as that, so that the differences of
+        // the sums of the steps behind it keep their bits (a NaN stays)
+        float rate = d * a2;
+        if (rate < kNone) rate = kNone;
         float upto, behind, total;
-        wave_sums(d * a2, lane, &upto, &behind, &total);
+        wave_sums(rate, lane, &upto, &behind, &total);
         float *to = steps + ((s_slot * plan.heads + job) * kStepRows) * kChunk + lane;
         if (lane < kChunk) {
             to[0] = upto;

@@ -231,6 +231,17 @@ def test_scan_keeps_bad_values_where_the_recurrence_takes_them(bad):
             assert torch.equal(case.pool, states) and torch.equal(out[0, 98:], want[0, 98:])
 
 
+@pytest.mark.parametrize("step", [300.0, 1e6, 3e37])
+@pytest.mark.parametrize("state", [torch.float32, torch.bfloat16])
+def test_scan_after_a_step_that_decays_everything(step, state):
+    """A step whose decay is zero leaves the decays between the tokens behind it as exact as
+    any others, though a chunk's sum of dt A has grown to the size of that step's."""
+    case = Scan(21, [70], 3, 64, 1, 64, state=state, init=[True], soft=False, dt_f32=True)
+    case.x[0, 40] *= 1.0 / step
+    case.dt[0, 40] = step
+    case.check()
+
+
 def test_scan_more_units_than_blocks():
     n = (1 << 20) + 5
     x = torch.randn(n, 1, 1, 2, device="cuda").to(torch.bfloat16)
