@@ -719,8 +719,12 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
 
 // The states ahead of every segment, in place: position u + 1 of the workspace
 // holds what segment u built up from zero and its decay.  A thread carries VEC
-// neighbouring values along a sequence's segments.
+// neighbouring values along a sequence's segments, and reads kJoinAhead segments at a
+// time: as the values it writes lie in the same array, reads one by one would each wait
+// for the write before (the whole call on 16381 tokens of 24 heads: 98.1 us reading one,
+// 94.8 four, 94.5 eight, 95.4 sixteen).
 constexpr int kJoinBlock = 256;
+constexpr int kJoinAhead = 8;
 template <int VEC>
 __global__ __launch_bounds__(kJoinBlock) void selective_join_kernel(const SelectiveScanParams p, const ScanPlan plan,
                                                                     int blocks_per_seq) {
@@ -750,18 +754,26 @@ __global__ __launch_bounds__(kJoinBlock) void selective_join_kernel(const Select
             typedef float fvec __attribute__((ext_vector_type(VEC)));
             fvec *ws = reinterpret_cast<fvec *>(p.workspace + u0 * hpk + e);
             const float *dec = p.workspace + plan.slots * hpk + (int64_t)u0 * p.h + e / pk;
-#pragma unroll 4
-            for (int j = 0; j < count; ++j) {
-                fvec v;
-                if (j > 0) {
-                    v = ws[j * (hpk / VEC)];
-                    const float d = dec[(int64_t)j * p.h];
+            for (int j0 = 0; j0 < count; j0 += kJoinAhead) {
+                fvec v[kJoinAhead];
+                float d[kJoinAhead];
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) run[i] = __builtin_fmaf(run[i], d, v[i]);
+                for (int q = 0; q < kJoinAhead; ++q) {
+                    const int j = min(j0 + q, count - 1);
+                    v[q] = ws[j * (hpk / VEC)];
+                    d[q] = dec[(int64_t)j * p.h];
                 }
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) v[i] = run[i];
-                ws[j * (hpk / VEC)] = v;
+                for (int q = 0; q < kJoinAhead; ++q) {
+                    const int j = j0 + q;
+                    if (j >= count) break;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        if (j > 0) run[i] = __builtin_fmaf(run[i], d[q], v[q][i]);
+                        v[q][i] = run[i];
+                    }
+                    ws[j * (hpk / VEC)] = v[q];
+                }
             }
         }
     });
