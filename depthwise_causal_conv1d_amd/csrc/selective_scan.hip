@@ -780,18 +780,33 @@ __global__ __launch_bounds__(kJoinBlock) void selective_join_kernel(const Select
 }
 
 // Three blocks a CU fill the card.  With fewer than one a CU, sequences are cut into
-// segments, as many as fill it but not below kMinSegment tokens: a segment costs
-// another pass over its x and B, and a state's round trip through memory.  Packed
-// sequences, whose lengths the host does not know, are cut where they are longer than
-// kLongSequence even if there are enough of them, so that one does not outlast the rest.
+// segments, as many as fill it (16381 tokens of 24 heads: 94 us; with 640 and 512 blocks
+// 106 and 111) but not below kMinSegment tokens (with 64, 96, 128 and 256: 400 tokens of
+// 24 heads 25, 27, 29 and 39 us, 1000 tokens 38, 36, 34 and 43).  Packed sequences, whose
+// lengths the host does not know, are cut where they are longer than kLongSequence even
+// if there are enough of them, so that one does not outlast the rest (16 of up to 1967
+// tokens, 60 heads: 186 us whole, 254 to 270 cut at 768 to 1536).
 constexpr int64_t kFullGrid = 768;
 constexpr int64_t kEnoughBlocks = 256;
-constexpr int64_t kMinSegment = 256;
+constexpr int64_t kMinSegment = 96;
 constexpr int64_t kLongSequence = 2048;
+// Runs of blocks that share B and C, at least: 8 x 2048 tokens of 96 heads take 200 us
+// with 16, 32 and 64, and 224 with every block a run.
 constexpr int64_t kRuns = 32;
 constexpr int64_t kJoinBlocks = 2048;  // of the join, over all sequences
 
-ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, bool packed) {
+// Whether cutting the longest sequence at `seg` saves time: a chunk takes about 1.9 us,
+// and 0.6 of that again in the pass that builds up the segments' states, which costs two
+// more launches and moves each state four times (24 heads of 64 x 128, whole and cut: 320
+// tokens 25 and 26 us, 400 tokens 31 and 27, 1000 tokens 66 and 36; 8 x 400 tokens 32 and
+// 50, 8 x 700 tokens 49 and 56).
+constexpr int64_t kChunkNs = 1900, kCutNs = 10000, kCutChunkNs = kChunkNs * 8 / 5, kStatesPerNs = 312;
+bool cut_pays(int64_t longest, int64_t seg, int64_t slots, int64_t state) {
+    const auto chunks = [](int64_t tokens) { return (tokens + kChunk - 1) / kChunk; };
+    return kChunkNs * chunks(longest) > kCutNs + kCutChunkNs * chunks(seg) + slots * state / kStatesPerNs;
+}
+
+ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k, bool packed) {
     ScanPlan plan;
     plan.np = (int32_t)((p + kUnitP - 1) / kUnitP);
     plan.quads = (int32_t)((h / g * plan.np + kScanWaves - 1) / kScanWaves);
@@ -805,9 +820,11 @@ ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, bool p
     } else {
         const int64_t each = kFullGrid / ((packed ? 1 : n) * per_slot);  // segments of the t axis
         seg = each > 1 ? (t + each - 1) / each : t;
+        if (seg < kMinSegment) seg = kMinSegment;
+        // (packed: the longest of n is taken for twice the mean)
+        if (!cut_pays(packed && n > 2 ? 2 * t / n : t, seg, packed ? t / seg + n : n * ((t + seg - 1) / seg), h * p * k)) seg = t;
     }
     seg = (seg + kChunk - 1) / kChunk * kChunk;
-    if (seg < kMinSegment) seg = kMinSegment;
     if (seg >= t) seg = (t + kChunk - 1) / kChunk * kChunk;
     if (seg < kChunk) seg = kChunk;
     plan.seg = (int32_t)seg;
@@ -890,12 +907,12 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c, int64_t heads) {
 }  // namespace
 
 int64_t selective_scan_workspace_floats(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k, bool packed) {
-    const ScanPlan plan = make_plan(n, t, h, p, g, packed);
+    const ScanPlan plan = make_plan(n, t, h, p, g, k, packed);
     return plan.split ? plan.slots * (h * p * k + h) : 0;
 }
 
 hipError_t launch_selective_scan(const SelectiveScanParams &p, hipStream_t stream, const char **kernel_name) {
-    const ScanPlan plan = make_plan(p.n, p.t, p.h, p.p, p.g, p.starts != nullptr);
+    const ScanPlan plan = make_plan(p.n, p.t, p.h, p.p, p.g, p.k, p.starts != nullptr);
     const int64_t heads = p.h / p.g;
     const bool wide = p.p % 8 == 0 && p.k % 8 == 0 && rows16(p.x, p.xs_n, p.xs_t, p.xs_h, heads) &&
                       rows16(p.b, p.bs_n, p.bs_t, p.bs_g, 1) && rows16(p.c, p.cs_n, p.cs_t, p.cs_g, 1) &&
