@@ -16,17 +16,28 @@
 //
 // A wave owns 16 of a head's p and all of the state's k: H stays in its FP32
 // accumulators for the whole sequence, already in the lane order that the next
-// product reads it in (below).  A block is eight such waves of one group (two heads
-// at p = 64), which share the chunk's B and C in LDS and the products C B^T: the
-// lower triangle's three tiles, scaled for each head of the block, are shared out.
+// product reads it in (below).  A block is four such waves of one group (one head at
+// p = 64), which share the chunk's B and C in LDS and the products C B^T: the lower
+// triangle's three tiles, scaled for each head of the block, are shared out.  (Blocks of
+// eight and twelve waves, which share more, took 344 and 244 us where four took 229.)
 //
-// One barrier a chunk: between two of them a wave finishes chunk i (the product with
-// X, H', the outputs), starts chunk i + 1 (C H^T, its tiles of C B^T), puts chunk
-// i + 2's B and C into LDS and requests chunk i + 3's.  B is kept in three places in
-// LDS, C and L o C B^T in two, and x, which a wave reads alone, in one: 70 KiB at
-// k = 128 with two heads, so that two blocks fit a CU, and fewer than 128 registers,
-// so that all their waves run.  (Chunks of 64 tokens need more of both, and took
-// three barriers: 286 us against 2xx for 8 x 2048 tokens of 96 heads.)
+// Two barriers a chunk: waves finish chunk i (the product with X, H', the outputs); then
+// they put chunk i + 1's x and z and chunk i + 2's B and C into LDS, request the chunk
+// behind each, and start chunk i + 1 (C H^T, its tiles of C B^T).  So B and C are kept in
+// two places in LDS, x, z (and the outputs, in z's place) and L o C B^T in one: 49 KiB
+// at k = 128, and 150 registers, for three blocks a CU.  (Four blocks need 128 registers
+// and spill: 410 to 440 us against 200.  Chunks of 64 tokens need more of both and took
+// 286 us where 32 took 270.)  x, z and the outputs move in whole rows of the block, 128
+// bytes at p = 64: a wave's own 32 bytes a row cost 256 us against 229.
+//
+// What bounds it.  8 x 2048 tokens of 96 heads, 64 x 128 in 8 groups, with BF16 states:
+// 200 us, 687 MB at 3.4 TB/s and 64 GFLOP at 320 TFLOP/s, where the memory's rate would
+// allow 117 us.  The vector units are busy for 54 % of the time, LDS for 44 %, the matrix
+// cores for 15 %: a chunk is a chain of products, exponentials and LDS round trips, about
+// 3.1 us long, and twelve waves a CU do not hide all of it.  16 packed sequences of up to
+// 1967 tokens (60 heads, F32 states): 188 us, 427 MB at 2.3 TB/s, the longest sequence's
+// chunks one after the other.  One sequence of 16381 tokens of 24 heads: 96 us, 119 MB, of
+// them about 38 the segments' states and 10 the join.  37 tokens: 10.3 us, two chunks' latency and the launch.
 //
 // Layouts.  v_mfma_f32_16x16x32_bf16 takes, in lane l with r = l & 15 and g = l >> 4,
 // row (column) r of an operand at inner indices 8 g .. 8 g + 7, and leaves column r,
@@ -45,7 +56,9 @@
 // FP32.  The scaled products L o C B^T and the copy of H that C reads are rounded to
 // BF16 (each about as much as the BF16 output's own rounding).  The scaled x that
 // enters H is split into SPLIT BF16 parts whose products are added up: three carry all
-// 24 bits, for states that are handed out in FP32.
+// 24 bits, for states that are handed out in FP32.  One part is what a BF16 state needs:
+// against 64 bits the outputs' error is then 0.0023 of their size, 0.0019 with three and
+// 0.0017 for the best rounding (two parts: 222 us where one took 209).
 #include "selective_common.h"
 
 namespace dcconv {

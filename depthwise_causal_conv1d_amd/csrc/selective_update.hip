@@ -15,12 +15,21 @@
 // for all of the block's items at once, as FP32.  All arithmetic is FP32; a BF16 state
 // is rounded when it is stored, after C has read the unrounded value.
 //
+// 256 rows of 96 heads, 64 x 128, F32 states: 258 us, 1621 MB at 6.3 TB/s (a plain copy
+// reaches 5.9).  61 rows of 30 heads, 80 x 72, BF16 states: 14.4 us, 38 MB at 2.7 TB/s:
+// items whose rows of 144 bytes fill neither the 16 lanes nor a cache line.  4 rows of 24
+// heads: 5 us, a launch and one item's latency.
+//
 // The fused form computes x, B and C as the width-4 convolution of its channels
 // (kept in FP32, not rounded to BF16 between the two operators).  Every block of
 // a group needs the group's B and C channels (several items a block make that cheap),
 // and the convolution state of those is advanced in place: each block counts itself in
 // `arrivals[row, group]` once it has read them, and the block that completes the count
 // writes their state and sets the count back to zero.  Nothing waits on the count.
+// 256 rows of 96 heads with BF16 states: 155 us, 841 MB at 5.4 TB/s.  64 rows of 60
+// heads in one group, F32 states, some padding: 54.7 us, 225 MB at 4.1 TB/s, as the group's
+// B and C are convolved by 30 blocks a row.  One row of 24 heads: 7.8 us, the loads of the
+// taps and then of the state behind the launch.
 #include "selective_common.h"
 
 namespace dcconv {

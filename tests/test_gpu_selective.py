@@ -1,7 +1,7 @@
 """The state-space recurrence on the GPU against its 64-bit form: whole sequences, one
 token, and one token with the convolution ahead of it.
 
-Sizes sit at and around the kernels' edges (chunks of 64 tokens, tiles of 16 state
+Sizes sit at and around the kernels' edges (chunks of 32 tokens, tiles of 16 state
 values and 32 channels, segments of long sequences, more units than blocks), with
 strided views, padding and rejected rows, empty sequences and both state types.  The
 bounds are derived in ``selective_reference``.
