@@ -315,9 +315,9 @@ extern "C" int dcconv_selective_scan(const void *x, int64_t n, int64_t t, int64_
                                      int64_t ss_s, const int32_t *state_indices, const uint8_t *has_initial_state,
                                      void *out, int64_t os_n, int64_t os_t, int64_t os_h, void *workspace,
                                      int64_t workspace_bytes, int32_t *dev_status, void *stream) {
-    const bool stateless = ssm_state == nullptr && s == 0 && state_indices == nullptr;
-    if (stateless && has_initial_state != nullptr)
-        return fail(DCCONV_EINVAL, "has_initial_state needs an ssm_state");
+    const bool stateless = ssm_state == nullptr && s == 0;
+    if (stateless && (has_initial_state != nullptr || state_indices != nullptr))
+        return fail(DCCONV_EINVAL, "has_initial_state and state_indices need an ssm_state");
     int rc = check_shapes(n, h, p, g, k, dt_dtype, state_dtype, s, ss_s, state_indices != nullptr, stateless);
     if (rc != DCCONV_OK) return rc;
     if (t < 0) return fail(DCCONV_EINVAL, "t (tokens) must be >= 0, got %lld", (long long)t);

@@ -351,9 +351,9 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
             raise ValueError("has_initial_state must be a contiguous bool/uint8 [n] tensor")
         init = _vector("has_initial_state", has_initial_state, has_initial_state.dtype, n, dev)
     final = None
+    if ssm_state is None and (has_initial_state is not None or state_indices is not None):
+        raise ValueError("has_initial_state and state_indices need an ssm_state")
     if ssm_state is None and return_final_state:
-        if has_initial_state is not None or state_indices is not None:
-            raise ValueError("has_initial_state and state_indices need an ssm_state")
         ssm_state = final = _t.empty(n, H, P, K, dtype=_F32, device=x.device)
     code, S, slot, pool = DCCONV_DTYPE_F32, 0, 0, None
     if ssm_state is not None:
