@@ -44,7 +44,8 @@ def _import_torch():
     import torch
 
     _b.bind_torch(torch)
-    _t, _BF16, _F32, _I32 = torch, torch.bfloat16, torch.float32, torch.int32
+    _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+    _t = torch  # last: another thread's first call goes by it
 
 
 def declare(lib: ctypes.CDLL) -> None:

@@ -2,6 +2,8 @@
 it: no GPU.  Made-up device addresses are never dereferenced, so calls with them run only
 where no GPU is visible.
 """
+import sys
+
 import pytest
 import torch
 
@@ -19,3 +21,29 @@ def test_scan_without_a_pool_refuses_what_selects_from_one(over, packed):
     """No slot exists that an index could select: not a call whose sequences are all padding."""
     starts = dict(seq_starts=P[11]) if packed else {}
     refused(scan, dict(ssm_state=None, s=0, **over, **starts), dc.DCCONV_EINVAL, "ssm_state")
+
+
+def test_a_second_thread_finds_torch_only_with_its_types(monkeypatch):
+    """A first call publishes torch in ``_t``, which other threads take as the sign that all
+    of the module's names are set: so they are, at every step on the way."""
+    from depthwise_causal_conv1d_amd import _binding, selective
+
+    for module, names in ((selective, ("_t", "_BF16", "_F32", "_I32")), (_binding, ("_torch", "stream"))):
+        for name in names:
+            monkeypatch.setattr(module, name, None)
+    rest = ((selective, "_BF16"), (selective, "_F32"), (selective, "_I32"), (_binding, "_torch"), (_binding, "stream"))
+    missing = []
+
+    def trace(frame, event, arg):
+        frame.f_trace_opcodes = True
+        if selective._t is not None:
+            missing.extend(name for module, name in rest if getattr(module, name) is None)
+        return trace
+
+    before = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        selective._import_torch()
+    finally:
+        sys.settrace(before)
+    assert selective._t is torch and not missing
