@@ -333,8 +333,10 @@ int dcconv_conv_selective_update(const void *xbc, int64_t n, int64_t h, int64_t 
  *             state there.  An empty sequence leaves its initial state or zeros.
  * workspace   dcconv_selective_scan_workspace() bytes, 16-byte aligned; its contents
  *             need not be kept and are not read from one call to the next.
- * A finite dt is assumed; an infinity or NaN in x, B, C or z reaches the outputs and
- * the state that the recurrence takes it to, and no other.
+ * A finite dt is assumed.  The outputs and state values that the recurrence takes an
+ * infinity or NaN of x, B, C or z to are not finite, and no others are.  An infinity
+ * may become a NaN there (the one-token entry points keep it): it is a term of matrix
+ * products, whose other operand may be zero or split into parts of either sign.
  * Returns as dcconv_selective_update.
  */
 int dcconv_selective_scan(const void *x, int64_t n, int64_t t, int64_t h, int64_t p,

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import depthwise_causal_conv1d_amd as dc
-from test_gpu_selective import Scan
+from selective_reference import U, close, recurrence
+from test_gpu_selective import Scan, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +26,25 @@ def test_scan_without_a_pool_refuses_what_selects_from_one(more, packed):
     for final in (False, True):
         with pytest.raises(ValueError, match="need an ssm_state"):
             case.call(return_final_state=final)
+
+
+@pytest.mark.parametrize("name", ["x", "B"])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("state", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,at", [(70, 3), (70, 37), (70, 69), (700, 100), (700, 650)])
+def test_scan_is_not_finite_where_the_recurrence_is_not(name, bad, state, tokens, at):
+    """An infinity or NaN of x or B is one or the other in the state and the outputs that the
+    recurrence takes it to, and every other value is as close as ever."""
+    case = Scan(51, [tokens], 2, 64, 1, 64, state=state, init=[True])
+    getattr(case, name)[0, at, 0, 5] = bad
+    out = case.call()
+    cut = [f64(t[0]) for t in (case.x, case.dt, case.B, case.C, case.z)]
+    y, ya, h, ha = recurrence(cut[0], cut[1], f64(case.A), cut[2], cut[3], f64(case.D), cut[4], f64(case.bias), True,
+                              f64(case.state[0]))
+    keep = torch.isfinite(h)
+    assert not keep.all() and torch.equal(torch.isfinite(case.pool[0]).cpu(), keep)
+    bound = 2.0 ** -17 * ha if state == torch.float32 else U * h.abs() + (U + 2.0 ** -13) * ha
+    close(case.pool[0].cpu()[keep], h[keep], bound[keep], "finite states")
+    keep = torch.isfinite(y)
+    assert not keep.all() and torch.equal(torch.isfinite(out[0]).cpu(), keep)
+    close(out[0].cpu()[keep], y[keep], (U * y.abs() + (U + 2.0 ** -13) * ya)[keep], "finite outputs")
