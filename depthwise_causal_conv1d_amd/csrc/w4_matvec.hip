@@ -7,15 +7,18 @@
 // keep it so.  The codes come in tiles of 16 outputs by 128 inputs in the order that
 // lanes use them: one coalesced 16-byte load is a lane's share of four matrix
 // instructions.  A code becomes a BF16 without a conversion: or-ed into the mantissa
-// of 128 it reads 128 + q, exactly, two codes at a time (an and-or, and a shift for
-// three of four), because a word's nibbles i and i + 4 hold neighbouring inputs.  And
-// the matrix cores do the multiplying for one row of x as for sixteen; they also sum
-// x itself against ones, and per group
+// of s = 2^-8 it reads s (1 + q / 128), exactly, two codes at a time (an and-or, and a
+// shift for three of four), because a word's nibbles i and i + 4 hold neighbouring
+// inputs.  And the matrix cores do the multiplying for one row of x as for sixteen; they
+// also sum x itself times s, and per group
 //
-//     sum x (q - zero) = sum x (128 + q) - (128 + zero) * sum x
+//     s sum x (q - zero) / 128 = sum x s (1 + q / 128) - (1 + zero / 128) * sum x s
 //
 // takes the offset out again in FP32 (it costs about 5 of FP32's 24 bits, of which a
-// BF16 result keeps 8).  Products and sums are FP32 throughout; out is rounded once.
+// BF16 result keeps 8).  The factor s / 128 = 2^-15, undone when the waves are joined,
+// leaves room for a group's sum of the largest x, which a small scale may bring back into
+// range; sums of x below 2^-117 lose bits to it.  Products and sums are FP32 throughout;
+// out is rounded once.
 //
 // A block owns a tile of outputs and its waves share out the inputs, 128 at a
 // time; they are joined through LDS in the order of the waves.
@@ -35,17 +38,19 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kTileN = 16, kTileK = 128;
 constexpr int kMaxW4Waves = 16;
+constexpr uint32_t kUnit = 0x3b80;  // 2^-8 as BF16
+constexpr float kBack = 32768.0f;   // a code's step there is 2^-15
 
 __device__ __forceinline__ f32x4_t mfma(u32x4 a, u32x4 b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
 }
 
-// Eight codes -> eight BF16 128 + q: nibbles i and i + 4 become word i.
+// Eight codes -> eight BF16 2^-8 (1 + q / 128): nibbles i and i + 4 become word i.
 __device__ __forceinline__ u32x4 expand(uint32_t w) {
     u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    for (int i = 0; i < 4; ++i) v[i] = ((w >> (4 * i)) & 0x000f000fu) | kUnit * 0x10001u;
     return v;
 }
 
@@ -116,7 +121,7 @@ __global__ __launch_bounds__(kMaxW4Waves *kWave) void w4_matvec_kernel(const W4P
         const int m = m0 + 16 * b + r;
         row[b] = m < p.m ? 2u * ((uint32_t)m * (uint32_t)p.xs_m + 8u * (uint32_t)g) : kNowhere;
     }
-    const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    const u32x4 units = {kUnit * 0x10001u, kUnit * 0x10001u, kUnit * 0x10001u, kUnit * 0x10001u};
     const u32x4 *tiles = reinterpret_cast<const u32x4 *>(p.q) + (int64_t)nt * ktiles * kWave;
 
     for (int kt = wave; kt < ktiles; kt += waves) {
@@ -145,16 +150,16 @@ __global__ __launch_bounds__(kMaxW4Waves *kWave) void w4_matvec_kernel(const W4P
                 const u32x4 w = expand(q[s * STEPS + i]);
 #pragma unroll
                 for (int b = 0; b < MT; ++b) {
-                    sum[b] = mfma(x[b][s * STEPS + i], ones, sum[b]);
+                    sum[b] = mfma(x[b][s * STEPS + i], units, sum[b]);
                     acc[b] = mfma(x[b][s * STEPS + i], w, acc[b]);
                 }
             }
-            const float sc = bf16_bits_to_f32(scale[s]), offset = -sc * (128.0f + (float)zero[s]);
+            const float sc = bf16_bits_to_f32(scale[s]), offset = -1.0f - (float)zero[s] * 0x1p-7f;
 #pragma unroll
             for (int b = 0; b < MT; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    total[b][i] = __builtin_fmaf(offset, sum[b][i], __builtin_fmaf(sc, acc[b][i], total[b][i]));
+                    total[b][i] = __builtin_fmaf(sc, __builtin_fmaf(offset, sum[b][i], acc[b][i]), total[b][i]);
         }
     }
 
@@ -167,8 +172,9 @@ __global__ __launch_bounds__(kMaxW4Waves *kWave) void w4_matvec_kernel(const W4P
     for (int e = threadIdx.x; e < MT * 256; e += blockDim.x) {
         const int col = nt * kTileN + (e & 15), m = m0 + (e >> 4);
         if (col >= p.n || m >= p.m) continue;
-        float v = p.bias != nullptr ? bf16_bits_to_f32(p.bias[col]) : 0.0f;
+        float v = 0.0f;
         for (int w = 0; w < waves; ++w) v += joined[w * MT * 256 + e];
+        v = __builtin_fmaf(v, kBack, p.bias != nullptr ? bf16_bits_to_f32(p.bias[col]) : 0.0f);
         p.out[(int64_t)m * p.os_m + col] = f32_to_bf16_bits(v);
     }
 }
