@@ -26,10 +26,11 @@ def quantize(w, group_size):
     N, K = w.shape
     groups = -(-K // group_size)  # the last may be shorter
     v = torch.nn.functional.pad(w, (0, groups * group_size - K)).view(N, groups, group_size)
-    lo, hi = v.amin(-1), v.amax(-1)
+    lo, hi = v.amin(-1).clamp(max=0), v.amax(-1).clamp(min=0)   # a zero point is a code: zero is in the range
     scale = ((hi - lo) / 15).to(torch.bfloat16)
-    zero = (-lo / scale.float()).round().clamp(0, 15)
-    codes = (v / scale.float()[..., None] + zero[..., None]).round().clamp(0, 15)
+    step = torch.where(scale > 0, scale.float(), 1.0)            # (a group of zeros has none)
+    zero = (-lo / step).round().clamp(0, 15)
+    codes = (v / step[..., None] + zero[..., None]).round().clamp(0, 15)
     return (dc.w4_pack(codes.to(torch.uint8).view(N, -1)[:, :K].contiguous()), scale.t().contiguous(),
             zero.to(torch.uint8).t().contiguous())
 
