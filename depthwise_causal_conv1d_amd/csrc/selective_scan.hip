@@ -90,6 +90,8 @@ struct ScanPlan {
     int32_t run;     // of them that follow each other on one XCD
     int32_t parts;   // runs a group takes
     int32_t heads;   // most heads of one block
+    int32_t places;  // states in the workspace
+    bool sparse;     // packed: see first_place
     bool split;      // some sequence may have more than one segment
 };
 
@@ -136,8 +138,20 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 struct Segment {
     int seq, first, last, index, count;  // tokens [first, last) of sequence seq; segment `index` of `count`
     int token0;                          // the sequence's first token on the t axis
+    int place;                           // of the workspace (count > 1)
     bool ok;
 };
+
+// The workspace's place for the first segment of sequence seq, which starts at token a and
+// is cut; the others follow.  Batch form: that of the segment's position.  Packed, either
+// likewise, with a place for each sequence's last, partial segment; or, where there are
+// many sequences, 2 (a / seg): the sequence of c > 1 segments is more than (c - 1) seg
+// tokens long, so the next cut one starts at 2 (c - 1) >= c places further or more.
+__device__ __forceinline__ int first_place(const ScanPlan &plan, bool packed, int seq, int a) {
+    if (!packed) return seq * plan.nseg;
+    const int before = uniform(a / plan.seg);
+    return plan.sparse ? 2 * before : before + seq;
+}
 
 // The segment at position u: sequence i has positions i * nseg .. in the batch
 // form, and starts[i] / seg + i .. in the packed form (which leaves room for every
@@ -167,6 +181,7 @@ __device__ __forceinline__ Segment find_segment(const SelectiveScanParams &p, co
     }
     s.count = len > 0 ? uniform((len - 1) / plan.seg) + 1 : 1;
     s.ok = len >= 0 && s.index >= 0 && s.index < s.count;
+    s.place = first_place(plan, p.starts != nullptr, s.seq, s.token0) + s.index;
     s.first = s.ok ? s.index * plan.seg : 0;
     s.last = s.ok ? s.first + min(len - s.first, plan.seg) : 0;
     return s;
@@ -385,7 +400,7 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
     for (int m = 0; m < kTiles; ++m) hs[m] = f32x4_t{0, 0, 0, 0};
     const bool from_ws = seg.count > 1;
     if (OUT && (from_ws || (p.state != nullptr && p.has_init != nullptr && p.has_init[seg.seq] != 0))) {
-        const void *src = from_ws ? p.workspace + u * (int64_t)p.h * p.p * p.k : p.state;
+        const void *src = from_ws ? p.workspace + seg.place * (int64_t)p.h * p.p * p.k : p.state;
         const bool f32 = from_ws || p.state_f32, wide = from_ws ? p.k % 4 == 0 : wide_state(p);
         const int64_t at = (from_ws ? 0 : slot * p.ss_s) + ((int64_t)head * p.p + p0 + r) * p.k;
         if (r < pcount)
@@ -723,18 +738,18 @@ __global__ __launch_bounds__(kScanBlock, KS <= 128 ? 3 : 2) void selective_scan_
     const int64_t hpk = (int64_t)late.h * late.p * late.k;
     void *to = OUT ? late.state : late.workspace;
     const bool f32 = !OUT || late.state_f32, wide = OUT ? wide_state(late) : late.k % 4 == 0;
-    const int64_t at = (OUT ? slot * late.ss_s : (u + 1) * hpk) + ((int64_t)head * late.p + p0 + here(r)) * late.k;
+    const int64_t at = (OUT ? slot * late.ss_s : (seg.place + 1) * hpk) + ((int64_t)head * late.p + p0 + here(r)) * late.k;
     const int gg = here(g);
     if (r < pcount)
 #pragma unroll
         for (int m = 0; m < kTiles; ++m)
             store_state4(to, f32, wide, at + column(m, gg), late.k - column(m, gg), hs[m]);
     if (!OUT && has_job && lane == 0)
-        late.workspace[plan.slots * hpk + (int64_t)(u + 1) * late.h + job_head] = __builtin_amdgcn_exp2f(decay_sum);
+        late.workspace[plan.places * hpk + (int64_t)(seg.place + 1) * late.h + job_head] = __builtin_amdgcn_exp2f(decay_sum);
 }
 
-// The states ahead of every segment, in place: position u + 1 of the workspace
-// holds what segment u built up from zero and its decay.  A thread carries VEC
+// The states ahead of every segment, in place: the workspace's place behind a segment's
+// holds what that segment built up from zero and its decay.  A thread carries VEC
 // neighbouring values along a sequence's segments, and reads kJoinAhead segments at a
 // time: as the values it writes lie in the same array, reads one by one would each wait
 // for the write before (the whole call on 16381 tokens of 24 heads: 98.1 us reading one,
@@ -747,16 +762,15 @@ __global__ __launch_bounds__(kJoinBlock) void selective_join_kernel(const Select
     const int64_t hpk = (int64_t)p.h * p.p * p.k, pk = (int64_t)p.p * p.k;
     for_each_unit((int64_t)p.n * blocks_per_seq, [&](int64_t unit) {
         const int seq = uniform((int)(unit / blocks_per_seq)), part = (int)(unit - (int64_t)seq * blocks_per_seq);
-        int first = 0, len = p.t, u0 = seq * plan.nseg;
+        int first = 0, len = p.t;
         if (p.starts != nullptr) {
             first = load_uniform(p.starts, seq);
             const int end = load_uniform(p.starts, seq + 1);
             if (first < 0 || first > end || end > p.t) return;
             len = end - first;
-            u0 = first / plan.seg + seq;
         }
         if (len <= plan.seg) return;  // one segment
-        const int count = (len - 1) / plan.seg + 1;
+        const int count = (len - 1) / plan.seg + 1, u0 = first_place(plan, p.starts != nullptr, seq, first);
         const int slot = route_row(p.idx, nullptr, p.n, p.s, seq, threadIdx.x & 63);
         const bool init = slot >= 0 && p.state != nullptr && p.has_init != nullptr && p.has_init[seq] != 0;
         for (int64_t e = ((int64_t)part * kJoinBlock + threadIdx.x) * VEC; e < hpk;
@@ -769,7 +783,7 @@ __global__ __launch_bounds__(kJoinBlock) void selective_join_kernel(const Select
                                        : bf16_bits_to_f32(static_cast<const uint16_t *>(p.state)[slot * p.ss_s + e + i]);
             typedef float fvec __attribute__((ext_vector_type(VEC)));
             fvec *ws = reinterpret_cast<fvec *>(p.workspace + u0 * hpk + e);
-            const float *dec = p.workspace + plan.slots * hpk + (int64_t)u0 * p.h + e / pk;
+            const float *dec = p.workspace + plan.places * hpk + (int64_t)u0 * p.h + e / pk;
             for (int j0 = 0; j0 < count; j0 += kJoinAhead) {
                 fvec v[kJoinAhead];
                 float d[kJoinAhead];
@@ -847,6 +861,10 @@ ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_
     plan.nseg = (int32_t)(t > 0 ? (t + seg - 1) / seg : 1);
     plan.split = plan.nseg > 1;
     plan.slots = (int32_t)(packed ? t / seg + n : n * plan.nseg);
+    // sparse places end at 2 (nseg - 1), as one of c segments starts (c - 1) seg tokens ahead of t's last
+    const int64_t cut = 2 * ((int64_t)plan.nseg - 1);
+    plan.sparse = packed && cut < plan.slots;
+    plan.places = plan.sparse ? (int32_t)cut : plan.slots;
     // the longest runs of which there are still kRuns (of equal length: packed
     // sequences would leave some XCDs with more to do than others)
     const int64_t run = packed ? 1 : plan.slots * per_slot / kRuns;
@@ -924,7 +942,7 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c, int64_t heads) {
 
 int64_t selective_scan_workspace_floats(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k, bool packed) {
     const ScanPlan plan = make_plan(n, t, h, p, g, k, packed);
-    return plan.split ? plan.slots * (h * p * k + h) : 0;
+    return plan.split ? plan.places * (h * p * k + h) : 0;
 }
 
 hipError_t launch_selective_scan(const SelectiveScanParams &p, hipStream_t stream, const char **kernel_name) {

@@ -48,3 +48,22 @@ def test_scan_is_not_finite_where_the_recurrence_is_not(name, bad, state, tokens
     keep = torch.isfinite(y)
     assert not keep.all() and torch.equal(torch.isfinite(out[0]).cpu(), keep)
     close(out[0].cpu()[keep], y[keep], (U * y.abs() + (U + 2.0 ** -13) * ya)[keep], "finite outputs")
+
+
+@pytest.mark.parametrize("state", [torch.float32, torch.bfloat16])
+def test_scan_of_many_packed_sequences_some_of_them_cut(state):
+    """More sequences than segments (of 2048 tokens here): places in the workspace go to the cut
+    ones alone, several of them one behind the other, ending with the last token.  A value that
+    the workspace must not be read or written past lies behind it."""
+    gen = torch.Generator().manual_seed(61)
+    lens = torch.randint(0, 12, (300,), generator=gen).tolist()
+    lens[40:43], lens[150], lens[299] = [2049, 2049, 4097], 2048, 2500
+    init = (torch.rand(300, generator=gen) < 0.5).tolist()
+    case = Scan(61, lens, 1, 16, 1, 16, state=state, packed=True, slots=303, init=init,
+                table=[-1 if i % 50 == 7 else 302 - i for i in range(300)])
+    need = dc.dcconv_selective_scan_workspace(300, sum(lens), 1, 16, 1, 16, 1)
+    assert 0 < need <= 2 * (sum(lens) // 2048) * 4 * (16 * 16 + 1)
+    buf = torch.full((need + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    case.check(workspace=buf[:need])
+    assert dc.dcconv_last_kernel().startswith("selective_scan_split")
+    assert bool((buf[need:] == 0xAB).all())

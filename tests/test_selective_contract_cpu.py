@@ -47,3 +47,18 @@ def test_a_second_thread_finds_torch_only_with_its_types(monkeypatch):
     finally:
         sys.settrace(before)
     assert selective._t is torch and not missing
+
+
+def test_packed_workspace_grows_with_tokens_not_with_sequences():
+    """Only a sequence that is cut into segments has a place in the workspace; as it is longer
+    than a segment, t tokens hold at most two segments of cut sequences for each of theirs."""
+    heads = (96, 64, 8, 128)
+    state = 4 * 96 * (64 * 128 + 1)
+    sizes = [dc.dcconv_selective_scan_workspace(n, 65536, *heads, 1) for n in (64, 256, 1024, 65536)]
+    assert len(set(sizes)) == 1 and 0 < sizes[0] <= 2 * (65536 // 2048) * state
+    assert dc.dcconv_selective_scan_workspace(256, 2100, *heads, 1) <= 2 * state
+    assert dc.dcconv_selective_scan_workspace(256, 2000, *heads, 1) == 0
+    # few sequences: no more than a place for each segment
+    for n in (1, 2, 5):
+        few = dc.dcconv_selective_scan_workspace(n, 16381, 24, 64, 2, 128, 1)
+        assert 0 < few <= (-(-16381 // 96) + n) * 4 * 24 * (64 * 128 + 1)
