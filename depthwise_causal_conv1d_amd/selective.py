@@ -325,7 +325,11 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
     final state there; ``state_indices`` (int32 [n]) routes sequences to slots, -1 being
     padding.  return_final_state: without ``ssm_state``, returns ``(out, state)`` with
     a new float32 [n, H, P, K] state.  ``workspace``: a uint8 buffer of
-    ``dcconv_selective_scan_workspace`` bytes (allocated here if None)."""
+    ``dcconv_selective_scan_workspace`` bytes (allocated here if None).
+
+    Sums and states are 32 bits; operands of the matrix products are rounded to bf16 (the
+    copy of the state that C reads, the products of C and B, and, unless ``ssm_state`` is
+    float32 or a final state is returned, the scaled x that enters the state)."""
     lib = _lib()
     if x.dim() != 4 or B.dim() != 4:
         raise ValueError(f"x must be [N, T, H, P] and B [N, T, G, K], got {tuple(x.shape)} and {tuple(B.shape)}")
