@@ -17,7 +17,7 @@
 //
 // 256 rows of 96 heads, 64 x 128, F32 states: 258 us, 1621 MB at 6.3 TB/s (a plain copy
 // reaches 5.9).  61 rows of 30 heads, 80 x 72, BF16 states: 14.4 us, 38 MB at 2.7 TB/s:
-// items whose rows of 144 bytes fill neither the 16 lanes nor a cache line.  4 rows of 24
+// items of 4.6 KiB, whose rows of 144 bytes fill neither the 16 lanes nor a cache line.  4 rows of 24
 // heads: 5 us, a launch and one item's latency.
 //
 // The fused form computes x, B and C as the width-4 convolution of its channels
@@ -29,7 +29,7 @@
 // 256 rows of 96 heads with BF16 states: 155 us, 841 MB at 5.4 TB/s.  64 rows of 60
 // heads in one group, F32 states, some padding: 54.7 us, 225 MB at 4.1 TB/s, as the group's
 // B and C are convolved by 30 blocks a row.  One row of 24 heads: 7.8 us, the loads of the
-// taps and then of the state behind the launch.
+// taps, the count and then the state's items behind the launch.
 #include "selective_common.h"
 
 namespace dcconv {
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(kUpdateBlock) void selective_update_kernel(const Se
 // convolves its group's B and C; but no more than leave kUpdateBlocks blocks.  (256 rows
 // of 96 heads, 64 x 128: F32 states with 16, 32 and 64 KiB a block 295, 257 and 285 us,
 // BF16 147 at 16 and 136 at 32 KiB; fused, BF16 states, 201, 160 and 154 us at 16, 32
-// and 64 KiB.)
+// and 64 KiB, eight items; F32 states, four items in 64 KiB, were not measured at others.)
 constexpr int64_t kMinLargeItems = 2048;
 constexpr int64_t kUpdateBlocks = 768;
 constexpr int64_t kBlockState = 32 * 1024, kFusedBlockState = 64 * 1024;

@@ -26,8 +26,10 @@
 // One row of x, 14432 x 4096 weights in groups of 128: 8.8 us, 30.5 MB at 3.5 TB/s; with
 // 7200 waves of four tiles each, the launch, the first loads' latency and the join are
 // the rest.  13 rows, 4096 x 6144 in groups of 64 with zero points: 9.2 us, 14 MB
-// at 1.5 TB/s; every block reads all of x through its L2 (41 MB in all, three times the
-// codes).  (Reading two or four tiles ahead was slower.)
+// at 1.5 TB/s: one block a CU, whose sixteen waves take three tiles one after the other,
+// load scales and zero points two bytes and one at a time, sum x again in every block
+// and are joined by a quarter of the threads; x comes through the L2s (41 MB in all, about
+// 1 us).  (Reading two or four tiles ahead was slower.)
 #include "selective_common.h"
 
 namespace dcconv {
