@@ -17,7 +17,8 @@ update continues (batch or packed variable-length sequences).
 
 ``selective_scan``, ``selective_update`` and ``causal_conv1d_selective_update`` (module
 ``selective``) are the state-space recurrence that the convolution feeds, for prompts
-and for single tokens.
+and for single tokens; ``gated_delta_scan`` and ``gated_delta_update`` (module ``delta``) the
+gated delta rule, with the norms of its layer, ``gated_rms_norm`` and ``add_rms_norm``.
 
 There is no fallback: if the HIP library is missing, every call raises.
 """
@@ -27,7 +28,8 @@ import ctypes
 import os
 import threading
 
-from . import _binding, selective
+from . import _binding, delta, selective
+from .delta import *  # noqa: F401,F403
 from .selective import *  # noqa: F401,F403
 
 __all__ = [
@@ -38,7 +40,7 @@ __all__ = [
     "causal_conv1d_update_tokens", "dcconv_prefill", "causal_conv1d", "library_path", "DcconvError",
     "DCCONV_DEV_BAD_SEQ", "DCCONV_DEV_BAD_SEQLEN", "dcconv_stream_copy", "stream_copy",
     "dcconv_busy_spin", "busy_spin",
-] + selective.__all__
+] + selective.__all__ + delta.__all__
 
 DCCONV_OK, DCCONV_EINVAL, DCCONV_EUNSUPPORTED, DCCONV_EHIP = 0, 1, 2, 3
 DCCONV_ACT_IDENTITY, DCCONV_ACT_SILU = 0, 1
@@ -109,6 +111,7 @@ def _load() -> ctypes.CDLL:
             lib.dcconv_busy_spin.restype = i32
             lib.dcconv_busy_spin.argtypes = [ctypes.c_double, vp]     # microseconds, stream
             selective.declare(lib)
+            delta.declare(lib)
             _lib = lib
     return _lib
 

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdcconv.so")
 SOURCES = ["abi.hip", "update.hip", "update_tokens.hip", "prefill.hip", "update_ring.hip", "copy_control.hip",
-           "selective_abi.hip", "selective_update.hip", "selective_scan.hip", "w4_matvec.hip"]
+           "selective_abi.hip", "selective_update.hip", "selective_scan.hip", "w4_matvec.hip",
+           "delta_abi.hip", "delta_update.hip", "delta_scan.hip", "norms.hip"]
 ARCH = "gfx950"
 
 

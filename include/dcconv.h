@@ -364,6 +364,132 @@ int dcconv_selective_scan(const void *x, int64_t n, int64_t t, int64_t h, int64_
 int64_t dcconv_selective_scan_workspace(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k,
                                         int packed);
 
+/* ---------------------------------------------------------------------------
+ * The gated delta rule behind the convolution.
+ *
+ * Heads i = 0..h-1 of p channels each; q and key of k values belong to the head's
+ * group i / (h/g).  With d = softplus(dt + dt_bias[i]) (or dt + dt_bias[i] without
+ * dt_softplus), b = sigmoid(beta) (or beta without beta_sigmoid), a head's state
+ * S [p, k] and a token's q, key and v:
+ *
+ *     S    = exp(d * a[i]) * S
+ *     u    = b * (v - S key)
+ *     S    = S + u key^T
+ *     out  = scale * S q
+ *
+ * With qk_l2norm, q and key are first multiplied by 1 / sqrt(sum of squares +
+ * l2norm_eps).  Sums, exponentials and the recurrence are FP32.  The one-token entry
+ * point rounds out, and a BF16 state, once and nothing else; dcconv_gated_delta_scan
+ * rounds some operands of its matrix products besides (see there).
+ *
+ * Operands of both entry points:
+ *  q, key      BF16, k unit-stride values of a group.  1 <= k <= 256.
+ *  v, out      BF16, p unit-stride channels of a head.  Other strides are given in
+ *              elements, >= 0; out must give every element its own address.
+ *  dt, beta    BF16 or F32 (dt_dtype, beta_dtype), h unit-stride values of a token.
+ *  dt_bias, a  F32 [h]; dt_bias may be NULL (zero).
+ *  l2norm_eps  positive and finite with qk_l2norm, else unused; scale: finite.
+ *  state       F32 or BF16 (state_dtype) [s, h, p, k], slots ss_s elements apart and
+ *              dense inside, READ AND WRITTEN.
+ *  state_indices, dev_status, stream: as conv_state_indices, dev_status and stream
+ *              of dcconv_update: -1 is a padding row (zero output, no state moves);
+ *              a bad index, and with dev_status a duplicate one, makes a row padding.
+ * Operands are aligned to their elements; rows that start on 16 bytes (and sizes
+ * that are multiples of 8) take 16-byte accesses.  Nothing that a call writes may
+ * lie within the range another operand spans.  The sums of squares of a q and of a
+ * key are assumed to be finite in FP32 (values below 2^59 are enough).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * dcconv_gated_delta_update -- one token of n rows, in place.
+ * q and key [n, g, k] (strides qs_n, qs_g and ks_n, ks_g), v and out [n, h, p], dt and
+ * beta [n, h] (ds_n and es_n).  n == 0 returns DCCONV_OK and enqueues nothing.
+ * Returns DCCONV_OK, DCCONV_EINVAL, DCCONV_EUNSUPPORTED (k > 256, or sizes past
+ * n, s < 2^31, h*p and g*k <= 2^26) or DCCONV_EHIP.
+ */
+int dcconv_gated_delta_update(const void *q, const void *key, const void *v, int64_t n, int64_t h, int64_t p,
+                              int64_t g, int64_t k, int64_t qs_n, int64_t qs_g, int64_t ks_n, int64_t ks_g,
+                              int64_t vs_n, int64_t vs_h,
+                              const void *dt, int dt_dtype, int64_t ds_n, const float *dt_bias, int dt_softplus,
+                              const float *a, const void *beta, int beta_dtype, int64_t es_n, int beta_sigmoid,
+                              int qk_l2norm, float l2norm_eps, float scale,
+                              void *state, int state_dtype, int64_t s, int64_t ss_s, const int32_t *state_indices,
+                              void *out, int64_t os_n, int64_t os_h, int32_t *dev_status, void *stream);
+
+/*
+ * dcconv_gated_delta_scan -- whole sequences (prefill).
+ * q and key [n, t, g, k], v and out [n, t, h, p], dt and beta [n, t, h]; or, with
+ * seq_starts (device int32 [n+1], as for dcconv_prefill), n packed sequences on one
+ * axis of t tokens, the _n strides unused.
+ * state       NULL (with s == 0, no indices and no has_initial_state: every sequence
+ *             starts from zero and its final state is dropped), or the pool: sequence
+ *             i starts from its slot's state where has_initial_state[i] (uint8 [n],
+ *             NULL: nowhere) is nonzero, from zero elsewhere, and leaves its final
+ *             state there.  An empty sequence leaves its initial state or zeros.
+ * Returns as dcconv_gated_delta_update.
+ */
+int dcconv_gated_delta_scan(const void *q, const void *key, const void *v, int64_t n, int64_t t, int64_t h, int64_t p,
+                            int64_t g, int64_t k, int64_t qs_n, int64_t qs_t, int64_t qs_g,
+                            int64_t ks_n, int64_t ks_t, int64_t ks_g, int64_t vs_n, int64_t vs_t, int64_t vs_h,
+                            const void *dt, int dt_dtype, int64_t ds_n, int64_t ds_t, const float *dt_bias,
+                            int dt_softplus, const float *a,
+                            const void *beta, int beta_dtype, int64_t es_n, int64_t es_t, int beta_sigmoid,
+                            int qk_l2norm, float l2norm_eps, float scale, const int32_t *seq_starts,
+                            void *state, int state_dtype, int64_t s, int64_t ss_s, const int32_t *state_indices,
+                            const uint8_t *has_initial_state,
+                            void *out, int64_t os_n, int64_t os_t, int64_t os_h, int32_t *dev_status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms of the layer: behind the recurrence, and between blocks.  All arithmetic is
+ * FP32, and what is stored is rounded once.  weight_dtype (and post_weight's, the
+ * same) is BF16 or F32; weight_offset is added to every weight (1 for weights that
+ * are kept as their difference from one).  rms(v) = sqrt(mean of v^2 + eps) over the
+ * d values of a row; the squares of all finite values are served, also where their
+ * sum is not finite or zero in FP32.  1 <= d <= 16384.  x, z, gate and out are BF16 with
+ * d unit-stride values of a row and other strides >= 0, in elements.  Nothing that a
+ * call writes may lie within the range another operand spans.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * dcconv_gated_rms_norm -- rows x [n, t, h, d], each normed by itself, times SiLU(z):
+ *
+ *     out = x / rms(x) * (weight + weight_offset) * SiLU(z)
+ *     out = y / rms(y) * (weight + weight_offset), y = x * SiLU(z)     (gate_first)
+ *
+ * z           as x, or NULL (no gate).
+ * weight      [d] (ws_h == 0) or a row of d for each h, ws_h elements apart; or NULL
+ *             (ones, and weight_offset is not added).
+ * n, t, h     0 of any returns DCCONV_OK and enqueues nothing.
+ * Returns DCCONV_OK, DCCONV_EINVAL, DCCONV_EUNSUPPORTED (d > 16384, or 2^40 rows) or
+ * DCCONV_EHIP.
+ */
+int dcconv_gated_rms_norm(const void *x, int64_t n, int64_t t, int64_t h, int64_t d,
+                          int64_t xs_n, int64_t xs_t, int64_t xs_h,
+                          const void *z, int64_t zs_n, int64_t zs_t, int64_t zs_h, int gate_first,
+                          const void *weight, int weight_dtype, int64_t ws_h, float weight_offset, float eps,
+                          void *out, int64_t os_n, int64_t os_t, int64_t os_h, void *stream);
+
+/*
+ * dcconv_add_rms_norm -- the residual stream between two blocks, rows [n, t, d]:
+ *
+ *     y        = x, or x / rms(x) * (post_weight + weight_offset)
+ *     residual = residual + residual_scale * y * gate
+ *     out      = residual / rms(residual) * (weight + weight_offset)
+ *
+ * x           the block's output.
+ * gate        [n, t, d] (strides of 0 share a row), or NULL (1).
+ * post_weight, weight  [d]; post_weight NULL: x enters as it is.
+ * residual    BF16 or F32 (residual_dtype), READ AND WRITTEN; its rows must not share
+ *             addresses.  out is made from the sum before it is rounded to BF16.
+ * n == 0 or t == 0 returns DCCONV_OK and enqueues nothing.
+ * Returns as dcconv_gated_rms_norm.
+ */
+int dcconv_add_rms_norm(const void *x, int64_t n, int64_t t, int64_t d, int64_t xs_n, int64_t xs_t,
+                        void *residual, int residual_dtype, int64_t rs_n, int64_t rs_t,
+                        const void *gate, int64_t gs_n, int64_t gs_t, float residual_scale,
+                        const void *post_weight, const void *weight, int weight_dtype, float weight_offset, float eps,
+                        void *out, int64_t os_n, int64_t os_t, void *stream);
+
 /*
  * dcconv_w4_matvec -- a few rows times a 4-bit weight matrix, as the projections
  * before and after the convolution and the recurrence:
