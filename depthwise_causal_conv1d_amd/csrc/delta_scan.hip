@@ -106,6 +106,12 @@ __device__ __forceinline__ u32x4 load_columns(const uint16_t *at, int pitch) {
 
 __device__ __forceinline__ bool is_finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+// v, not known to be the same as anywhere else: addresses formed from it are formed where they
+// are used, instead of being kept in registers through a loop.
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
 // Two result tiles as an operand of N parts: a BF16 value, and what each leaves.
 template <int N>
@@ -147,80 +153,100 @@ __device__ __forceinline__ double prefix_sum(double v, int lane) {
     return v + (lane >= 48 ? r0 + r1 + r2 : lane >= 32 ? r0 + r1 : lane >= 16 ? r0 : 0.0);
 }
 
-// The sum over 8, 16 or 32 neighbouring lanes, in all of them.
-template <int LANES>
-__device__ __forceinline__ float sum_lanes(float v) {
-#pragma unroll
-    for (int s = 1; s < LANES; s *= 2) v += __shfl_xor(v, s);
-    return v;
+// log(1 + e^v) and 1 / (1 + e^-v) with the hardware's exponential, logarithm and reciprocal,
+// each within about 2^-21 of itself: a series where the logarithm's argument is near one.
+__device__ __forceinline__ float softplus_near(float v) {
+    const float t = __builtin_amdgcn_exp2f(-__builtin_fabsf(v) * kLog2e);
+    const float series = t * (1.0f + t * (-0.5f + t * (1.0f / 3.0f + t * (-0.25f + t * 0.2f))));
+    const float far = __builtin_amdgcn_logf(1.0f + t) * 0.6931471805599453f;
+    return (v > 0.0f ? v : 0.0f) + (t > 0x1p-5f ? far : series);
+}
+__device__ __forceinline__ float sigmoid_near(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 
-// One operand's rows of a chunk: a lane moves eight values from column col, of which
-// `count` exist.  WIDE reads them at once (16 bytes) through a buffer that ends with the
-// chunk's last row, so that what lies behind it reads as zeros.
-template <bool WIDE>
-struct Rows {
+// The place of 16-byte piece i of row `row` in a tile of rows of ACROSS pieces is i ^ swap: what
+// sixteen lanes read at a time, a piece of 16 rows or four of four rows, then lies on banks of its own.
+template <int ACROSS>
+__device__ __forceinline__ int swap_of(int row) {
+    return ACROSS == 8 ? ((row >> 1 & 1) << 2) | (row >> 2 & 3) : ((row & 3) << 2) | (row >> 2 & 3);
+}
+
+// One operand's tile of ROWS tokens in LDS, brought there by four waves.  WIDE: straight from
+// memory, 64 pieces of 16 bytes an instruction, through a buffer that ends with the chunk's last
+// row (what lies behind reads as zeros); the caller waits for them.
+template <int ACROSS, int ROWS, bool WIDE>
+struct Tile {
+    static constexpr int kLoads = ROWS * ACROSS / kHalfBlock;
     const uint16_t *base;  // wave-uniform: the sequence's first row
     int64_t stride;
-    int32_t row0, step, col, count, width;
-    __device__ __forceinline__ Rows(const uint16_t *first, int64_t stride, int width, int row0, int step, int col)
-        : base(first), stride(stride), row0(row0), step(step), col(col), count(width - col), width(width) {}
-    // rows row0 + q * step of the chunk at token t0; n: the sequence's rows from there
-    template <int N>
-    __device__ __forceinline__ void load(u32x4 (&w)[N], int64_t t0, int n) const {
+    int32_t width;
+    // rows of the chunk at token t0; n: the sequence's rows from there
+    __device__ __forceinline__ void load(uint16_t *to, int64_t t0, int n, int wave, int lane) const {
+        typedef __attribute__((address_space(3))) void *Lds;
         const uint16_t *from = base + t0 * stride;
-        if (WIDE) {
-            const uint32_t pitch = 2u * (uint32_t)stride;
-            n = min(n, N * step);  // the chunk's rows
-            const Buffer buf = make_buffer(from, n > 0 ? (uint32_t)(n - 1) * pitch + 2u * (uint32_t)width : 0u);
+        n = min(n, ROWS);
+        const uint32_t pitch = 2u * (uint32_t)stride;
+        const Buffer buf = make_buffer(from, WIDE && n > 0 ? (uint32_t)(n - 1) * pitch + 2u * (uint32_t)width : 0u);
 #pragma unroll
-            for (int q = 0; q < N; ++q) {
-                const int row = row0 + q * step;
-                w[q] = buffer_load<kCached>(buf, row < n && count > 0 ? (uint32_t)row * pitch + 2u * (uint32_t)col : kNowhere);
+        for (int q = 0; q < kLoads; ++q) {
+            const int first = (wave * kLoads + q) * kWave, row = (first + lane) / ACROSS;
+            const int piece = (first + lane) % ACROSS ^ swap_of<ACROSS>(row);
+            if (WIDE) {
+                const uint32_t at = row < n && 8 * piece < width ? (uint32_t)row * pitch + 16u * (uint32_t)piece : kNowhere;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (Lds)(to + 8 * first), 16, at, 0, 0, 0);
+                continue;
             }
-            return;
-        }
-#pragma unroll
-        for (int q = 0; q < N; ++q) {
-            const int row = row0 + q * step;
-            w[q] = u32x4{0, 0, 0, 0};
+            u32x4 w = {0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (row < n && i < count) w[q][i >> 1] |= (uint32_t)from[row * stride + col + i] << (16 * (i & 1));
+                if (row < n && 8 * piece + i < width)
+                    w[i >> 1] |= (uint32_t)from[row * stride + 8 * piece + i] << (16 * (i & 1));
+            *reinterpret_cast<u32x4 *>(to + 8 * (first + lane)) = w;
         }
     }
 };
+__device__ __forceinline__ void wait_for_tiles() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All waves' LDS accesses up to here done, tiles on their way or not (__syncthreads waits for those).
+__device__ __forceinline__ void block_sync() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Four consecutive state values at element `at`, of which `count` exist.
-__device__ __forceinline__ f32x4_t load_state4(const void *s, bool f32, bool wide, int64_t at, int count) {
-    f32x4_t v = {0, 0, 0, 0};
-    if (wide && count >= 4) {
-        if (f32) return *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(s) + at);
-        const u32x2 w = *reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(s) + at);
+// Four consecutive state values, F32 or BF16, from byte offset `at` of a buffer, of which
+// `count` exist; WIDE: in one access.
+template <bool F32, bool WIDE>
+__device__ __forceinline__ f32x4_t load_state4(Buffer buf, uint32_t at, int count) {
+    if (WIDE) {
+        at = count > 0 ? at : kNowhere;
+        if (F32) return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(buf, at, 0, kCached));
+        const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(buf, at, 0, kCached);
         return f32x4_t{lo_f32(w[0]), hi_f32(w[0]), lo_f32(w[1]), hi_f32(w[1])};
     }
+    f32x4_t v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < count) v[i] = load_either(s, f32, at + i);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t to = i < count ? at + (F32 ? 4u : 2u) * i : kNowhere;
+        v[i] = F32 ? __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buf, to, 0, kCached))
+                   : bf16_bits_to_f32(__builtin_amdgcn_raw_buffer_load_b16(buf, to, 0, kCached));
+    }
     return v;
 }
-__device__ __forceinline__ void store_state4(void *s, bool f32, bool wide, int64_t at, int count, f32x4_t v) {
-    if (wide && count >= 4) {
-        if (f32)
-            *reinterpret_cast<f32x4_t *>(static_cast<float *>(s) + at) = v;
+template <bool F32, bool WIDE>
+__device__ __forceinline__ void store_state4(Buffer buf, uint32_t at, int count, f32x4_t v) {
+    if (WIDE) {
+        at = count > 0 ? at : kNowhere;
+        if (F32)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), buf, at, 0, kCached);
         else
-            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(s) + at) =
-                u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, buf, at, 0, kCached);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < count) {
-            if (f32)
-                static_cast<float *>(s)[at + i] = v[i];
-            else
-                static_cast<uint16_t *>(s)[at + i] = f32_to_bf16_bits(v[i]);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t to = i < count ? at + (F32 ? 4u : 2u) * i : kNowhere;
+        if (F32)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), buf, to, 0, kCached);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_bits(v[i]), buf, to, 0, kCached);
+    }
 }
 
 // The state column of row 4 g of the state's tile m.
@@ -241,33 +267,32 @@ __device__ __forceinline__ void check_table(const DeltaParams &p) {
 // of a chunk; NT: tiles of 16 state rows a wave owns; PARTS: see above.
 template <int KS, int C, int NT, int PARTS>
 struct Sizes {
-    static constexpr int kKeyPitch = KS + 16;  // of 16-bit values: 32 bytes more than a multiple of 64
     static constexpr int kRowsP = kHalf * 16 * NT;  // state rows of a block
-    static constexpr int kVPitch = kRowsP + 8;
-    static constexpr int kTPitch = C + 16;
+    static constexpr int kPPitch = C + 8, kTPitch = 40;  // rows of 16 lanes' 16-byte reads on banks of their own
     static constexpr int kTParts = PARTS == 1 ? 2 : PARTS;
-    static constexpr int kBlocks = C / 16, kTiles = kBlocks * (kBlocks + 1) / 2;
-    static constexpr int kKey = 0;                                   // [2][C][kKeyPitch]
-    static constexpr int kQuery = kKey + 2 * C * kKeyPitch * 2;      // [2][C][kKeyPitch]
-    static constexpr int kV = kQuery + 2 * C * kKeyPitch * 2;        // [C][kVPitch]
-    static constexpr int kT = kV + C * kVPitch * 2;                  // [kTParts][C][kTPitch]
-    static constexpr int kP = kT + kTParts * C * kTPitch * 2;        // [C][kTPitch]
-    static constexpr int kA = kP + C * kTPitch * 2;                  // [kTiles][16][kAPitch] floats
-    static constexpr int kToken = kA + kTiles * 16 * kAPitch * 4;    // [2][kTokenRows][C] floats
-    static constexpr int kBytes = kToken + 2 * kTokenRows * C * 4;
+    static constexpr int kBlocks = C / 16, kHalves = C / 32;
+    static constexpr int kKey = 0;                                   // [3][C][KS]
+    static constexpr int kQuery = kKey + 3 * C * KS * 2;             // [3][C][KS]
+    static constexpr int kV = kQuery + 3 * C * KS * 2;               // [C][kRowsP]
+    static constexpr int kT = kV + C * kRowsP * 2;                   // [kTParts][C][kTPitch]
+    static constexpr int kOff = kT + kTParts * C * kTPitch * 2;      // [kTParts][C - 32][kTPitch]
+    static constexpr int kP = kOff + kTParts * (C - 32) * kTPitch * 2;  // [C][kPPitch]
+    static constexpr int kA = kP + C * kPPitch * 2;                  // [3 kHalves][16][kAPitch] floats
+    static constexpr int kToken = kA + 3 * kHalves * 16 * kAPitch * 4;  // [3][kTokenRows][C] floats
+    static constexpr int kBytes = kToken + 3 * kTokenRows * C * 4;
     static_assert(kBytes <= 160 * 1024, "more LDS than a CU has");
 };
 
 template <int KS, int C, int NT, int PARTS, bool WIDE>
 __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaParams p, const ScanPlan plan) {
     using Z = Sizes<KS, C, NT, PARTS>;
-    constexpr int kB = Z::kBlocks, KP = Z::kKeyPitch, VP = Z::kVPitch, TP = Z::kTPitch, kSteps = KS / 32;
+    constexpr int kB = Z::kBlocks, VP = Z::kRowsP, TP = Z::kTPitch, PP = Z::kPPitch, kSteps = KS / 32;
     constexpr int kTParts = Z::kTParts;
     extern __shared__ u32x4 smem[];
     char *lds = reinterpret_cast<char *>(smem);
     uint16_t *sk = reinterpret_cast<uint16_t *>(lds + Z::kKey), *sq = reinterpret_cast<uint16_t *>(lds + Z::kQuery);
     uint16_t *sv = reinterpret_cast<uint16_t *>(lds + Z::kV), *st = reinterpret_cast<uint16_t *>(lds + Z::kT);
-    uint16_t *sp = reinterpret_cast<uint16_t *>(lds + Z::kP);
+    uint16_t *sp = reinterpret_cast<uint16_t *>(lds + Z::kP), *so = reinterpret_cast<uint16_t *>(lds + Z::kOff);
     float *sa = reinterpret_cast<float *>(lds + Z::kA), *tokens = reinterpret_cast<float *>(lds + Z::kToken);
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
@@ -311,241 +336,364 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
     // the tiles of T and P above the diagonal that products over 32 tokens read: zeros for good
     for (int i = tid; i < (kTParts + 1) * (kB / 2) * 16 * 4; i += kScanBlock) {
         const int piece = i & 3, row = (i >> 2) & 15, m = (i >> 6) % (kB / 2), part = (i >> 6) / (kB / 2);
-        uint16_t *to = (part < kTParts ? st + part * C * TP : sp) + (32 * m + row) * TP + 32 * m + 8 * piece + 4;
-        *reinterpret_cast<u32x2 *>(to) = u32x2{0, 0};
+        uint16_t *to = part < kTParts ? st + (part * C + 32 * m + row) * TP : sp + (32 * m + row) * PP + 32 * m;
+        *reinterpret_cast<u32x2 *>(to + 8 * piece + 4) = u32x2{0, 0};
     }
+
+    // Where a lane reads its share of k (of q: kQuery - kKey further): row r's inner indices
+    // 32 m + 8 g .. of the state's columns, and, with tokens as the inner index, columns 16 t ..
+    constexpr int kAcross = KS / 8;
+    int by_row_at[kSteps < 4 ? kSteps : 4], by_column_at[kSteps < 4 ? kSteps : 4];
+#pragma unroll
+    for (int m = 0; m < kSteps && m < 4; ++m) {
+        by_row_at[m] = r * KS + 8 * ((4 * m + g) ^ swap_of<kAcross>(r));
+        by_column_at[m] = (4 * g + (r >> 2)) * KS + 8 * ((4 * m + (r & 3)) ^ swap_of<kAcross>(4 * g + (r >> 2)));
+    }
+    const auto row_at = [&](int m) { return by_row_at[m & 3] + 128 * (m >> 2); };
+    const auto column_at = [&](int t) { return by_column_at[t >> 1 & 3] + 128 * (t >> 3) + 4 * (t & 1); };
 
     if (wave >= kHalf) {
         // ================================================== the waves that prepare T and P
-        const int ptid = tid - kHalfBlock, pw = wave - kHalf;
-        constexpr int kAcross = KS / 8, kRowsPer = kHalfBlock / kAcross, kMoves = C / kRowsPer;
-        const int row0 = ptid / kAcross, col = ptid % kAcross * 8;
-        const Rows<WIDE> rk(p.key + seq * p.ks_n + (int64_t)first * p.ks_t + group * p.ks_g, p.ks_t, p.k, row0, kRowsPer, col);
-        const Rows<WIDE> rq(p.q + seq * p.qs_n + (int64_t)first * p.qs_t + group * p.qs_g, p.qs_t, p.k, row0, kRowsPer, col);
-        u32x4 nk[kMoves], nq[kMoves];
+        const int pw = wave - kHalf;
+        const Tile<kAcross, C, WIDE> keys = {p.key + seq * p.ks_n + (int64_t)first * p.ks_t + group * p.ks_g, p.ks_t, p.k};
+        const Tile<kAcross, C, WIDE> queries = {p.q + seq * p.qs_n + (int64_t)first * p.qs_t + group * p.qs_g, p.qs_t, p.k};
+        const Tile<Z::kRowsP / 8, C, WIDE> values = {p.v + seq * p.vs_n + (int64_t)first * p.vs_t + head * p.vs_h + p0,
+                                                     p.vs_t, rows};
         auto fetch = [&](int j) {
-            rk.load(nk, (int64_t)j * C, len - j * C);
-            rq.load(nq, (int64_t)j * C, len - j * C);
+            keys.load(sk + j % 3 * C * KS, (int64_t)j * C, len - j * C, pw, lane);
+            queries.load(sq + j % 3 * C * KS, (int64_t)j * C, len - j * C, pw, lane);
         };
-        // q and k of chunk j into LDS, with the factors that make their rows of length one
-        auto stage = [&](int j) {
-            uint16_t *tk = sk + (j & 1) * C * KP, *tq = sq + (j & 1) * C * KP;
-            float *tok = tokens + (j & 1) * kTokenRows * C;
-#pragma unroll
-            for (int q = 0; q < kMoves; ++q) {
-                const int row = row0 + q * kRowsPer;
-                *reinterpret_cast<u32x4 *>(tk + row * KP + col) = nk[q];
-                *reinterpret_cast<u32x4 *>(tq + row * KP + col) = nq[q];
-                float k2 = 0.0f, q2 = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    k2 = __builtin_fmaf(lo_f32(nk[q][i]), lo_f32(nk[q][i]), k2);
-                    k2 = __builtin_fmaf(hi_f32(nk[q][i]), hi_f32(nk[q][i]), k2);
-                    q2 = __builtin_fmaf(lo_f32(nq[q][i]), lo_f32(nq[q][i]), q2);
-                    q2 = __builtin_fmaf(hi_f32(nq[q][i]), hi_f32(nq[q][i]), q2);
-                }
-                k2 = sum_lanes<kAcross>(k2);
-                q2 = sum_lanes<kAcross>(q2);
-                if (col == 0) {
-                    tok[kUnitK * C + row] = is_finite(k2) ? unit_factor(p, k2) : __builtin_nanf("");
-                    tok[kUnitQ * C + row] = p.scale * unit_factor(p, q2);
-                }
-            }
-        };
+        auto fetch_v = [&](int j) { values.load(sv, (int64_t)j * C, len - j * C, pw, lane); };
         // ---- decays and weights of a chunk's tokens, a lane each (as they are in memory:
         // converting them here would wait for them)
         const float rate = p.a[head] * kLog2e, bias = p.dt_bias != nullptr ? p.dt_bias[head] : 0.0f;
-        const int64_t dt0 = seq * p.ds_n + (int64_t)first * p.ds_t + head, beta0 = seq * p.es_n + (int64_t)first * p.es_t + head;
+        const char *dt_at = static_cast<const char *>(p.dt) +
+                            (p.dt_f32 ? 4 : 2) * (seq * p.ds_n + (int64_t)(first + lane) * p.ds_t + head);
+        const char *beta_at = static_cast<const char *>(p.beta) +
+                              (p.beta_f32 ? 4 : 2) * (seq * p.es_n + (int64_t)(first + lane) * p.es_t + head);
+        const int64_t dt_hop = (p.dt_f32 ? 4 : 2) * C * p.ds_t, beta_hop = (p.beta_f32 ? 4 : 2) * C * p.es_t;
         uint32_t dt_raw = 0, beta_raw = 0;
-        auto fetch_gates = [&](int j) {
-            const int64_t t = (int64_t)j * C + lane;
+        auto fetch_gates = [&](int j) {  // chunk after chunk
             dt_raw = beta_raw = 0;
-            if (lane < C && t < len) {
-                dt_raw = p.dt_f32 ? static_cast<const uint32_t *>(p.dt)[dt0 + t * p.ds_t]
-                                  : (uint32_t)static_cast<const uint16_t *>(p.dt)[dt0 + t * p.ds_t] << 16;
-                beta_raw = p.beta_f32 ? static_cast<const uint32_t *>(p.beta)[beta0 + t * p.es_t]
-                                      : (uint32_t)static_cast<const uint16_t *>(p.beta)[beta0 + t * p.es_t] << 16;
+            if (lane < min(C, len - j * C)) {
+                dt_raw = p.dt_f32 ? *reinterpret_cast<const uint32_t *>(dt_at) : *reinterpret_cast<const uint16_t *>(dt_at);
+                beta_raw = p.beta_f32 ? *reinterpret_cast<const uint32_t *>(beta_at)
+                                      : *reinterpret_cast<const uint16_t *>(beta_at);
             }
+            dt_at += dt_hop;
+            beta_at += beta_hop;
         };
         auto put_gates = [&](int j) {
-            float d = __uint_as_float(dt_raw) + bias;
-            if (p.dt_softplus) d = softplus(d);
-            float decay = d * rate, weight = weight_of(p, __uint_as_float(beta_raw));
-            if (lane >= C || j * C + lane >= len) decay = weight = 0.0f;
+            float d = __uint_as_float(p.dt_f32 ? dt_raw : dt_raw << 16) + bias;
+            if (p.dt_softplus) d = softplus_near(d);
+            float decay = d * rate, weight = __uint_as_float(p.beta_f32 ? beta_raw : beta_raw << 16);
+            if (p.beta_sigmoid) weight = sigmoid_near(weight);
+            if (lane >= min(C, len - j * C)) decay = weight = 0.0f;
             if (decay < kNone) decay = kNone;
             if (!is_finite(weight)) decay = __builtin_nanf(""), weight = 0.0f;
             const double c = prefix_sum((double)decay, lane);
             const float high = (float)c;
-            float *tok = tokens + (j & 1) * kTokenRows * C + lane;
+            float *tok = tokens + j % 3 * kTokenRows * C + lane;
             if (lane < C) {
                 tok[kSumHigh * C] = high;
                 tok[kSumLow * C] = (float)(c - (double)high);
                 tok[kWeight * C] = weight;
             }
         };
-        // what the state's waves scale their products by
+        // what the state's waves scale S k, S q and U by
         auto put_scales = [&](int j) {
             if (lane >= C) return;
-            float *tok = tokens + (j & 1) * kTokenRows * C;
+            float *tok = tokens + j % 3 * kTokenRows * C;
             const float high = tok[kSumHigh * C + lane], low = tok[kSumLow * C + lane];
-            const float e = __builtin_amdgcn_exp2f(high + low);
-            const float behind =
-                __builtin_amdgcn_exp2f((tok[kSumHigh * C + C - 1] - high) + (tok[kSumLow * C + C - 1] - low));
-            const float unit = tok[kUnitK * C + lane];
+            const float end = tok[kSumHigh * C + C - 1], end_low = tok[kSumLow * C + C - 1];
+            const float unit = tok[kUnitK * C + lane], e = __builtin_amdgcn_exp2f(high + low);
             tok[kForK * C + lane] = e * unit;
             tok[kForQ * C + lane] = e * tok[kUnitQ * C + lane];
-            tok[kForU * C + lane] = behind * unit;
+            tok[kForU * C + lane] = __builtin_amdgcn_exp2f((end - high) + (end_low - low)) * unit;
         };
-        // ---- tiles of A of chunk j + 1 (transposed: row u, column t) and of P of chunk j
-        auto grams = [&](int ja, bool with_a, bool with_p) {
-            for (int it = with_a ? pw : Z::kTiles + pw; it < (with_p ? 2 : 1) * Z::kTiles; it += kHalf) {
-                const bool is_p = it >= Z::kTiles;
-                const int e = is_p ? it - Z::kTiles : it;
-                const int bt = e >= 6 ? 3 : e >= 3 ? 2 : e >= 1 ? 1 : 0, bu = e - bt * (bt + 1) / 2;
-                const int j = is_p ? ja - 1 : ja;
-                const uint16_t *km = sk + (j & 1) * C * KP, *tm = is_p ? sq + (j & 1) * C * KP : km;
-                const float *tok = tokens + (j & 1) * kTokenRows * C;
-                f32x4_t acc = {0, 0, 0, 0};
+        // ---- the factors that make rows of length one, from the diagonals of the rows'
+        // products with themselves (that of row r in lanes g = r >> 2)
+        auto put_units = [&](int j) {
+            if (pw >= kB) return;
+            const uint16_t *km = sk + (j % 3 * C + 16 * pw) * KS, *qm = sq + (j % 3 * C + 16 * pw) * KS;
+            f32x4_t k2 = {0, 0, 0, 0}, q2 = {0, 0, 0, 0};
+            u32x4 kf[kSteps], qf[kSteps];
+#pragma unroll
+            for (int m = 0; m < kSteps; ++m) kf[m] = lds16(km + row_at(m)), qf[m] = lds16(qm + row_at(m));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < kSteps; ++m) k2 = mfma(kf[m], kf[m], k2), q2 = mfma(qf[m], qf[m], q2);
+            const float k0 = r & 1 ? k2[1] : k2[0], k1 = r & 1 ? k2[3] : k2[2], kk = r & 2 ? k1 : k0;
+            const float q0 = r & 1 ? q2[1] : q2[0], q1 = r & 1 ? q2[3] : q2[2], qq = r & 2 ? q1 : q0;
+            float *tok = tokens + j % 3 * kTokenRows * C + 16 * pw + r;
+            if (g == r >> 2) {
+                tok[kUnitK * C] = is_finite(kk) ? unit_factor(p, kk) : __builtin_nanf("");
+                tok[kUnitQ * C] = p.scale * unit_factor(p, qq);
+            }
+        };
+        // Four values as kTParts parts, `apart` values apart.
+        auto put_parts = [&](float (&v)[4], uint16_t *to, int apart) {
+#pragma unroll
+            for (int part = 0; part < kTParts; ++part) {
+                const uint32_t h0 = pack_bf16x2(v[0], v[1]), h1 = pack_bf16x2(v[2], v[3]);
+                *reinterpret_cast<u32x2 *>(to + part * apart) = u32x2{h0, h1};
+                v[0] -= lo_f32(h0), v[1] -= hi_f32(h0), v[2] -= lo_f32(h1), v[3] -= hi_f32(h1);
+            }
+        };
+        // ---- block row I of A of chunk j + 1 and block row kB - 1 - I of P of chunk j (together as
+        // many tiles for every I).  A tile of A inside a half of 32 tokens is kept in FP32,
+        // transposed (row u, column t); the others, negative and without the weight, as P.
+        auto form = [&](auto row_constant, auto with_p, int j, bool with_a) {
+            constexpr int I = decltype(row_constant)::value, H = I & ~1;  // the half's first block
+            constexpr int J = kB - 1 - I;
+            constexpr bool kWithP = decltype(with_p)::value;
+            const uint16_t *km = sk + (j + 1) % 3 * C * KS, *pm = sk + j % 3 * C * KS, *qm = sq + j % 3 * C * KS;
+            const float *tok = tokens + (j + 1) % 3 * kTokenRows * C, *ptok = tokens + j % 3 * kTokenRows * C;
+            u32x4 tf[kSteps], pf[J + 1][kSteps], f[I + 1][kSteps];
+            f32x4_t pacc[J + 1], ph[J + 1], pl[J + 1], pk[J + 1], acc[I + 1];
+            float pth = 0, ptl = 0, punit = 0, pref = 0, pref_low = 0;
+            if constexpr (kWithP) {
 #pragma unroll
                 for (int m = 0; m < kSteps; ++m) {
-                    const u32x4 u = lds16(km + (16 * bu + r) * KP + 32 * m + 8 * g);
-                    const u32x4 t = lds16(tm + (16 * bt + r) * KP + 32 * m + 8 * g);
-                    acc = is_p ? mfma(u, t, acc) : mfma(t, u, acc);
-                }
-                float v[4];
-                if (is_p) {  // lane: column t = r, rows u
-                    const int t = 16 * bt + r, u0 = 16 * bu + 4 * g;
-                    const f32x4_t uh = lds4f(tok + kSumHigh * C + u0), ul = lds4f(tok + kSumLow * C + u0);
-                    const f32x4_t uk = lds4f(tok + kUnitK * C + u0);
-                    const float th = tok[kSumHigh * C + t], tl = tok[kSumLow * C + t], tq = tok[kUnitQ * C + t];
+                    tf[m] = lds16(qm + 16 * J * KS + row_at(m));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = u0 + i <= t ? acc[i] * tq * uk[i] * __builtin_amdgcn_exp2f((th - uh[i]) + (tl - ul[i])) : 0.0f;
-                    *reinterpret_cast<u32x2 *>(sp + t * TP + 32 * (bu >> 1) + 8 * g + 4 * (bu & 1)) =
-                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                } else {  // lane: column u = r, rows t
-                    const int u = 16 * bu + r, t0 = 16 * bt + 4 * g;
-                    const f32x4_t th = lds4f(tok + kSumHigh * C + t0), tl = lds4f(tok + kSumLow * C + t0);
-                    const f32x4_t tk = lds4f(tok + kUnitK * C + t0), tb = lds4f(tok + kWeight * C + t0);
-                    const float uh = tok[kSumHigh * C + u], ul = tok[kSumLow * C + u], uk = tok[kUnitK * C + u];
+                    for (int b = 0; b <= J; ++b) pf[b][m] = lds16(pm + 16 * b * KS + row_at(m));
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < kSteps; ++m)
+#pragma unroll
+                for (int b = I; b >= 0; --b) f[b][m] = lds16(km + 16 * b * KS + row_at(m));
+            if constexpr (kWithP) {
+                const int t = 16 * J + r;
+                pth = ptok[kSumHigh * C + t], ptl = ptok[kSumLow * C + t], punit = ptok[kUnitQ * C + t];
+                if (J > 0) pref = ptok[kSumHigh * C + 16 * J - 1], pref_low = ptok[kSumLow * C + 16 * J - 1];
+#pragma unroll
+                for (int b = 0; b <= J; ++b) {
+                    const int u0 = 16 * b + 4 * g;
+                    ph[b] = lds4f(ptok + kSumHigh * C + u0), pl[b] = lds4f(ptok + kSumLow * C + u0);
+                    pk[b] = lds4f(ptok + kUnitK * C + u0);
+                    pacc[b] = f32x4_t{0, 0, 0, 0};
+                }
+            }
+            const int t0 = 16 * I + 4 * g;
+            const f32x4_t th = lds4f(tok + kSumHigh * C + t0), tl = lds4f(tok + kSumLow * C + t0);
+            const f32x4_t tw = lds4f(tok + kWeight * C + t0), tu = lds4f(tok + kUnitK * C + t0);
+            const float th1 = tok[kSumHigh * C + 16 * I + r], tl1 = tok[kSumLow * C + 16 * I + r];
+            const float unit1 = tok[kUnitK * C + 16 * I + r];
+            float uh1 = 0, ul1 = 0, uu1 = 0, ref = 0, ref_low = 0;
+            f32x4_t uh[2], ul[2], uu[2];
+            if (I > H)
+                uh1 = tok[kSumHigh * C + 16 * H + r], ul1 = tok[kSumLow * C + 16 * H + r], uu1 = tok[kUnitK * C + 16 * H + r];
+            if (H > 0) {
+                ref = tok[kSumHigh * C + 16 * H - 1], ref_low = tok[kSumLow * C + 16 * H - 1];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int u0 = 16 * b + 4 * g;
+                    uh[b] = lds4f(tok + kSumHigh * C + u0), ul[b] = lds4f(tok + kSumLow * C + u0);
+                    uu[b] = lds4f(tok + kUnitK * C + u0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b <= I; ++b) acc[b] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < kSteps; ++m) {
+                if constexpr (kWithP)
+#pragma unroll
+                    for (int b = 0; b <= J; ++b) pacc[b] = mfma(pf[b][m], tf[m], pacc[b]);
+#pragma unroll
+                for (int b = I; b >= 0; --b) acc[b] = b < H ? mfma(f[b][m], f[I][m], acc[b]) : mfma(f[I][m], f[b][m], acc[b]);
+            }
+            if constexpr (kWithP) {  // lane: column t = r, rows u; decays by way of the block's start
+                const float ft = punit * __builtin_amdgcn_exp2f((pth - pref) + (ptl - pref_low));
+#pragma unroll
+                for (int b = 0; b <= J; ++b) {
+                    float v[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        v[i] = acc[i] * (tk[i] * tb[i]) * uk * __builtin_amdgcn_exp2f((th[i] - uh) + (tl[i] - ul));
-                        if (!(u < t0 + i && is_finite(v[i]))) v[i] = 0.0f;
+                        if (b < J)
+                            v[i] = pacc[b][i] * ft * pk[b][i] * __builtin_amdgcn_exp2f((pref - ph[b][i]) + (pref_low - pl[b][i]));
+                        else
+                            v[i] = 4 * g + i <= r ? pacc[b][i] * punit * pk[b][i] *
+                                                        __builtin_amdgcn_exp2f((pth - ph[b][i]) + (ptl - pl[b][i]))
+                                                  : 0.0f;
                     }
-                    *reinterpret_cast<f32x4_t *>(sa + (e * 16 + r) * kAPitch + 4 * g) = f32x4_t{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<u32x2 *>(sp + (16 * J + r) * PP + 32 * (b >> 1) + 8 * g + 4 * (b & 1)) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                }
+            }
+            if (!with_a) return;
+            const f32x4_t tk = tw * tu;
+            // the diagonal block, and the one beside it: lane: column u = r, rows t
+#pragma unroll
+            for (int b = H; b <= I; ++b) {
+                const float unit = b == I ? unit1 : uu1;
+                const float h1 = b == I ? th1 : uh1, l1 = b == I ? tl1 : ul1;
+                f32x4_t v = acc[b];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] *= tk[i] * unit * __builtin_amdgcn_exp2f((th[i] - h1) + (tl[i] - l1));
+                    if (!((b < I || r < 4 * g + i) && is_finite(v[i]))) v[i] = 0.0f;
+                }
+                *reinterpret_cast<f32x4_t *>(sa + ((3 * (I >> 1) + (b == I ? I - H : 2)) * 16 + r) * kAPitch + 4 * g) = v;
+            }
+            // the first half's: lane: column t = r, rows u; decays by way of the half's start
+            if constexpr (H > 0) {
+                const float ft = -unit1 * __builtin_amdgcn_exp2f((th1 - ref) + (tl1 - ref_low));
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = acc[b][i] * ft * uu[b][i] *
+                               __builtin_amdgcn_exp2f((ref - uh[b][i]) + (ref_low - ul[b][i]));
+                        if (!is_finite(v[i])) v[i] = 0.0f;
+                    }
+                    put_parts(v, so + (16 * (I - H) + r) * TP + 8 * g + 4 * b, (C - 32) * TP);
                 }
             }
         };
         // ---- the inverses of I + A's diagonal blocks, a column a lane, in place (transposed)
         auto invert = [&]() {
-            const int blk = g;
-            if (blk >= kB) return;
-            float *tile = sa + (blk * (blk + 1) / 2 + blk) * 16 * kAPitch;
+            if (g >= kB) return;
+            float *tile = sa + (3 * (g >> 1) + (g & 1)) * 16 * kAPitch;
+            // (a group of A's columns read while the one before is worked off)
+            f32x4_t a[2][4][4];
+            auto read_columns = [&](int u0) {
+#pragma unroll
+                for (int u = u0; u < u0 + 4 && u < 15; ++u)
+#pragma unroll
+                    for (int q = (u + 1) / 4; q < 4; ++q) a[u0 >> 2 & 1][u - u0][q] = lds4f(tile + u * kAPitch + 4 * q);
+            };
             float x[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = i == r ? 1.0f : 0.0f;
+            read_columns(0);
 #pragma unroll
-            for (int u = 0; u < 15; ++u) {
+            for (int u0 = 0; u0 < 15; u0 += 4) {
+                read_columns(u0 + 4);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int q = (u + 1) / 4; q < 4; ++q) {
-                    const f32x4_t a = lds4f(tile + u * kAPitch + 4 * q);
+                for (int u = u0; u < u0 + 4 && u < 15; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (4 * q + i > u) x[4 * q + i] = __builtin_fmaf(-a[i], x[u], x[4 * q + i]);
-                }
+                    for (int i = u + 1; i < 16; ++i)
+                        x[i] = __builtin_fmaf(-a[u0 >> 2 & 1][u - u0][i / 4][i % 4], x[u], x[i]);
             }
             wave_lds_sync();
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 *reinterpret_cast<f32x4_t *>(tile + r * kAPitch + 4 * q) = f32x4_t{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
         };
-        // ---- block row I of T: T_ij = -(sum_{j < k <= i} T_ik A_kj) T_jj, transposed throughout
+        // ---- block row I of its half's T: the diagonal block's inverse, and in the second row
+        // T_10 = -T_11 A_10 T_00, all transposed; times the weights, in parts
         auto join = [&](auto row_constant, int j) {
             constexpr int I = decltype(row_constant)::value;
-            const float *weight = tokens + ((j & 1) * kTokenRows + kWeight) * C;
-            f32x4_t y[I + 1];
-            const float *diag = sa + (I * (I + 1) / 2 + I) * 16 * kAPitch;
+            const float *weight = tokens + (j % 3 * kTokenRows + kWeight) * C + 16 * (I & ~1) + 4 * g;
+            const float *half = sa + 3 * (I >> 1) * 16 * kAPitch;
+            uint16_t *to = st + (16 * I + r) * TP + 8 * g;
+            const float *diag = half + (I & 1) * 16 * kAPitch;
+            f32x4_t y, a, t, w0 = lds4f(weight), w1;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) y[I][s] = diag[(4 * g + s) * kAPitch + r];
-#pragma unroll
-            for (int b = I - 1; b >= 0; --b) {
-                f32x4_t acc = {0, 0, 0, 0};
-#pragma unroll
-                for (int k = I; k > b; --k)
-                    acc = mfma_f32(lds4f(sa + ((k * (k + 1) / 2 + b) * 16 + r) * kAPitch + 4 * g), y[k], acc);
+            for (int s = 0; s < 4; ++s) y[s] = diag[(4 * g + s) * kAPitch + r];
+            if constexpr ((I & 1) == 0) {
+                y *= w0;
+                float v[4] = {y[0], y[1], y[2], y[3]};
+                put_parts(v, to, C * TP);
+            } else {
+                a = lds4f(half + (2 * 16 + r) * kAPitch + 4 * g), t = lds4f(half + r * kAPitch + 4 * g);
+                w1 = lds4f(weight + 16);
                 const f32x4_t zero = {0, 0, 0, 0};
-                y[b] = -mfma_f32(lds4f(sa + ((b * (b + 1) / 2 + b) * 16 + r) * kAPitch + 4 * g), acc, zero);
-            }
-#pragma unroll
-            for (int b = 0; b <= I; ++b) {
-                const f32x4_t w = lds4f(weight + 16 * b + 4 * g);
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = y[b][i] * w[i];
-#pragma unroll
-                for (int part = 0; part < kTParts; ++part) {
-                    const uint32_t h0 = pack_bf16x2(v[0], v[1]), h1 = pack_bf16x2(v[2], v[3]);
-                    *reinterpret_cast<u32x2 *>(st + part * C * TP + (16 * I + r) * TP + 32 * (b >> 1) + 8 * g + 4 * (b & 1)) =
-                        u32x2{h0, h1};
-                    v[0] -= lo_f32(h0), v[1] -= hi_f32(h0), v[2] -= lo_f32(h1), v[3] -= hi_f32(h1);
-                }
+                const f32x4_t x = mfma_f32(t, mfma_f32(a, y, zero), zero) * w0;
+                y *= w1;
+                float v0[4] = {-x[0], -x[1], -x[2], -x[3]}, v1[4] = {y[0], y[1], y[2], y[3]};
+                put_parts(v1, to + 4, C * TP);
+                put_parts(v0, to, C * TP);
             }
         };
 
+        // body(block row) for the block row of this wave
+        auto by_row = [&](int row, auto &&body) {
+            if (row == 0) body(std::integral_constant<int, 0>{});
+            if (row == 1) body(std::integral_constant<int, 1>{});
+            if constexpr (kB > 2) {
+                if (row == 2) body(std::integral_constant<int, 2>{});
+                if (row == 3) body(std::integral_constant<int, 3>{});
+            }
+        };
+        // (what a wave has to do beside its rows goes to those that wait)
+        const bool gates = pw == 2, scales = pw == 1;
+        if (gates) fetch_gates(0);
         fetch(0);
-        if (pw == 0) fetch_gates(0);
-        stage(0);
-        if (pw == 0) put_gates(0);
+        fetch_v(0);
+        wait_for_tiles();
+        block_sync();
         fetch(1);
-        if (pw == 0) fetch_gates(1);
-        __syncthreads();
-        grams(0, true, false);
-        __syncthreads();
+        put_units(0);
+        if (gates) put_gates(0), fetch_gates(1);
+        block_sync();
+        by_row(pw, [&](auto row) { form(row, std::false_type{}, -1, true); });
+        wait_for_tiles();
+        block_sync();
         if (pw == 0) invert();
-        if (pw == 1) put_scales(0);
-        __syncthreads();
+        if (scales) put_scales(0);
+        if (gates) put_gates(1);
+        put_units(1);
+        block_sync();
         for (int j = 0; j < chunks; ++j) {
             const bool more = j + 1 < chunks;
-            if (more) {
-                stage(j + 1);
-                if (pw == 0) put_gates(j + 1);
-                fetch(j + 2);
-                if (pw == 0) fetch_gates(j + 2);
-            }
-            if (pw == 0) join(std::integral_constant<int, 0>{}, j);
-            if (pw == 1) join(std::integral_constant<int, 1>{}, j);
-            if constexpr (kB > 2) {
-                if (pw == 2) join(std::integral_constant<int, 2>{}, j);
-                if (pw == 3) join(std::integral_constant<int, 3>{}, j);
-            }
-            __syncthreads();
-            grams(j + 1, more, true);
-            __syncthreads();
+            if (j + 2 < chunks) fetch(j + 2);
+            by_row(pw, [&](auto row) { join(row, j); });
+            block_sync();
+            if (more) fetch_v(j + 1);
+            if (gates) fetch_gates(j + 2);
+            by_row(pw, [&](auto row) { form(row, std::true_type{}, j, more); });
+            wait_for_tiles();
+            block_sync();
             if (more) {
                 if (pw == 0) invert();
-                if (pw == 1) put_scales(j + 1);
+                if (scales) put_scales(j + 1);
+                if (gates) put_gates(j + 2);
+                if (j + 2 < chunks) put_units(j + 2);
             }
-            __syncthreads();
+            block_sync();
         }
         return;
     }
 
     // ====================================================== the waves that hold the state
-    constexpr int kAcross = Z::kRowsP / 8, kRowsPer = kHalfBlock / kAcross, kMoves = C / kRowsPer;
-    const int vrow = tid / kAcross, vcol = tid % kAcross * 8;
-    const Rows<WIDE> rv(p.v + seq * p.vs_n + (int64_t)first * p.vs_t + head * p.vs_h + p0, p.vs_t, rows, vrow, kRowsPer, vcol);
-    u32x4 nv[kMoves];
-    auto fetch_v = [&](int j) { rv.load(nv, (int64_t)j * C, len - j * C); };
-    auto stage_v = [&]() {
-#pragma unroll
-        for (int q = 0; q < kMoves; ++q) *reinterpret_cast<u32x4 *>(sv + (vrow + q * kRowsPer) * VP + vcol) = nv[q];
-    };
     // Tile n's column r is row own(n, r) of the wave's, so that result rows 4 g .. of the
     // two tiles are eight neighbours.
     const int mine = wave * 16 * NT, left_rows = rows - mine;  // this wave's rows start at p0 + mine
     const auto own = [&](int n, int c) { return NT == 2 ? 8 * (c >> 2) + 4 * n + (c & 3) : c; };
-    const bool busy = left_rows > 0;
+
+    // Outputs of chunk j: a lane holds 4 NT neighbouring rows p of tokens 16 tt + r.
+    auto put_out = [&](const f32x4_t(&o)[kB][NT], int j) {
+        uint16_t *base = out + (int64_t)j * C * p.os_t;
+        const int r = here(lane) & 15, g = here(lane) >> 4;
+        const int left = min(len - j * C, C);
+        const uint32_t pitch = 2u * (uint32_t)p.os_t;
+        const Buffer buf = make_buffer(base, WIDE ? (uint32_t)(left - 1) * pitch + 2u * (uint32_t)rows : 0u);
+        const uint32_t at = 4 * NT * g < left_rows ? (uint32_t)r * pitch + 2u * (uint32_t)(mine + 4 * NT * g) : kNowhere;
+#pragma unroll
+        for (int tt = 0; tt < kB; ++tt) {
+            uint32_t w[2 * NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                w[2 * n] = pack_bf16x2(o[tt][n][0], o[tt][n][1]);
+                w[2 * n + 1] = pack_bf16x2(o[tt][n][2], o[tt][n][3]);
+            }
+            const int t = 16 * tt + r;
+            if (WIDE) {
+                buffer_store_words<2 * NT, kCached>(w, buf, t < left ? at + 16u * (uint32_t)tt * pitch : kNowhere);
+            } else if (t < left) {
+                uint16_t *to = base + t * p.os_t + mine + 4 * NT * g;
+#pragma unroll
+                for (int i = 0; i < 4 * NT; ++i)
+                    if (4 * NT * g + i < left_rows) to[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            }
+        }
+    };
 
     // ---- the state ahead: tile m, rows k = column(m, g) + i, columns p = own(n, r)
     f32x4_t hs[KS / 16][NT];
@@ -553,87 +701,83 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
     for (int m = 0; m < KS / 16; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) hs[m][n] = f32x4_t{0, 0, 0, 0};
+    // body(its tile, its columns' state, byte offset in the head's state, values there of four)
+    constexpr bool kF32 = PARTS > 1;  // the state in memory, where there is one
     const bool wide_state = p.k % 4 == 0 && p.ss_s % 4 == 0 && reinterpret_cast<uintptr_t>(p.state) % 16 == 0;
-    const int64_t state_at = slot * p.ss_s + ((int64_t)head * p.p + p0 + mine) * p.k;
-    if (p.state != nullptr && p.has_init != nullptr && p.has_init[seq] != 0)
+    const auto head_state = [&]() {
+        const int64_t pk = (int64_t)p.p * p.k;
+        return make_buffer(static_cast<const char *>(p.state) + (kF32 ? 4 : 2) * (slot * p.ss_s + head * pk),
+                           (uint32_t)((kF32 ? 4 : 2) * pk));
+    };
+    const auto each_state4 = [&](auto &&body) {
+        const int rr = here(r), gg = here(g);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (own(n, r) < left_rows)
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t row = (uint32_t)(p0 + mine + own(n, rr)) * (uint32_t)p.k;
+            const int most = own(n, rr) < left_rows ? p.k : 0;
 #pragma unroll
-                for (int m = 0; m < KS / 16; ++m)
-                    hs[m][n] = load_state4(p.state, p.state_f32, wide_state,
-                                           state_at + (int64_t)own(n, r) * p.k + column(m, g), p.k - column(m, g));
+            for (int m = 0; m < KS / 16; ++m)
+                body(hs[m][n], (kF32 ? 4u : 2u) * (row + (uint32_t)column(m, gg)), most - column(m, gg));
+        }
+    };
+    if (p.state != nullptr && p.has_init != nullptr && p.has_init[seq] != 0) {
+        const Buffer buf = head_state();
+        if (wide_state)
+            each_state4([&](f32x4_t &v, uint32_t at, int count) { v = load_state4<kF32, true>(buf, at, count); });
+        else
+            each_state4([&](f32x4_t &v, uint32_t at, int count) { v = load_state4<kF32, false>(buf, at, count); });
+    }
 
-    fetch_v(0);
-    stage_v();
-    fetch_v(1);
-    __syncthreads();
-    __syncthreads();
-    __syncthreads();
+    block_sync();
+    block_sync();
+    block_sync();
+    block_sync();
     for (int j = 0; j < chunks; ++j) {
-        const uint16_t *km = sk + (j & 1) * C * KP, *qm = sq + (j & 1) * C * KP;
-        const float *tok = tokens + (j & 1) * kTokenRows * C;
-        int cut[NT];  // the first token whose R or U is not finite
-#pragma unroll
-        for (int n = 0; n < NT; ++n) cut[n] = C;
+        const uint16_t *km = sk + j % 3 * C * KS, *qm = sq + j % 3 * C * KS;
+        const float *tok = tokens + j % 3 * kTokenRows * C;
         f32x4_t d[kB][NT], o[kB][NT];
-        // Zeros for the tokens of d from the first on that is not finite.
-        auto cut_off = [&]() {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                for (int tt = kB - 1; tt >= 0; --tt)
-#pragma unroll
-                    for (int i = 3; i >= 0; --i)
-                        if (!is_finite(d[tt][n][i])) cut[n] = min(cut[n], 16 * tt + 4 * g + i);
-                cut[n] = min(cut[n], __shfl_xor(cut[n], 16));
-                cut[n] = min(cut[n], __shfl_xor(cut[n], 32));
-#pragma unroll
-                for (int tt = 0; tt < kB; ++tt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (16 * tt + 4 * g + i >= cut[n]) d[tt][n][i] = 0.0f;
-            }
-        };
-        auto not_finite = [&]() {
-            float probe = 0.0f;
+        u32x4 rp[NT][PARTS];
+        // ---- d = S k (columns p, rows t), then R
+        {
+            const int lane_here = here(lane), r = lane_here & 15, g = lane_here >> 4;
 #pragma unroll
             for (int tt = 0; tt < kB; ++tt)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) d[tt][n] = f32x4_t{0, 0, 0, 0};
+            // Rows of k, read ahead of their products; the next 32 columns of the state are split meanwhile.
+            u32x4 f[2][kB], hp[2][NT][PARTS];
+            auto read_rows = [&](int m) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) probe = __builtin_fmaf(d[tt][n][i], 0.0f, probe);
-            return __any(probe != 0.0f);
-        };
-        bool bad = false;
-        u32x4 rp[kB / 2][NT][PARTS];
-        // ---- d = S k (columns p, rows t), o = S q (columns t, rows p), then d = R
-        if (busy) {
+                for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(km + 16 * tt * KS + row_at(m));
+            };
+            auto split_state = [&](int m) {
 #pragma unroll
-            for (int tt = 0; tt < kB; ++tt)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) d[tt][n] = o[tt][n] = f32x4_t{0, 0, 0, 0};
+                for (int n = 0; n < NT; ++n) split<PARTS>(hs[2 * m][n], hs[2 * m + 1][n], hp[m & 1][n]);
+            };
+            read_rows(0);
+            split_state(0);
 #pragma unroll
             for (int m = 0; m < kSteps; ++m) {
-                u32x4 kf[kB], qf[kB];
+                if (m + 1 < kSteps) read_rows(m + 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int tt = 0; tt < kB; ++tt) {
-                    kf[tt] = lds16(km + (16 * tt + r) * KP + 32 * m + 8 * g);
-                    qf[tt] = lds16(qm + (16 * tt + r) * KP + 32 * m + 8 * g);
-                }
+                for (int part = PARTS - 1; part >= 0; --part)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    u32x4 hp[PARTS];
-                    split<PARTS>(hs[2 * m][n], hs[2 * m + 1][n], hp);
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int tt = 0; tt < kB; ++tt) {
+                        for (int tt = 0; tt < kB; ++tt) d[tt][n] = mfma(f[m & 1][tt], hp[m & 1][n][part], d[tt][n]);
+                if (m + 1 < kSteps) {
+                    split_state(m + 1);
+                    // a product, and what the vector units do meanwhile
 #pragma unroll
-                        for (int part = PARTS - 1; part >= 0; --part) d[tt][n] = mfma(kf[tt], hp[part], d[tt][n]);
-                        o[tt][n] = mfma(hp[0], qf[tt], o[tt][n]);
+                    for (int i = 0; i < PARTS * NT * kB; ++i) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, PARTS == 1 ? 2 : 4, 0);
                     }
                 }
             }
-            const uint16_t *va = sv + (4 * g + (r >> 2)) * VP + mine + (NT == 2 ? 8 : 4) * (r & 3);
+            const int vrow = 4 * g + (r >> 2), vpiece = NT == 2 ? 4 * wave + (r & 3) : 2 * wave + (r >> 1 & 1);
+            const uint16_t *va = sv + vrow * VP + 8 * (vpiece ^ swap_of<VP / 8>(vrow)) + (NT == 2 ? 0 : 4 * (r & 1));
 #pragma unroll
             for (int m = 0; m < kB / 2; ++m) {
                 const f32x4_t w0 = lds4f(tok + kForK * C + 32 * m + 4 * g), w1 = lds4f(tok + kForK * C + 32 * m + 16 + 4 * g);
@@ -645,80 +789,185 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                         d[2 * m][n][i] = ((i & 1) ? hi_f32(v[i >> 1]) : lo_f32(v[i >> 1])) - w0[i] * d[2 * m][n][i];
                         d[2 * m + 1][n][i] = ((i & 1) ? hi_f32(v[2 + (i >> 1)]) : lo_f32(v[2 + (i >> 1)])) - w1[i] * d[2 * m + 1][n][i];
                     }
+                    if (m == 0) split<PARTS>(d[0][n], d[1][n], rp[n]);
                 }
             }
-            if (not_finite()) {
-                bad = true;
-                cut_off();
-            }
-#pragma unroll
-            for (int m = 0; m < kB / 2; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) split<PARTS>(d[2 * m][n], d[2 * m + 1][n], rp[m][n]);
         }
-        __syncthreads();
-        // ---- d = U = T R
-        if (busy) {
+        block_sync();
+        // ---- d = U, half by half: U_0 = T_0 R_0, U_1 = T_1 (R_1 - A_10 U_0)
+        int cut[NT];  // the first token whose R or U is not finite
+        bool bad = false;
+        u32x4 up[kB / 2][NT][kTParts], wp[kB / 2][NT][PARTS];
+        {
+            const int lane_here = here(lane), r = lane_here & 15, g = lane_here >> 4;
 #pragma unroll
-            for (int tt = 0; tt < kB; ++tt) {
+            for (int n = 0; n < NT; ++n) cut[n] = C;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) d[tt][n] = f32x4_t{0, 0, 0, 0};
+            for (int m = 0; m < kB / 2; ++m) {
+                f32x4_t(&d0)[NT] = d[2 * m], (&d1)[NT] = d[2 * m + 1];
+                if (m > 0) {
+                    u32x4 af[2][kTParts];
 #pragma unroll
-                for (int m = 0; m <= tt / 2; ++m)
+                    for (int a = kTParts - 1; a >= 0; --a)
 #pragma unroll
-                    for (int a = kTParts - 1; a >= 0; --a) {
-                        const u32x4 tf = lds16(st + a * C * TP + (16 * tt + r) * TP + 32 * m + 8 * g);
+                        for (int tt = 0; tt < 2; ++tt) af[tt][a] = lds16(so + (a * (C - 32) + 16 * tt + r) * TP + 8 * g);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                    for (int a = kTParts - 1; a >= 0; --a)
 #pragma unroll
-                            for (int b = PARTS - 1; b >= 0; --b)
-                                if (a + b < kTParts) d[tt][n] = mfma(tf, rp[m][n][b], d[tt][n]);
+                        for (int b = PARTS - 1; b >= 0; --b)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                if (a + b < kTParts) {
+                                    d0[n] = mfma(af[0][a], up[0][n][b], d0[n]);
+                                    d1[n] = mfma(af[1][a], up[0][n][b], d1[n]);
+                                }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if (bad && cut[n] < 32) d0[n] = d1[n] = f32x4_t{0, 0, 0, 0};
+                        split<PARTS>(d0[n], d1[n], rp[n]);
                     }
-            }
-            if (not_finite()) {
-                bad = true;
-                cut_off();
-            } else if (bad) {
+                }
+                u32x4 tf[2][kTParts];
+#pragma unroll
+                for (int a = kTParts - 1; a >= 0; --a)
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt) tf[tt][a] = lds16(st + (a * C + 32 * m + 16 * tt + r) * TP + 8 * g);
+                const f32x4_t w0 = lds4f(tok + kForU * C + 32 * m + 4 * g), w1 = lds4f(tok + kForU * C + 32 * m + 16 + 4 * g);
+                auto correct = [&]() {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) d0[n] = d1[n] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+                    for (int a = kTParts - 1; a >= 0; --a)
+#pragma unroll
+                        for (int b = PARTS - 1; b >= 0; --b)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                if (a + b < kTParts) {
+                                    d0[n] = mfma(tf[0][a], rp[n][b], d0[n]);
+                                    d1[n] = mfma(tf[1][a], rp[n][b], d1[n]);
+                                }
+                };
+                correct();
+                float probe[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int tt = 0; tt < kB; ++tt)
+                    for (int i = 0; i < 4; ++i) probe[i] = __builtin_fmaf(d1[n][i], 0.0f, __builtin_fmaf(d0[n][i], 0.0f, probe[i]));
+                if (__any((probe[0] + probe[1]) + (probe[2] + probe[3]) != 0.0f)) {
+                    // zeros for R from the first token on where it is not finite, U anew, and the same for U
+                    bad = true;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (16 * tt + 4 * g + i >= cut[n]) d[tt][n][i] = 0.0f;
+                    for (int n = 0; n < NT; ++n) {
+                        int at = 32;  // of the half's tokens
+#pragma unroll
+                        for (int i = 7; i >= 0; --i)
+                            if (!is_finite((i & 1) ? hi_f32(rp[n][0][i >> 1]) : lo_f32(rp[n][0][i >> 1])))
+                                at = 16 * (i >> 2) + 4 * g + (i & 3);
+                        at = min(at, __shfl_xor(at, 16));
+                        at = min(at, __shfl_xor(at, 32));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (16 * (i >> 2) + 4 * g + (i & 3) >= at)
+#pragma unroll
+                                for (int part = 0; part < PARTS; ++part)
+                                    rp[n][part][i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+                        if (at < 32) cut[n] = min(cut[n], 32 * m + at);
+                    }
+                    correct();
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (!is_finite(d0[n][i])) cut[n] = min(cut[n], 32 * m + 4 * g + i);
+                            if (!is_finite(d1[n][i])) cut[n] = min(cut[n], 32 * m + 16 + 4 * g + i);
+                        }
+                        cut[n] = min(cut[n], __shfl_xor(cut[n], 16));
+                        cut[n] = min(cut[n], __shfl_xor(cut[n], 32));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (32 * m + 4 * g + i >= cut[n]) d0[n][i] = 0.0f;
+                            if (32 * m + 16 + 4 * g + i >= cut[n]) d1[n][i] = 0.0f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    split<kTParts>(d0[n], d1[n], up[m][n]);
+                    split<PARTS>(d0[n] * w0, d1[n] * w1, wp[m][n]);
+                }
+            }
+            // ---- o = S q (columns t, rows p)
+#pragma unroll
+            for (int tt = 0; tt < kB; ++tt)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) o[tt][n] = f32x4_t{0, 0, 0, 0};
+            u32x4 f[2][kB];
+            auto read_rows = [&](int m) {
+#pragma unroll
+                for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(qm + 16 * tt * KS + row_at(m));
+            };
+            read_rows(0);
+#pragma unroll
+            for (int m = 0; m < kSteps; ++m) {
+                if (m + 1 < kSteps) read_rows(m + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    u32x4 hp[1];
+                    split<1>(hs[2 * m][n], hs[2 * m + 1][n], hp);
+#pragma unroll
+                    for (int tt = 0; tt < kB; ++tt) o[tt][n] = mfma(hp[0], f[m & 1][tt], o[tt][n]);
+                }
             }
         }
-        if (j + 1 < chunks) {
-            stage_v();
-            fetch_v(j + 2);
-        }
-        __syncthreads();
+        block_sync();
         // ---- the outputs, and the state behind the chunk
-        if (busy) {
-            u32x4 up[kB / 2][NT][2];
+        {
+            const int lane_here = here(lane), r = lane_here & 15, g = lane_here >> 4;
+            u32x4 pf[kB][kB / 2], kt[3][kB / 2];
+            float e[kB];
+            auto read_keys = [&](int t) {
+#pragma unroll
+                for (int m = 0; m < kB / 2; ++m) kt[t % 3][m] = load_columns(km + 32 * m * KS + column_at(t), KS);
+            };
+#pragma unroll
+            for (int tt = 0; tt < kB; ++tt) {
+                e[tt] = tok[kForQ * C + 16 * tt + r];
+#pragma unroll
+                for (int m = 0; m <= tt / 2; ++m) pf[tt][m] = lds16(sp + (16 * tt + r) * PP + 32 * m + 8 * g);
+            }
+            const float dec = __builtin_amdgcn_exp2f(tok[kSumHigh * C + C - 1] + tok[kSumLow * C + C - 1]);
+            read_keys(0);
+            read_keys(1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int tt = 0; tt < kB; ++tt)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) o[tt][n] *= e[tt];
 #pragma unroll
             for (int m = 0; m < kB / 2; ++m)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) split<2>(d[2 * m][n], d[2 * m + 1][n], up[m][n]);
+                for (int part = 1; part >= 0; --part)
 #pragma unroll
-            for (int tt = 0; tt < kB; ++tt) {
-                const float e = tok[kForQ * C + 16 * tt + r];
-                u32x4 pf[kB / 2];
+                    for (int tt = 2 * m; tt < kB; ++tt)
 #pragma unroll
-                for (int m = 0; m <= tt / 2; ++m) pf[m] = lds16(sp + (16 * tt + r) * TP + 32 * m + 8 * g);
+                        for (int n = 0; n < NT; ++n) o[tt][n] = mfma(up[m][n][part], pf[tt][m], o[tt][n]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    o[tt][n] *= e;
+            for (int t = 0; t < KS / 16; ++t) {
+                if (t + 2 < KS / 16) read_keys(t + 2);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int m = 0; m <= tt / 2; ++m) {
-                        o[tt][n] = mfma(up[m][n][1], pf[m], o[tt][n]);
-                        o[tt][n] = mfma(up[m][n][0], pf[m], o[tt][n]);
-                    }
-                }
+                for (int n = 0; n < NT; ++n) hs[t][n] *= dec;
+#pragma unroll
+                for (int m = 0; m < kB / 2; ++m)
+#pragma unroll
+                    for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) hs[t][n] = mfma(kt[t % 3][m], wp[m][n][part], hs[t][n]);
             }
             if (bad) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int from = __shfl(cut[n], 4 * g + i);
@@ -726,78 +975,25 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                         for (int tt = 0; tt < kB; ++tt)
                             if (16 * tt + r >= from) o[tt][n][i] = __builtin_nanf("");
                     }
-            }
-            const int left = len - j * C;
-            uint16_t *to = out + (int64_t)j * C * p.os_t + mine + 4 * NT * g;
-#pragma unroll
-            for (int tt = 0; tt < kB; ++tt) {
-                if (16 * tt + r >= left) continue;
-                uint16_t *at = to + (int64_t)(16 * tt + r) * p.os_t;
-                uint32_t w[2 * NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    w[2 * n] = pack_bf16x2(o[tt][n][0], o[tt][n][1]);
-                    w[2 * n + 1] = pack_bf16x2(o[tt][n][2], o[tt][n][3]);
-                }
-                if (WIDE) {
-                    if (4 * NT * g < left_rows) {
-                        if constexpr (NT == 2)
-                            *reinterpret_cast<u32x4 *>(at) = u32x4{w[0], w[1], w[2], w[3]};
-                        else
-                            *reinterpret_cast<u32x2 *>(at) = u32x2{w[0], w[1]};
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4 * NT; ++i)
-                        if (4 * NT * g + i < left_rows) at[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-                }
-            }
-            const float dec =
-                __builtin_amdgcn_exp2f(tok[kSumHigh * C + C - 1] + tok[kSumLow * C + C - 1]);
-            u32x4 wp[kB / 2][NT][PARTS];
-#pragma unroll
-            for (int m = 0; m < kB / 2; ++m) {
-                const f32x4_t w0 = lds4f(tok + kForU * C + 32 * m + 4 * g), w1 = lds4f(tok + kForU * C + 32 * m + 16 + 4 * g);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) split<PARTS>(d[2 * m][n] * w0, d[2 * m + 1][n] * w1, wp[m][n]);
-            }
-            const uint16_t *ka = km + (4 * g + (r >> 2)) * KP + 8 * (r & 3);
-#pragma unroll
-            for (int t = 0; t < KS / 16; ++t) {
-                u32x4 kt[kB / 2];
-#pragma unroll
-                for (int m = 0; m < kB / 2; ++m) kt[m] = load_columns(ka + 32 * m * KP + 32 * (t >> 1) + 4 * (t & 1), KP);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    hs[t][n] *= dec;
-#pragma unroll
-                    for (int m = 0; m < kB / 2; ++m)
-#pragma unroll
-                        for (int part = PARTS - 1; part >= 0; --part) hs[t][n] = mfma(kt[m], wp[m][n][part], hs[t][n]);
-                }
-            }
-            if (bad) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
                     if (cut[n] < C)
 #pragma unroll
                         for (int t = 0; t < KS / 16; ++t)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) hs[t][n][i] = __builtin_nanf("");
+                }
             }
+            put_out(o, j);
         }
-        __syncthreads();
+        block_sync();
     }
 
     // ---- the state behind the sequence
     if (p.state == nullptr) return;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        if (own(n, r) < left_rows)
-#pragma unroll
-            for (int m = 0; m < KS / 16; ++m)
-                store_state4(p.state, p.state_f32, wide_state, state_at + (int64_t)own(n, r) * p.k + column(m, g),
-                             p.k - column(m, g), hs[m][n]);
+    const Buffer buf = head_state();
+    if (wide_state)
+        each_state4([&](f32x4_t &v, uint32_t at, int count) { store_state4<kF32, true>(buf, at, count, v); });
+    else
+        each_state4([&](f32x4_t &v, uint32_t at, int count) { store_state4<kF32, false>(buf, at, count, v); });
 }
 
 // Lets a kernel use a CU's whole LDS; once for each device, whose bit of *done is
