@@ -354,6 +354,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 
     if (wave >= kHalf) {
         // ================================================== the waves that prepare T and P
+        if (chunks == 0) return;
         const int pw = wave - kHalf;
         const Tile<kAcross, C, WIDE> keys = {p.key + seq * p.ks_n + (int64_t)first * p.ks_t + group * p.ks_g, p.ks_t, p.k};
         const Tile<kAcross, C, WIDE> queries = {p.q + seq * p.qs_n + (int64_t)first * p.qs_t + group * p.qs_g, p.qs_t, p.k};
@@ -367,21 +368,13 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         // ---- decays and weights of a chunk's tokens, a lane each (as they are in memory:
         // converting them here would wait for them)
         const float rate = p.a[head] * kLog2e, bias = p.dt_bias != nullptr ? p.dt_bias[head] : 0.0f;
-        const char *dt_at = static_cast<const char *>(p.dt) +
-                            (p.dt_f32 ? 4 : 2) * (seq * p.ds_n + (int64_t)(first + lane) * p.ds_t + head);
-        const char *beta_at = static_cast<const char *>(p.beta) +
-                              (p.beta_f32 ? 4 : 2) * (seq * p.es_n + (int64_t)(first + lane) * p.es_t + head);
-        const int64_t dt_hop = (p.dt_f32 ? 4 : 2) * C * p.ds_t, beta_hop = (p.beta_f32 ? 4 : 2) * C * p.es_t;
+        const int64_t dt0 = seq * p.ds_n + (int64_t)first * p.ds_t + head, beta0 = seq * p.es_n + (int64_t)first * p.es_t + head;
         uint32_t dt_raw = 0, beta_raw = 0;
-        auto fetch_gates = [&](int j) {  // chunk after chunk
-            dt_raw = beta_raw = 0;
-            if (lane < min(C, len - j * C)) {
-                dt_raw = p.dt_f32 ? *reinterpret_cast<const uint32_t *>(dt_at) : *reinterpret_cast<const uint16_t *>(dt_at);
-                beta_raw = p.beta_f32 ? *reinterpret_cast<const uint32_t *>(beta_at)
-                                      : *reinterpret_cast<const uint16_t *>(beta_at);
-            }
-            dt_at += dt_hop;
-            beta_at += beta_hop;
+        auto fetch_gates = [&](int j) {  // (behind the end: the last token's, which put_gates leaves out)
+            const int64_t t = min(j * C + lane, len - 1);
+            const int64_t d = dt0 + t * p.ds_t, e = beta0 + t * p.es_t;
+            dt_raw = p.dt_f32 ? static_cast<const uint32_t *>(p.dt)[d] : static_cast<const uint16_t *>(p.dt)[d];
+            beta_raw = p.beta_f32 ? static_cast<const uint32_t *>(p.beta)[e] : static_cast<const uint16_t *>(p.beta)[e];
         };
         auto put_gates = [&](int j) {
             float d = __uint_as_float(p.dt_f32 ? dt_raw : dt_raw << 16) + bias;
@@ -431,127 +424,165 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                 tok[kUnitQ * C] = p.scale * unit_factor(p, qq);
             }
         };
-        // Four values as kTParts parts, `apart` values apart.
-        auto put_parts = [&](float (&v)[4], uint16_t *to, int apart) {
+        // Four values as kTParts parts, and put `apart` values apart.
+        auto to_parts = [&](float (&v)[4], u32x2 (&parts)[kTParts]) {
 #pragma unroll
             for (int part = 0; part < kTParts; ++part) {
                 const uint32_t h0 = pack_bf16x2(v[0], v[1]), h1 = pack_bf16x2(v[2], v[3]);
-                *reinterpret_cast<u32x2 *>(to + part * apart) = u32x2{h0, h1};
+                parts[part] = u32x2{h0, h1};
                 v[0] -= lo_f32(h0), v[1] -= hi_f32(h0), v[2] -= lo_f32(h1), v[3] -= hi_f32(h1);
             }
         };
-        // ---- block row I of A of chunk j + 1 and block row kB - 1 - I of P of chunk j (together as
-        // many tiles for every I).  A tile of A inside a half of 32 tokens is kept in FP32,
-        // transposed (row u, column t); the others, negative and without the weight, as P.
-        auto form = [&](auto row_constant, auto with_p, int j, bool with_a) {
-            constexpr int I = decltype(row_constant)::value, H = I & ~1;  // the half's first block
-            constexpr int J = kB - 1 - I;
-            constexpr bool kWithP = decltype(with_p)::value;
-            const uint16_t *km = sk + (j + 1) % 3 * C * KS, *pm = sk + j % 3 * C * KS, *qm = sq + j % 3 * C * KS;
-            const float *tok = tokens + (j + 1) % 3 * kTokenRows * C, *ptok = tokens + j % 3 * kTokenRows * C;
-            u32x4 tf[kSteps], pf[J + 1][kSteps], f[I + 1][kSteps];
-            f32x4_t pacc[J + 1], ph[J + 1], pl[J + 1], pk[J + 1], acc[I + 1];
-            float pth = 0, ptl = 0, punit = 0, pref = 0, pref_low = 0;
-            if constexpr (kWithP) {
+        auto put_parts = [&](float (&v)[4], uint16_t *to, int apart) {
+            u32x2 parts[kTParts];
+            to_parts(v, parts);
 #pragma unroll
-                for (int m = 0; m < kSteps; ++m) {
-                    tf[m] = lds16(qm + 16 * J * KS + row_at(m));
+            for (int part = 0; part < kTParts; ++part) *reinterpret_cast<u32x2 *>(to + part * apart) = parts[part];
+        };
+        // ---- block row I of P of chunk j
+        auto form_p = [&](auto row_constant, int j) {
+            constexpr int I = decltype(row_constant)::value;
+            const uint16_t *km = sk + j % 3 * C * KS, *qm = sq + j % 3 * C * KS;
+            const float *tok = tokens + j % 3 * kTokenRows * C;
+            u32x4 tf[kSteps], f[I + 1][kSteps];
+            f32x4_t acc[I + 1], uh[I + 1], ul[I + 1], uk[I + 1];
 #pragma unroll
-                    for (int b = 0; b <= J; ++b) pf[b][m] = lds16(pm + 16 * b * KS + row_at(m));
-                }
+            for (int m = 0; m < kSteps; ++m) {
+                tf[m] = lds16(qm + 16 * I * KS + row_at(m));
+#pragma unroll
+                for (int b = 0; b <= I; ++b) f[b][m] = lds16(km + 16 * b * KS + row_at(m));
             }
+            const int t = 16 * I + r;
+            const float th = tok[kSumHigh * C + t], tl = tok[kSumLow * C + t], unit = tok[kUnitQ * C + t];
+            float ref = 0, ref_low = 0;
+            if (I > 0) ref = tok[kSumHigh * C + 16 * I - 1], ref_low = tok[kSumLow * C + 16 * I - 1];
 #pragma unroll
-            for (int m = 0; m < kSteps; ++m)
-#pragma unroll
-                for (int b = I; b >= 0; --b) f[b][m] = lds16(km + 16 * b * KS + row_at(m));
-            if constexpr (kWithP) {
-                const int t = 16 * J + r;
-                pth = ptok[kSumHigh * C + t], ptl = ptok[kSumLow * C + t], punit = ptok[kUnitQ * C + t];
-                if (J > 0) pref = ptok[kSumHigh * C + 16 * J - 1], pref_low = ptok[kSumLow * C + 16 * J - 1];
-#pragma unroll
-                for (int b = 0; b <= J; ++b) {
-                    const int u0 = 16 * b + 4 * g;
-                    ph[b] = lds4f(ptok + kSumHigh * C + u0), pl[b] = lds4f(ptok + kSumLow * C + u0);
-                    pk[b] = lds4f(ptok + kUnitK * C + u0);
-                    pacc[b] = f32x4_t{0, 0, 0, 0};
-                }
-            }
-            const int t0 = 16 * I + 4 * g;
-            const f32x4_t th = lds4f(tok + kSumHigh * C + t0), tl = lds4f(tok + kSumLow * C + t0);
-            const f32x4_t tw = lds4f(tok + kWeight * C + t0), tu = lds4f(tok + kUnitK * C + t0);
-            const float th1 = tok[kSumHigh * C + 16 * I + r], tl1 = tok[kSumLow * C + 16 * I + r];
-            const float unit1 = tok[kUnitK * C + 16 * I + r];
-            float uh1 = 0, ul1 = 0, uu1 = 0, ref = 0, ref_low = 0;
-            f32x4_t uh[2], ul[2], uu[2];
-            if (I > H)
-                uh1 = tok[kSumHigh * C + 16 * H + r], ul1 = tok[kSumLow * C + 16 * H + r], uu1 = tok[kUnitK * C + 16 * H + r];
-            if (H > 0) {
-                ref = tok[kSumHigh * C + 16 * H - 1], ref_low = tok[kSumLow * C + 16 * H - 1];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int u0 = 16 * b + 4 * g;
-                    uh[b] = lds4f(tok + kSumHigh * C + u0), ul[b] = lds4f(tok + kSumLow * C + u0);
-                    uu[b] = lds4f(tok + kUnitK * C + u0);
-                }
+            for (int b = 0; b <= I; ++b) {
+                const int u0 = 16 * b + 4 * g;
+                uh[b] = lds4f(tok + kSumHigh * C + u0), ul[b] = lds4f(tok + kSumLow * C + u0);
+                uk[b] = lds4f(tok + kUnitK * C + u0);
+                acc[b] = f32x4_t{0, 0, 0, 0};
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int b = 0; b <= I; ++b) acc[b] = f32x4_t{0, 0, 0, 0};
+            for (int m = 0; m < kSteps; ++m)
 #pragma unroll
-            for (int m = 0; m < kSteps; ++m) {
-                if constexpr (kWithP)
+                for (int b = 0; b <= I; ++b) acc[b] = mfma(f[b][m], tf[m], acc[b]);
+            // lane: column t = r, rows u; decays by way of the block's start
+            const float ft = unit * __builtin_amdgcn_exp2f((th - ref) + (tl - ref_low));
 #pragma unroll
-                    for (int b = 0; b <= J; ++b) pacc[b] = mfma(pf[b][m], tf[m], pacc[b]);
-#pragma unroll
-                for (int b = I; b >= 0; --b) acc[b] = b < H ? mfma(f[b][m], f[I][m], acc[b]) : mfma(f[I][m], f[b][m], acc[b]);
-            }
-            if constexpr (kWithP) {  // lane: column t = r, rows u; decays by way of the block's start
-                const float ft = punit * __builtin_amdgcn_exp2f((pth - pref) + (ptl - pref_low));
-#pragma unroll
-                for (int b = 0; b <= J; ++b) {
-                    float v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (b < J)
-                            v[i] = pacc[b][i] * ft * pk[b][i] * __builtin_amdgcn_exp2f((pref - ph[b][i]) + (pref_low - pl[b][i]));
-                        else
-                            v[i] = 4 * g + i <= r ? pacc[b][i] * punit * pk[b][i] *
-                                                        __builtin_amdgcn_exp2f((pth - ph[b][i]) + (ptl - pl[b][i]))
-                                                  : 0.0f;
-                    }
-                    *reinterpret_cast<u32x2 *>(sp + (16 * J + r) * PP + 32 * (b >> 1) + 8 * g + 4 * (b & 1)) =
-                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                }
-            }
-            if (!with_a) return;
-            const f32x4_t tk = tw * tu;
-            // the diagonal block, and the one beside it: lane: column u = r, rows t
-#pragma unroll
-            for (int b = H; b <= I; ++b) {
-                const float unit = b == I ? unit1 : uu1;
-                const float h1 = b == I ? th1 : uh1, l1 = b == I ? tl1 : ul1;
-                f32x4_t v = acc[b];
+            for (int b = 0; b <= I; ++b) {
+                float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[i] *= tk[i] * unit * __builtin_amdgcn_exp2f((th[i] - h1) + (tl[i] - l1));
-                    if (!((b < I || r < 4 * g + i) && is_finite(v[i]))) v[i] = 0.0f;
+                    if (b < I)
+                        v[i] = acc[b][i] * ft * uk[b][i] * __builtin_amdgcn_exp2f((ref - uh[b][i]) + (ref_low - ul[b][i]));
+                    else
+                        v[i] = 4 * g + i <= r ? acc[b][i] * unit * uk[b][i] *
+                                                    __builtin_amdgcn_exp2f((th - uh[b][i]) + (tl - ul[b][i]))
+                                              : 0.0f;
                 }
-                *reinterpret_cast<f32x4_t *>(sa + ((3 * (I >> 1) + (b == I ? I - H : 2)) * 16 + r) * kAPitch + 4 * g) = v;
+                *reinterpret_cast<u32x2 *>(sp + t * PP + 32 * (b >> 1) + 8 * g + 4 * (b & 1)) =
+                    u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
             }
-            // the first half's: lane: column t = r, rows u; decays by way of the half's start
-            if constexpr (H > 0) {
-                const float ft = -unit1 * __builtin_amdgcn_exp2f((th1 - ref) + (tl1 - ref_low));
+        };
+        // ---- A of chunk j, tile by tile.  Tiles inside a half of 32 tokens are kept in FP32,
+        // transposed (row u, column t); the others, negative and without the weight, as P.
+        struct Log {
+            float high, low;
+            __device__ __forceinline__ float to(const Log &u) const {  // e^{this - u}
+                return __builtin_amdgcn_exp2f((high - u.high) + (low - u.low));
+            }
+        };
+        auto log_at = [&](const float *tok, int t) { return Log{tok[kSumHigh * C + t], tok[kSumLow * C + t]}; };
+        struct Logs {
+            f32x4_t high, low;
+        };
+        auto logs_at = [&](const float *tok, int t) {
+            return Logs{lds4f(tok + kSumHigh * C + t), lds4f(tok + kSumLow * C + t)};
+        };
+        u32x2 off[2][kTParts];  // what this wave has formed of the tiles between halves
+        auto form_a = [&](auto wave_constant, int j) {
+            // wave W's tiles: diagonal block W, and: blocks (2, W) and (3, W) for W = 0, 1, block
+            // (1, 0) for W = 2 and (3, 2) for W = 3.  (Two blocks: (0, 0), and (1, 1) and (1, 0).)
+            constexpr int W = decltype(wave_constant)::value;
+            constexpr bool kOff = kB > 2 && W < 2, kSide = kB > 2 ? W >= 2 : W == 1;
+            constexpr int S = kB > 2 && W == 3 ? 3 : 1;  // the block beside it: (S, S - 1)
+            const uint16_t *km = sk + j % 3 * C * KS;
+            const float *tok = tokens + j % 3 * kTokenRows * C;
+            u32x4 f[kSteps], x[kSteps], y[kSteps];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    float v[4];
+            for (int m = 0; m < kSteps; ++m) {
+                f[m] = lds16(km + 16 * W * KS + row_at(m));
+                if (kOff) x[m] = lds16(km + 32 * KS + row_at(m)), y[m] = lds16(km + 48 * KS + row_at(m));
+                if (kSide) y[m] = lds16(km + 16 * (S - 1) * KS + row_at(m));
+                if (kSide && S != W) x[m] = lds16(km + 16 * S * KS + row_at(m));
+            }
+            const int t0 = 16 * W + 4 * g, s0 = 16 * S + 4 * g;
+            const Logs tl = logs_at(tok, t0);
+            const f32x4_t tw = lds4f(tok + kWeight * C + t0), tu = lds4f(tok + kUnitK * C + t0);
+            const Log ul = log_at(tok, 16 * W + r);
+            const float uu = tok[kUnitK * C + 16 * W + r];
+            Logs sl = tl;
+            f32x4_t sw = tw, su = tu;
+            Log vl = {0, 0}, ref = {0, 0}, xl = {0, 0}, yl = {0, 0};
+            float vu = 0, xu = 0, yu = 0;
+            if (kSide) {
+                vl = log_at(tok, 16 * (S - 1) + r), vu = tok[kUnitK * C + 16 * (S - 1) + r];
+                if (S != W) sl = logs_at(tok, s0), sw = lds4f(tok + kWeight * C + s0), su = lds4f(tok + kUnitK * C + s0);
+            }
+            if (kOff) {
+                ref = log_at(tok, 31), xl = log_at(tok, 32 + r), yl = log_at(tok, 48 + r);
+                xu = tok[kUnitK * C + 32 + r], yu = tok[kUnitK * C + 48 + r];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4_t self = {0, 0, 0, 0}, a0 = {0, 0, 0, 0}, a1 = {0, 0, 0, 0};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[i] = acc[b][i] * ft * uu[b][i] *
-                               __builtin_amdgcn_exp2f((ref - uh[b][i]) + (ref_low - ul[b][i]));
-                        if (!is_finite(v[i])) v[i] = 0.0f;
-                    }
-                    put_parts(v, so + (16 * (I - H) + r) * TP + 8 * g + 4 * b, (C - 32) * TP);
+            for (int m = 0; m < kSteps; ++m) {
+                self = mfma(f[m], f[m], self);
+                if (kOff) a0 = mfma(f[m], x[m], a0), a1 = mfma(f[m], y[m], a1);  // columns t, rows u
+                if (kSide) a0 = mfma(S != W ? x[m] : f[m], y[m], a0);           // columns u, rows t
+            }
+            float *tile = sa + (3 * (W >> 1) + (W & 1)) * 16 * kAPitch + r * kAPitch + 4 * g;
+            f32x4_t v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = self[i] * (tw[i] * tu[i]) * uu * Log{tl.high[i], tl.low[i]}.to(ul);
+                if (!(r < 4 * g + i && is_finite(v[i]))) v[i] = 0.0f;
+            }
+            *reinterpret_cast<f32x4_t *>(tile) = v;
+            if (kSide) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = a0[i] * (sw[i] * su[i]) * vu * Log{sl.high[i], sl.low[i]}.to(vl);
+                    if (!is_finite(v[i])) v[i] = 0.0f;
                 }
+                *reinterpret_cast<f32x4_t *>(sa + (3 * (S >> 1) + 2) * 16 * kAPitch + r * kAPitch + 4 * g) = v;
+            }
+            if (kOff) {  // decays by way of the second half's start
+                f32x4_t fu;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fu[i] = -tu[i] * ref.to(Log{tl.high[i], tl.low[i]});
+                const float fx = xu * xl.to(ref), fy = yu * yl.to(ref);
+                float v0[4], v1[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v0[i] = a0[i] * fx * fu[i], v1[i] = a1[i] * fy * fu[i];
+                    if (!is_finite(v0[i])) v0[i] = 0.0f;
+                    if (!is_finite(v1[i])) v1[i] = 0.0f;
+                }
+                to_parts(v0, off[0]);
+                to_parts(v1, off[1]);
+            }
+        };
+        // (written once the state's waves have done with the chunk before)
+        auto put_off = [&](int w) {
+            if (kB == 2 || w >= 2) return;
+#pragma unroll
+            for (int part = 0; part < kTParts; ++part) {
+                uint16_t *to = so + (part * (C - 32) + r) * TP + 8 * g + 4 * w;
+                *reinterpret_cast<u32x2 *>(to) = off[0][part];
+                *reinterpret_cast<u32x2 *>(to + 16 * TP) = off[1][part];
             }
         };
         // ---- the inverses of I + A's diagonal blocks, a column a lane, in place (transposed)
@@ -621,8 +652,19 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                 if (row == 3) body(std::integral_constant<int, 3>{});
             }
         };
-        // (what a wave has to do beside its rows goes to those that wait)
-        const bool gates = pw == 2, scales = pw == 1;
+        // the rows of P, for the waves beside the one that inverts
+        auto form_p_shared = [&](int j) {
+            if constexpr (kB > 2) {
+                if (pw == 1) form_p(std::integral_constant<int, 3>{}, j);
+                if (pw == 2) form_p(std::integral_constant<int, 2>{}, j);
+                if (pw == 3) form_p(std::integral_constant<int, 1>{}, j), form_p(std::integral_constant<int, 0>{}, j);
+            } else {
+                if (pw == 1) form_p(std::integral_constant<int, 1>{}, j);
+                if (pw == 2) form_p(std::integral_constant<int, 0>{}, j);
+            }
+        };
+        // (what a wave has to do beside its tiles goes to those that wait)
+        const bool gates = pw == 2, scales = pw == 0;
         if (gates) fetch_gates(0);
         fetch(0);
         fetch_v(0);
@@ -632,26 +674,31 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         put_units(0);
         if (gates) put_gates(0), fetch_gates(1);
         block_sync();
-        by_row(pw, [&](auto row) { form(row, std::false_type{}, -1, true); });
-        wait_for_tiles();
+        by_row(pw, [&](auto w) { form_a(w, 0); });
         block_sync();
         if (pw == 0) invert();
-        if (scales) put_scales(0);
         if (gates) put_gates(1);
+        wait_for_tiles();
+        block_sync();
+        by_row(pw, [&](auto row) { join(row, 0); });
+        put_off(pw);
+        if (scales) put_scales(0);
         put_units(1);
         block_sync();
         for (int j = 0; j < chunks; ++j) {
             const bool more = j + 1 < chunks;
+            if (gates) fetch_gates(j + 2);
             if (j + 2 < chunks) fetch(j + 2);
-            by_row(pw, [&](auto row) { join(row, j); });
+            if (more) by_row(pw, [&](auto w) { form_a(w, j + 1); });
             block_sync();
             if (more) fetch_v(j + 1);
-            if (gates) fetch_gates(j + 2);
-            by_row(pw, [&](auto row) { form(row, std::true_type{}, j, more); });
+            if (more && pw == 0) invert();
+            form_p_shared(j);
             wait_for_tiles();
             block_sync();
             if (more) {
-                if (pw == 0) invert();
+                by_row(pw, [&](auto row) { join(row, j + 1); });
+                put_off(pw);
                 if (scales) put_scales(j + 1);
                 if (gates) put_gates(j + 2);
                 if (j + 2 < chunks) put_units(j + 2);
@@ -728,10 +775,8 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             each_state4([&](f32x4_t &v, uint32_t at, int count) { v = load_state4<kF32, false>(buf, at, count); });
     }
 
-    block_sync();
-    block_sync();
-    block_sync();
-    block_sync();
+    if (chunks > 0)
+        for (int i = 0; i < 5; ++i) block_sync();
     for (int j = 0; j < chunks; ++j) {
         const uint16_t *km = sk + j % 3 * C * KS, *qm = sq + j % 3 * C * KS;
         const float *tok = tokens + j % 3 * kTokenRows * C;
@@ -775,6 +820,31 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                         __builtin_amdgcn_sched_group_barrier(0x002, PARTS == 1 ? 2 : 4, 0);
                     }
                 }
+            }
+            {
+            // ---- o = S q (columns t, rows p)
+#pragma unroll
+            for (int tt = 0; tt < kB; ++tt)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) o[tt][n] = f32x4_t{0, 0, 0, 0};
+            u32x4 f[2][kB];
+            auto read_rows = [&](int m) {
+#pragma unroll
+                for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(qm + 16 * tt * KS + row_at(m));
+            };
+            read_rows(0);
+#pragma unroll
+            for (int m = 0; m < kSteps; ++m) {
+                if (m + 1 < kSteps) read_rows(m + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    u32x4 hp[1];
+                    split<1>(hs[2 * m][n], hs[2 * m + 1][n], hp);
+#pragma unroll
+                    for (int tt = 0; tt < kB; ++tt) o[tt][n] = mfma(hp[0], f[m & 1][tt], o[tt][n]);
+                }
+            }
             }
             const int vrow = 4 * g + (r >> 2), vpiece = NT == 2 ? 4 * wave + (r & 3) : 2 * wave + (r >> 1 & 1);
             const uint16_t *va = sv + vrow * VP + 8 * (vpiece ^ swap_of<VP / 8>(vrow)) + (NT == 2 ? 0 : 4 * (r & 1));
@@ -894,29 +964,6 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                 for (int n = 0; n < NT; ++n) {
                     split<kTParts>(d0[n], d1[n], up[m][n]);
                     split<PARTS>(d0[n] * w0, d1[n] * w1, wp[m][n]);
-                }
-            }
-            // ---- o = S q (columns t, rows p)
-#pragma unroll
-            for (int tt = 0; tt < kB; ++tt)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) o[tt][n] = f32x4_t{0, 0, 0, 0};
-            u32x4 f[2][kB];
-            auto read_rows = [&](int m) {
-#pragma unroll
-                for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(qm + 16 * tt * KS + row_at(m));
-            };
-            read_rows(0);
-#pragma unroll
-            for (int m = 0; m < kSteps; ++m) {
-                if (m + 1 < kSteps) read_rows(m + 1);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    u32x4 hp[1];
-                    split<1>(hs[2 * m][n], hs[2 * m + 1][n], hp);
-#pragma unroll
-                    for (int tt = 0; tt < kB; ++tt) o[tt][n] = mfma(hp[0], f[m & 1][tt], o[tt][n]);
                 }
             }
         }
