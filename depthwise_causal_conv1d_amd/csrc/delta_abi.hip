@@ -50,7 +50,7 @@ int check_delta(int64_t n, int64_t h, int64_t p, int64_t g, int64_t k, int dt_dt
 }
 
 // Spans, addresses and overlaps of a call with `rows` rows of t tokens (n sequences), and its launch.
-int run_delta(const dcconv::DeltaParams &q, int64_t rows, int64_t slots, bool scan, void *stream) {
+int run_delta(const dcconv::DeltaParams &q, int64_t rows, int64_t slots, int64_t workspace_bytes, bool scan, void *stream) {
     const int64_t n = q.n, t = q.t, h = q.h, p = q.p, g = q.g, k = q.k;
     if (t > 0 && !rows_distinct({rows, t, h}, {q.os_n, q.os_t, q.os_h}, p))
         return fail(DCCONV_EINVAL, "out strides (%lld, %lld, %lld, 1) give two elements the same address",
@@ -67,6 +67,7 @@ int run_delta(const dcconv::DeltaParams &q, int64_t rows, int64_t slots, bool sc
         return fail(DCCONV_EINVAL, "strides span more than 2^47 bytes");
     const Operand ops[] = {{"out", q.out, ob, 2, true},
                            {"state", q.state, sb, state_bytes, true},
+                           {"workspace", q.workspace, workspace_bytes, 16, true},
                            {"dev_status", q.status, 4, 4, true},
                            {"q", q.q, qb, 2, false},
                            {"key", q.key, kb, 2, false},
@@ -121,7 +122,15 @@ extern "C" int dcconv_gated_delta_update(const void *q, const void *key, const v
     c.dt_f32 = dt_dtype == DCCONV_DTYPE_F32, c.beta_f32 = beta_dtype == DCCONV_DTYPE_F32;
     c.state_f32 = state_dtype == DCCONV_DTYPE_F32;
     c.dt_softplus = dt_softplus != 0, c.beta_sigmoid = beta_sigmoid != 0, c.l2norm = qk_l2norm != 0;
-    return run_delta(c, n, s, false, stream);
+    return run_delta(c, n, s, 0, false, stream);
+}
+
+extern "C" int64_t dcconv_gated_delta_scan_workspace(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k,
+                                                     int packed) {
+    if (n < 1 || t < 1 || h < 1 || p < 1 || g < 1 || k < 1 || h % g != 0 || n > kI32Max - (1 << 24) || t > kI32Max - 1024 ||
+        h > (1 << 20) || p > (1 << 20) || h * p > (1 << 26) || k > kMaxKey)
+        return 0;
+    return 4 * dcconv::delta_scan_workspace_floats(n, t, h, p, k, packed != 0);
 }
 
 extern "C" int dcconv_gated_delta_scan(const void *q, const void *key, const void *v, int64_t n, int64_t t, int64_t h,
@@ -133,7 +142,8 @@ extern "C" int dcconv_gated_delta_scan(const void *q, const void *key, const voi
                                        float l2norm_eps, float scale, const int32_t *seq_starts, void *state,
                                        int state_dtype, int64_t s, int64_t ss_s, const int32_t *state_indices,
                                        const uint8_t *has_initial_state, void *out, int64_t os_n, int64_t os_t,
-                                       int64_t os_h, int32_t *dev_status, void *stream) {
+                                       int64_t os_h, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
+                                       void *stream) {
     const bool stateless = state == nullptr && s == 0;
     if (stateless && (has_initial_state != nullptr || state_indices != nullptr))
         return fail(DCCONV_EINVAL, "has_initial_state and state_indices need a state");
@@ -142,8 +152,9 @@ extern "C" int dcconv_gated_delta_scan(const void *q, const void *key, const voi
     if (rc != DCCONV_OK) return rc;
     if (t < 0) return fail(DCCONV_EINVAL, "t (tokens) must be >= 0, got %lld", (long long)t);
     if (t > kI32Max - 1024) return fail(DCCONV_EUNSUPPORTED, "t >= 2^31 - 1024 tokens is not served");
-    if (any_negative({qs_n, qs_t, qs_g, ks_n, ks_t, ks_g, vs_n, vs_t, vs_h, ds_n, ds_t, es_n, es_t, os_n, os_t, os_h}))
-        return fail(DCCONV_EINVAL, "strides must be non-negative");
+    if (any_negative({qs_n, qs_t, qs_g, ks_n, ks_t, ks_g, vs_n, vs_t, vs_h, ds_n, ds_t, es_n, es_t, os_n, os_t, os_h,
+                      workspace_bytes}))
+        return fail(DCCONV_EINVAL, "strides and workspace_bytes must be non-negative");
     if (n == 0 || (t == 0 && stateless)) return succeed("");
     if (!a || (!state && s > 0) || (t > 0 && (!q || !key || !v || !dt || !beta || !out)))
         return fail(DCCONV_EINVAL, "q, key, v, dt, a, beta, out (and state when s > 0) must be non-NULL");
@@ -167,7 +178,12 @@ extern "C" int dcconv_gated_delta_scan(const void *q, const void *key, const voi
     c.dt_f32 = dt_dtype == DCCONV_DTYPE_F32, c.beta_f32 = beta_dtype == DCCONV_DTYPE_F32;
     c.state_f32 = state_dtype == DCCONV_DTYPE_F32;
     c.dt_softplus = dt_softplus != 0, c.beta_sigmoid = beta_sigmoid != 0, c.l2norm = qk_l2norm != 0;
-    return run_delta(c, packed ? 1 : n, s, true, stream);
+    const int64_t need = dcconv_gated_delta_scan_workspace(n, t, h, p, g, k, packed);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(DCCONV_EINVAL, "workspace of %lld bytes needed, got %lld", (long long)need,
+                    (long long)(workspace ? workspace_bytes : 0));
+    c.workspace = need > 0 ? static_cast<float *>(workspace) : nullptr;
+    return run_delta(c, packed ? 1 : n, s, need, true, stream);
 }
 
 namespace {

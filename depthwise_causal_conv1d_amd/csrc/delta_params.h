@@ -25,12 +25,16 @@ struct DeltaParams {
     int32_t *status;
     uint16_t *out;  // BF16 [n, t, h, p]
     int64_t os_n, os_t, os_h;
+    float *workspace;
     int32_t n, t, h, p, g, k, s;
     float eps, scale;
     bool dt_f32, dt_softplus, beta_f32, beta_sigmoid, l2norm, state_f32;
 };
 
 hipError_t launch_delta_update(const DeltaParams &p, hipStream_t stream, const char **kernel_name);
+// Floats of workspace a scan needs (0: none).
+int64_t delta_scan_workspace_floats(int64_t n, int64_t t, int64_t h, int64_t p, int64_t k, bool packed);
+
 hipError_t launch_delta_scan(const DeltaParams &p, hipStream_t stream, const char **kernel_name);
 
 // Rows [n, t, h] of d values, normed and gated.

@@ -74,7 +74,16 @@ constexpr uint32_t kNowhere = 0x80000000u;    // past the end of every buffer
 // of k and q; and from them what scales S k, S q and U.
 enum { kSumHigh, kSumLow, kWeight, kUnitK, kUnitQ, kForK, kForQ, kForU, kTokenRows };
 
+// How a call is cut up; the same on the host and in every kernel.
 struct ScanPlan {
+    int32_t seg;    // tokens of a segment (a multiple of a chunk's)
+    int32_t nseg;   // segments of a sequence (batch form)
+    int32_t slots;  // segments in all; packed: an upper bound, some empty
+    bool split;     // some sequence may have more than one segment
+    bool two;       // blocks of 128 state rows, not 64
+};
+// One kernel's blocks.
+struct ScanGrid {
     int32_t tiles;  // blocks of a head
     int32_t each;   // blocks of a group
     bool runs;      // a group's blocks follow each other on one XCD
@@ -263,6 +272,48 @@ __device__ __forceinline__ void check_table(const DeltaParams &p) {
     if (bad) atomicOr(p.status, DCCONV_DEV_BAD_SEQ);
 }
 
+struct Segment {
+    int seq, first, last, index, count;  // tokens [first, last) of sequence seq; segment `index` of `count`
+    int token0;                          // the sequence's first token on the t axis
+    bool ok;
+};
+
+// The segment at position u: sequence i has positions i * nseg .. in the batch form, and
+// starts[i] / seg + i .. in the packed form (which leaves room for every sequence's last,
+// partial segment).  A segment's position is its place in the workspace too.
+__device__ __forceinline__ Segment find_segment(const DeltaParams &p, const ScanPlan &plan, int u) {
+    Segment s;
+    int len;
+    if (p.starts == nullptr) {
+        s.seq = uniform(u / plan.nseg);
+        s.index = u - s.seq * plan.nseg;
+        s.token0 = 0;
+        len = p.t;
+    } else {
+        int lo = 0, hi = p.n;  // the last i with starts[i] / seg + i <= u
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (uniform(load_uniform(p.starts, mid) / plan.seg) + mid <= u)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s.seq = lo;
+        const int a = load_uniform(p.starts, lo), e = load_uniform(p.starts, lo + 1);
+        len = (a >= 0 && a <= e && e <= p.t) ? e - a : -1;
+        s.token0 = len >= 0 ? a : 0;
+        s.index = u - uniform(s.token0 / plan.seg) - lo;
+    }
+    s.count = len > 0 ? uniform((len - 1) / plan.seg) + 1 : 1;
+    s.ok = len >= 0 && s.index >= 0 && s.index < s.count;
+    s.first = s.ok ? s.index * plan.seg : 0;
+    s.last = s.ok ? s.first + min(len - s.first, plan.seg) : 0;
+    return s;
+}
+
+// A place of the workspace: for each head a segment's [p, k] and [k, k] floats.
+__device__ __forceinline__ int64_t place_floats(const DeltaParams &p) { return (int64_t)p.h * (p.p + p.k) * p.k; }
+
 // Sizes of a variant and its places in LDS (in bytes).  KS: keys' size, rounded up; C: tokens
 // of a chunk; NT: tiles of 16 state rows a wave owns; PARTS: see above.
 template <int KS, int C, int NT, int PARTS>
@@ -283,11 +334,14 @@ struct Sizes {
     static_assert(kBytes <= 160 * 1024, "more LDS than a CU has");
 };
 
-template <int KS, int C, int NT, int PARTS, bool WIDE>
-__global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaParams p, const ScanPlan plan) {
+// OUT: the outputs and final states.  Otherwise what a segment (any but a sequence's last) does
+// to a state: S' = S M + B, with B from no state and M, row by row, from the unit rows and no v.
+template <int KS, int C, int NT, int PARTS, bool OUT, bool WIDE>
+__global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaParams p, const ScanPlan plan,
+                                                                   const ScanGrid grid) {
     using Z = Sizes<KS, C, NT, PARTS>;
     constexpr int kB = Z::kBlocks, VP = Z::kRowsP, TP = Z::kTPitch, PP = Z::kPPitch, kSteps = KS / 32;
-    constexpr int kTParts = Z::kTParts;
+    constexpr int kTParts = Z::kTParts, kSParts = PARTS == 1 ? 1 : 2;
     extern __shared__ u32x4 smem[];
     char *lds = reinterpret_cast<char *>(smem);
     uint16_t *sk = reinterpret_cast<uint16_t *>(lds + Z::kKey), *sq = reinterpret_cast<uint16_t *>(lds + Z::kQuery);
@@ -297,38 +351,39 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = uniform(tid >> 6);
-    if (blockIdx.x == 0 && blockIdx.y == 0) check_table(p);
+    if (OUT && blockIdx.x == 0 && blockIdx.y == 0) check_table(p);
 
     // ---- this block's sequence, head and rows.  Blocks are dealt to the eight XCDs in turn:
     // a group's blocks, which read the same q and k, go to one of them.
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     int64_t ug;
     int member;
-    if (plan.runs) {
-        const int64_t turn = (block >> 3) / plan.each;
+    if (grid.runs) {
+        const int64_t turn = (block >> 3) / grid.each;
         ug = turn * 8 + (block & 7);
-        member = uniform((int)((block >> 3) - turn * plan.each));
+        member = uniform((int)((block >> 3) - turn * grid.each));
     } else {
-        ug = block / plan.each;
-        member = uniform((int)(block - ug * plan.each));
+        ug = block / grid.each;
+        member = uniform((int)(block - ug * grid.each));
     }
-    if (ug >= (int64_t)p.n * p.g) return;
-    const int seq = uniform((int)(ug / p.g)), group = uniform((int)(ug - (int64_t)seq * p.g));
-    const int which = uniform(member / plan.tiles);
-    const int head = group * uniform(p.h / p.g) + which, p0 = (member - which * plan.tiles) * Z::kRowsP;
-    int first = 0, len = p.t;
-    if (p.starts != nullptr) {
-        const int a = load_uniform(p.starts, seq), e = load_uniform(p.starts, seq + 1);
-        if (a < 0 || a > e || e > p.t) return;
-        first = a;
-        len = e - a;
-    }
-    const int rows = min(Z::kRowsP, p.p - p0);  // of this block
+    if (ug >= (int64_t)plan.slots * p.g) return;
+    const int place = uniform((int)(ug / p.g)), group = uniform((int)(ug - (int64_t)place * p.g));
+    const Segment segment = find_segment(p, plan, place);
+    if (!segment.ok || (!OUT && segment.index == segment.count - 1)) return;
+    const int seq = segment.seq, which = uniform(member / grid.tiles), tile = member - which * grid.tiles;
+    const int head = group * uniform(p.h / p.g) + which;
+    const int first = segment.token0 + segment.first, len = segment.last - segment.first;
+    // M's rows behind B's, in tiles of their own
+    const int own_tiles = OUT ? grid.tiles : (p.p + Z::kRowsP - 1) / Z::kRowsP;
+    const bool units = !OUT && tile >= own_tiles;
+    const int p0 = (units ? tile - own_tiles : tile) * Z::kRowsP;
+    const int rows = min(Z::kRowsP, (units ? p.k : p.p) - p0);  // of this block
     const int slot = uniform(route_row(p.idx, p.status, p.n, p.s, seq, lane));
     uint16_t *out = p.out + seq * p.os_n + (int64_t)first * p.os_t + head * p.os_h + p0;
     if (slot < 0) {  // a padding sequence: zeros, and no state moves
-        for (int t = wave; t < len; t += 2 * kHalf)
-            for (int c = lane; c < rows; c += kWave) out[t * p.os_t + c] = 0;
+        if (OUT)
+            for (int t = wave; t < len; t += 2 * kHalf)
+                for (int c = lane; c < rows; c += kWave) out[t * p.os_t + c] = 0;
         return;
     }
     const int chunks = (len + C - 1) / C;
@@ -364,7 +419,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             keys.load(sk + j % 3 * C * KS, (int64_t)j * C, len - j * C, pw, lane);
             queries.load(sq + j % 3 * C * KS, (int64_t)j * C, len - j * C, pw, lane);
         };
-        auto fetch_v = [&](int j) { values.load(sv, (int64_t)j * C, len - j * C, pw, lane); };
+        auto fetch_v = [&](int j) { values.load(sv, (int64_t)j * C, units ? 0 : len - j * C, pw, lane); };
         // ---- decays and weights of a chunk's tokens, a lane each (as they are in memory:
         // converting them here would wait for them)
         const float rate = p.a[head] * kLog2e, bias = p.dt_bias != nullptr ? p.dt_bias[head] : 0.0f;
@@ -693,7 +748,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             block_sync();
             if (more) fetch_v(j + 1);
             if (more && pw == 0) invert();
-            form_p_shared(j);
+            if constexpr (OUT) form_p_shared(j);
             wait_for_tiles();
             block_sync();
             if (more) {
@@ -748,31 +803,51 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
     for (int m = 0; m < KS / 16; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) hs[m][n] = f32x4_t{0, 0, 0, 0};
-    // body(its tile, its columns' state, byte offset in the head's state, values there of four)
-    constexpr bool kF32 = PARTS > 1;  // the state in memory, where there is one
-    const bool wide_state = p.k % 4 == 0 && p.ss_s % 4 == 0 && reinterpret_cast<uintptr_t>(p.state) % 16 == 0;
-    const auto head_state = [&]() {
+    // Where the state is from and where it goes: the pool's slot, or the workspace's place.
+    // body(a tile's four values, their byte offset in the head's state, how many there are)
+    constexpr bool kF32 = PARTS > 1;  // the pool's type, where there is a pool
+    const bool wide_pool = p.k % 4 == 0 && p.ss_s % 4 == 0 && reinterpret_cast<uintptr_t>(p.state) % 16 == 0;
+    const bool wide_place = p.k % 4 == 0;
+    const auto in_pool = [&]() {
         const int64_t pk = (int64_t)p.p * p.k;
         return make_buffer(static_cast<const char *>(p.state) + (kF32 ? 4 : 2) * (slot * p.ss_s + head * pk),
                            (uint32_t)((kF32 ? 4 : 2) * pk));
     };
-    const auto each_state4 = [&](auto &&body) {
+    const auto in_place = [&]() {
+        const int64_t head_floats = (int64_t)(p.p + p.k) * p.k;
+        return make_buffer(p.workspace + place * place_floats(p) + head * head_floats, (uint32_t)(4 * head_floats));
+    };
+    const auto each_state4 = [&](uint32_t bytes, auto &&body) {
         const int rr = here(r), gg = here(g);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint32_t row = (uint32_t)(p0 + mine + own(n, rr)) * (uint32_t)p.k;
+            const uint32_t row = (uint32_t)((units ? p.p : 0) + p0 + mine + own(n, rr)) * (uint32_t)p.k;
             const int most = own(n, rr) < left_rows ? p.k : 0;
 #pragma unroll
             for (int m = 0; m < KS / 16; ++m)
-                body(hs[m][n], (kF32 ? 4u : 2u) * (row + (uint32_t)column(m, gg)), most - column(m, gg));
+                body(hs[m][n], bytes * (row + (uint32_t)column(m, gg)), most - column(m, gg));
         }
     };
-    if (p.state != nullptr && p.has_init != nullptr && p.has_init[seq] != 0) {
-        const Buffer buf = head_state();
-        if (wide_state)
-            each_state4([&](f32x4_t &v, uint32_t at, int count) { v = load_state4<kF32, true>(buf, at, count); });
+    if (!OUT) {
+        if (units)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < KS / 16; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) hs[m][n][i] = column(m, g) + i == p0 + mine + own(n, r) ? 1.0f : 0.0f;
+    } else if (segment.count > 1) {
+        const Buffer buf = in_place();
+        if (wide_place)
+            each_state4(4, [&](f32x4_t &v, uint32_t at, int count) { v = load_state4<true, true>(buf, at, count); });
         else
-            each_state4([&](f32x4_t &v, uint32_t at, int count) { v = load_state4<kF32, false>(buf, at, count); });
+            each_state4(4, [&](f32x4_t &v, uint32_t at, int count) { v = load_state4<true, false>(buf, at, count); });
+    } else if (p.state != nullptr && p.has_init != nullptr && p.has_init[seq] != 0) {
+        const Buffer buf = in_pool();
+        if (wide_pool)
+            each_state4(kF32 ? 4 : 2, [&](f32x4_t &v, uint32_t at, int count) { v = load_state4<kF32, true>(buf, at, count); });
+        else
+            each_state4(kF32 ? 4 : 2, [&](f32x4_t &v, uint32_t at, int count) { v = load_state4<kF32, false>(buf, at, count); });
     }
 
     if (chunks > 0)
@@ -790,14 +865,14 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                 for (int n = 0; n < NT; ++n) d[tt][n] = f32x4_t{0, 0, 0, 0};
             // Rows of k, read ahead of their products; the next 32 columns of the state are split meanwhile.
-            u32x4 f[2][kB], hp[2][NT][PARTS];
+            u32x4 f[2][kB], hp[2][NT][kSParts];
             auto read_rows = [&](int m) {
 #pragma unroll
                 for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(km + 16 * tt * KS + row_at(m));
             };
             auto split_state = [&](int m) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) split<PARTS>(hs[2 * m][n], hs[2 * m + 1][n], hp[m & 1][n]);
+                for (int n = 0; n < NT; ++n) split<kSParts>(hs[2 * m][n], hs[2 * m + 1][n], hp[m & 1][n]);
             };
             read_rows(0);
             split_state(0);
@@ -806,7 +881,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                 if (m + 1 < kSteps) read_rows(m + 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int part = PARTS - 1; part >= 0; --part)
+                for (int part = kSParts - 1; part >= 0; --part)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -815,13 +890,13 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                     split_state(m + 1);
                     // a product, and what the vector units do meanwhile
 #pragma unroll
-                    for (int i = 0; i < PARTS * NT * kB; ++i) {
+                    for (int i = 0; i < kSParts * NT * kB; ++i) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, PARTS == 1 ? 2 : 4, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, PARTS == 1 ? 2 : 3, 0);
                     }
                 }
             }
-            {
+            if constexpr (OUT) {
             // ---- o = S q (columns t, rows p)
 #pragma unroll
             for (int tt = 0; tt < kB; ++tt)
@@ -977,16 +1052,18 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                 for (int m = 0; m < kB / 2; ++m) kt[t % 3][m] = load_columns(km + 32 * m * KS + column_at(t), KS);
             };
+            if constexpr (OUT)
 #pragma unroll
-            for (int tt = 0; tt < kB; ++tt) {
-                e[tt] = tok[kForQ * C + 16 * tt + r];
+                for (int tt = 0; tt < kB; ++tt) {
+                    e[tt] = tok[kForQ * C + 16 * tt + r];
 #pragma unroll
-                for (int m = 0; m <= tt / 2; ++m) pf[tt][m] = lds16(sp + (16 * tt + r) * PP + 32 * m + 8 * g);
-            }
+                    for (int m = 0; m <= tt / 2; ++m) pf[tt][m] = lds16(sp + (16 * tt + r) * PP + 32 * m + 8 * g);
+                }
             const float dec = __builtin_amdgcn_exp2f(tok[kSumHigh * C + C - 1] + tok[kSumLow * C + C - 1]);
             read_keys(0);
             read_keys(1);
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (OUT) {
 #pragma unroll
             for (int tt = 0; tt < kB; ++tt)
 #pragma unroll
@@ -999,6 +1076,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                     for (int tt = 2 * m; tt < kB; ++tt)
 #pragma unroll
                         for (int n = 0; n < NT; ++n) o[tt][n] = mfma(up[m][n][part], pf[tt][m], o[tt][n]);
+            }
 #pragma unroll
             for (int t = 0; t < KS / 16; ++t) {
                 if (t + 2 < KS / 16) read_keys(t + 2);
@@ -1029,18 +1107,115 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                             for (int i = 0; i < 4; ++i) hs[t][n][i] = __builtin_nanf("");
                 }
             }
-            put_out(o, j);
+            if constexpr (OUT) put_out(o, j);
         }
         block_sync();
     }
 
-    // ---- the state behind the sequence
-    if (p.state == nullptr) return;
-    const Buffer buf = head_state();
-    if (wide_state)
-        each_state4([&](f32x4_t &v, uint32_t at, int count) { store_state4<kF32, true>(buf, at, count, v); });
+    // ---- the state behind the segment
+    if (!OUT) {
+        const Buffer buf = in_place();
+        if (wide_place)
+            each_state4(4, [&](f32x4_t &v, uint32_t at, int count) { store_state4<true, true>(buf, at, count, v); });
+        else
+            each_state4(4, [&](f32x4_t &v, uint32_t at, int count) { store_state4<true, false>(buf, at, count, v); });
+        return;
+    }
+    if (p.state == nullptr || segment.index != segment.count - 1) return;
+    const Buffer buf = in_pool();
+    if (wide_pool)
+        each_state4(kF32 ? 4 : 2, [&](f32x4_t &v, uint32_t at, int count) { store_state4<kF32, true>(buf, at, count, v); });
     else
-        each_state4([&](f32x4_t &v, uint32_t at, int count) { store_state4<kF32, false>(buf, at, count, v); });
+        each_state4(kF32 ? 4 : 2, [&](f32x4_t &v, uint32_t at, int count) { store_state4<kF32, false>(buf, at, count, v); });
+}
+
+// The states ahead of every segment: S_0 the sequence's initial state, S_(i+1) = S_i M_i + B_i, in
+// FP32.  A block has 16 rows p of a head and its waves share out the columns, two tiles each; S_i,
+// which every wave needs whole, passes through LDS, and takes B_i's place in the workspace.
+template <int KS>
+__global__ __launch_bounds__(KS / 32 * kWave) void delta_join_kernel(const DeltaParams p, const ScanPlan plan, int ptiles) {
+    constexpr int kTiles = KS / 16, kMine = 2, kPitch = KS + 4;
+    __shared__ float ss[2][16 * kPitch];
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = uniform(threadIdx.x >> 6);
+    for_each_unit((int64_t)p.n * p.h * ptiles, [&](int64_t unit) {
+        const int64_t nh = unit / ptiles;
+        const int seq = uniform((int)(nh / p.h)), head = uniform((int)(nh - (int64_t)seq * p.h));
+        const int p0 = uniform((int)(unit - nh * ptiles)) * 16;
+        int token0 = 0, len = p.t;
+        if (p.starts != nullptr) {
+            token0 = load_uniform(p.starts, seq);
+            const int end = load_uniform(p.starts, seq + 1);
+            if (token0 < 0 || token0 > end || end > p.t) return;
+            len = end - token0;
+        }
+        if (len <= plan.seg) return;  // one segment
+        const int count = uniform((len - 1) / plan.seg) + 1;
+        const int place0 = p.starts != nullptr ? uniform(token0 / plan.seg) + seq : seq * plan.nseg;
+        const int slot = uniform(route_row(p.idx, p.status, p.n, p.s, seq, lane));
+        if (slot < 0) return;
+        const bool init = p.state != nullptr && p.has_init != nullptr && p.has_init[seq] != 0;
+        const int64_t head_floats = (int64_t)(p.p + p.k) * p.k;
+        const bool mine = p0 + r < p.p;
+        // tile t of this wave: columns k' = 16 (wave kMine + t) + 4 g + i of row p0 + r
+        f32x4_t now[kMine];
+#pragma unroll
+        for (int t = 0; t < kMine; ++t) {
+            const int c = 16 * (wave * kMine + t) + 4 * g;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                now[t][i] = init && mine && c + i < p.k
+                                ? load_either(p.state, p.state_f32, slot * p.ss_s + ((int64_t)head * p.p + p0 + r) * p.k + c + i)
+                                : 0.0f;
+        }
+        for (int j = 0; j < count; ++j) {
+            const Buffer buf = make_buffer(p.workspace + (place0 + j) * place_floats(p) + head * head_floats,
+                                           (uint32_t)(4 * head_floats));
+            float *mat = ss[j & 1];
+            // this wave's columns of M (row k = 16 m + 4 g + i, column r of the tile), and of B
+            float mm[kMine][kTiles][4];
+            f32x4_t next[kMine];
+            const bool last = j == count - 1;
+#pragma unroll
+            for (int t = 0; t < kMine; ++t) {
+                const int c = 16 * (wave * kMine + t);
+                const int count4 = mine && !last ? p.k - c - 4 * g : 0;
+                const uint32_t at = 4u * ((uint32_t)(p0 + r) * (uint32_t)p.k + (uint32_t)(c + 4 * g));
+                next[t] = p.k % 4 == 0 ? load_state4<true, true>(buf, at, count4) : load_state4<true, false>(buf, at, count4);
+#pragma unroll
+                for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = 16 * m + 4 * g + i;
+                        const uint32_t from = !last && row < p.k && c + r < p.k
+                                                  ? 4u * ((uint32_t)(p.p + row) * (uint32_t)p.k + (uint32_t)(c + r)) : kNowhere;
+                        mm[t][m][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buf, from, 0, kCached));
+                    }
+                *reinterpret_cast<f32x4_t *>(mat + r * kPitch + c + 4 * g) = now[t];
+            }
+            __syncthreads();
+            // (every wave has read its share of B, whose place S takes)
+#pragma unroll
+            for (int t = 0; t < kMine; ++t) {
+                const int c = 16 * (wave * kMine + t);
+                const int count4 = mine ? p.k - c - 4 * g : 0;
+                const uint32_t at = 4u * ((uint32_t)(p0 + r) * (uint32_t)p.k + (uint32_t)(c + 4 * g));
+                if (p.k % 4 == 0)
+                    store_state4<true, true>(buf, at, count4, now[t]);
+                else
+                    store_state4<true, false>(buf, at, count4, now[t]);
+            }
+            if (last) break;
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m) {
+                const f32x4_t s = lds4f(mat + r * kPitch + 16 * m + 4 * g);
+#pragma unroll
+                for (int t = 0; t < kMine; ++t) next[t] = mfma_f32(f32x4_t{mm[t][m][0], mm[t][m][1], mm[t][m][2], mm[t][m][3]}, s, next[t]);
+            }
+#pragma unroll
+            for (int t = 0; t < kMine; ++t) now[t] = next[t];
+        }
+        __syncthreads();  // the next unit reuses the LDS arrays
+    });
 }
 
 // Lets a kernel use a CU's whole LDS; once for each device, whose bit of *done is
@@ -1056,32 +1231,43 @@ hipError_t allow_lds(const void *kernel, uint64_t *done) {
     return set;
 }
 
-template <int KS, int C, int NT, int PARTS, bool WIDE>
+template <int KS, int C, int NT, int PARTS, bool OUT, bool WIDE>
 uint64_t lds_allowed = 0;
 
-template <int KS, int C, int NT, int PARTS, bool WIDE>
-hipError_t launch(const DeltaParams &p, hipStream_t stream) {
+template <int KS, int C, int NT, int PARTS, bool OUT, bool WIDE>
+hipError_t launch(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream) {
     using Z = Sizes<KS, C, NT, PARTS>;
-    ScanPlan plan;
-    plan.tiles = (p.p + Z::kRowsP - 1) / Z::kRowsP;
-    plan.each = p.h / p.g * plan.tiles;
-    const int64_t groups = (int64_t)p.n * p.g;
-    plan.runs = groups >= 32;
-    const int64_t units = (plan.runs ? (groups + 7) / 8 * 8 : groups) * plan.each;
-    auto kernel = delta_scan_kernel<KS, C, NT, PARTS, WIDE>;
-    const hipError_t allowed = allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, C, NT, PARTS, WIDE>);
+    const auto tiles = [](int64_t rows) { return (rows + Z::kRowsP - 1) / Z::kRowsP; };
+    ScanGrid grid;
+    grid.tiles = (int32_t)(tiles(p.p) + (OUT ? 0 : tiles(p.k)));
+    grid.each = p.h / p.g * grid.tiles;
+    const int64_t groups = (int64_t)plan.slots * p.g;
+    grid.runs = groups >= 32;
+    const int64_t units = (grid.runs ? (groups + 7) / 8 * 8 : groups) * grid.each;
+    auto kernel = delta_scan_kernel<KS, C, NT, PARTS, OUT, WIDE>;
+    const hipError_t allowed =
+        allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, C, NT, PARTS, OUT, WIDE>);
     if (allowed != hipSuccess) return allowed;
     const int64_t across = units < kMaxBlocks ? units : kMaxBlocks, deep = (units + across - 1) / across;
     if (deep > 65535) return hipErrorInvalidConfiguration;
-    kernel<<<dim3((unsigned)across, (unsigned)deep), kScanBlock, Z::kBytes, stream>>>(p, plan);
+    kernel<<<dim3((unsigned)across, (unsigned)deep), kScanBlock, Z::kBytes, stream>>>(p, plan, grid);
     return hipGetLastError();
 }
 
-template <int KS, int C, int NT>
-hipError_t launch_parts(const DeltaParams &p, bool wide, hipStream_t stream) {
-    if (p.state != nullptr && p.state_f32)
-        return wide ? launch<KS, C, NT, 3, true>(p, stream) : launch<KS, C, NT, 3, false>(p, stream);
-    return wide ? launch<KS, C, NT, 1, true>(p, stream) : launch<KS, C, NT, 1, false>(p, stream);
+template <int KS, int C, int NT, bool WIDE>
+hipError_t launch_passes(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream) {
+    if (plan.split) {
+        // (all 24 bits of M and B, whatever the state's type: their errors meet those of the state)
+        hipError_t err = launch<KS, C, NT, 3, false, WIDE>(p, plan, stream);
+        if (err != hipSuccess) return err;
+        const int ptiles = (p.p + 15) / 16;
+        const int64_t units = (int64_t)p.n * p.h * ptiles;
+        delta_join_kernel<KS><<<dim3((unsigned)(units < kMaxBlocks ? units : kMaxBlocks)), KS / 32 * kWave, 0, stream>>>(p, plan, ptiles);
+        err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return p.state != nullptr && p.state_f32 ? launch<KS, C, NT, 3, true, WIDE>(p, plan, stream)
+                                             : launch<KS, C, NT, 1, true, WIDE>(p, plan, stream);
 }
 
 // Whether rows at p with the given element strides start on 16 bytes, and a chunk's rows
@@ -1090,19 +1276,64 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0 && b < (1 << 23);
 }
 
-constexpr int64_t kEnoughBlocks = 256;
+// How a call is cut up, by a model of its time: rounds of a block a CU, in which a chunk takes
+// kChunkNs.  Blocks have 64 or 128 rows of a head's state.  Where there are fewer blocks than CUs,
+// cutting sequences into segments may save time: it takes a pass that makes M and B, with blocks
+// for M's rows too and kStatesNs a chunk, a join of kJoinNs a segment, and two launches, kCutNs.
+constexpr int64_t kCus = 256;
+constexpr int64_t kChunkNs[2] = {3900, 4500}, kStatesNs[2] = {3400, 3900}, kJoinNs = 1500, kCutNs = 12000;
+
+ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t k, bool packed) {
+    const int64_t c = k <= 128 ? 64 : 32;  // tokens of a chunk
+    const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    // (packed: of more than two sequences, the longest is taken for twice the mean)
+    const int64_t whole = up(t, c) > 0 ? up(t, c) : 1, longest = packed && n > 2 ? up(2 * t, n * c) : up(t, c);
+    const int64_t all = up(packed ? t : n * t, c);  // chunks in all
+    ScanPlan plan;
+    int64_t seg = whole, best = -1;
+    for (int two = 0; two < (k <= 128 && p > 64 ? 2 : 1); ++two) {
+        const int64_t tiles = up(p, two ? 128 : 64), key_tiles = up(k, two ? 128 : 64), rounds = up(n * h * tiles, kCus);
+        const int64_t uncut = rounds * longest * kChunkNs[two];
+        if (best < 0 || uncut < best) best = uncut, seg = whole, plan.two = two != 0;
+        for (int64_t s = 2; rounds == 1 && s <= 64 && 4 * s <= longest; ++s) {
+            const int64_t chunks = up(longest, s), pieces = up(all, chunks);
+            const int64_t time = kCutNs + s * kJoinNs + chunks * (up(pieces * h * (tiles + key_tiles), kCus) * kStatesNs[two] +
+                                                                  up(pieces * h * tiles, kCus) * kChunkNs[two]);
+            if (time < best) best = time, seg = chunks, plan.two = two != 0;
+        }
+    }
+    if (seg > whole) seg = whole;
+    plan.seg = (int32_t)(seg * c);
+    plan.nseg = (int32_t)up(whole, seg);
+    plan.split = plan.nseg > 1;
+    plan.slots = (int32_t)(packed ? t / (seg * c) + n : n * plan.nseg);
+    return plan;
+}
 
 }  // namespace
 
+int64_t delta_scan_workspace_floats(int64_t n, int64_t t, int64_t h, int64_t p, int64_t k, bool packed) {
+    const ScanPlan plan = make_plan(n, t, h, p, k, packed);
+    return plan.split ? plan.slots * (h * (p + k) * k) : 0;
+}
+
 hipError_t launch_delta_scan(const DeltaParams &p, hipStream_t stream, const char **kernel_name) {
+    const ScanPlan plan = make_plan(p.n, p.t, p.h, p.p, p.k, p.starts != nullptr);
     const bool wide = p.p % 8 == 0 && p.k % 8 == 0 && rows16(p.q, p.qs_n, p.qs_t, p.qs_g) &&
                       rows16(p.key, p.ks_n, p.ks_t, p.ks_g) && rows16(p.v, p.vs_n, p.vs_t, p.vs_h) &&
                       rows16(p.out, p.os_n, p.os_t, p.os_h);
-    *kernel_name = wide ? "delta_scan" : "delta_scan_scalar";
-    const bool two = (int64_t)p.n * p.h * ((p.p + 127) / 128) >= kEnoughBlocks && p.p > 64;
-    if (p.k <= 64) return two ? launch_parts<64, 64, 2>(p, wide, stream) : launch_parts<64, 64, 1>(p, wide, stream);
-    if (p.k <= 128) return two ? launch_parts<128, 64, 2>(p, wide, stream) : launch_parts<128, 64, 1>(p, wide, stream);
-    return launch_parts<256, 32, 1>(p, wide, stream);
+    *kernel_name = plan.split ? (wide ? "delta_scan_split" : "delta_scan_split_scalar")
+                              : (wide ? "delta_scan" : "delta_scan_scalar");
+    const bool two = plan.two;
+    if (p.k <= 64) {
+        if (two) return wide ? launch_passes<64, 64, 2, true>(p, plan, stream) : launch_passes<64, 64, 2, false>(p, plan, stream);
+        return wide ? launch_passes<64, 64, 1, true>(p, plan, stream) : launch_passes<64, 64, 1, false>(p, plan, stream);
+    }
+    if (p.k <= 128) {
+        if (two) return wide ? launch_passes<128, 64, 2, true>(p, plan, stream) : launch_passes<128, 64, 2, false>(p, plan, stream);
+        return wide ? launch_passes<128, 64, 1, true>(p, plan, stream) : launch_passes<128, 64, 1, false>(p, plan, stream);
+    }
+    return wide ? launch_passes<256, 32, 1, true>(p, plan, stream) : launch_passes<256, 32, 1, false>(p, plan, stream);
 }
 
 }  // namespace dcconv

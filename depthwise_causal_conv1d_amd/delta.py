@@ -25,7 +25,8 @@ from . import _binding as _b
 from . import selective as _s
 
 __all__ = [
-    "dcconv_gated_delta_update", "dcconv_gated_delta_scan", "dcconv_gated_rms_norm", "dcconv_add_rms_norm",
+    "dcconv_gated_delta_update", "dcconv_gated_delta_scan", "dcconv_gated_delta_scan_workspace",
+    "dcconv_gated_rms_norm", "dcconv_add_rms_norm",
     "gated_delta_scan", "gated_delta_update", "gated_rms_norm", "add_rms_norm",
 ]
 
@@ -50,7 +51,9 @@ def declare(lib: ctypes.CDLL) -> None:
         + [vp, i32, i64, i64, i32]                    # beta, beta_dtype, es_n, es_t, beta_sigmoid
         + [i32, f32, f32, vp]                         # qk_l2norm, l2norm_eps, scale, seq_starts
         + [vp, i32, i64, i64, vp, vp]                 # state, state_dtype, s, ss_s, state_indices, has_initial_state
-        + [vp, i64, i64, i64, vp, vp])                # out, os_n, os_t, os_h, dev_status, stream
+        + [vp, i64, i64, i64, vp, i64, vp, vp])       # out, os_n, os_t, os_h, workspace, bytes, dev_status, stream
+    lib.dcconv_gated_delta_scan_workspace.restype = i64
+    lib.dcconv_gated_delta_scan_workspace.argtypes = [i64] * 6 + [i32]
     lib.dcconv_gated_rms_norm.restype = i32
     lib.dcconv_gated_rms_norm.argtypes = (
         [vp] + [i64] * 7                              # x, n, t, h, d, xs_n, xs_t, xs_h
@@ -77,6 +80,11 @@ def dcconv_gated_delta_update(*args) -> int:
 def dcconv_gated_delta_scan(*args) -> int:
     """The whole-sequence C entry point, one to one (pointers as ints)."""
     return _b.load().dcconv_gated_delta_scan(*args)
+
+
+def dcconv_gated_delta_scan_workspace(n, t, h, p, g, k, packed) -> int:
+    """Bytes of workspace a scan of these sizes needs, one to one."""
+    return _b.load().dcconv_gated_delta_scan_workspace(n, t, h, p, g, k, packed)
 
 
 def dcconv_gated_rms_norm(*args) -> int:
@@ -160,7 +168,7 @@ def gated_delta_update(q, k, v, dt, A, beta, state, *, dt_bias=None, dt_softplus
 
 def gated_delta_scan(q, k, v, dt, A, beta, *, dt_bias=None, dt_softplus=False, beta_sigmoid=False, qk_l2norm=False,
                      l2norm_eps=1e-6, scale=None, state=None, state_indices=None, has_initial_state=None,
-                     seq_starts=None, return_final_state=False, out=None, dev_status=None):
+                     seq_starts=None, return_final_state=False, workspace=None, out=None, dev_status=None):
     """The recurrence over whole sequences; returns the output [N, T, H, P].
 
     q, k: bf16 [N, T, G, K]; v: bf16 [N, T, H, P]; dt, beta: bf16 or float32 [N, T, H]; A,
@@ -170,7 +178,8 @@ def gated_delta_scan(q, k, v, dt, A, beta, *, dt_bias=None, dt_softplus=False, b
     [n]) marks start from their slot's state, and every sequence leaves its final state there;
     ``state_indices`` (int32 [n]) routes sequences to slots, -1 being padding.
     return_final_state: without ``state``, returns ``(out, state)`` with a new float32
-    [n, H, P, K] state.  The rest as for ``gated_delta_update``."""
+    [n, H, P, K] state.  ``workspace``: a uint8 buffer of ``dcconv_gated_delta_scan_workspace``
+    bytes (allocated here if None).  The rest as for ``gated_delta_update``."""
     lib = _s._lib()
     if v.dim() != 4 or k.dim() != 4:
         raise ValueError(f"v must be [N, T, H, P] and k [N, T, G, K], got {tuple(v.shape)} and {tuple(k.shape)}")
@@ -209,6 +218,11 @@ def gated_delta_scan(q, k, v, dt, A, beta, *, dt_bias=None, dt_softplus=False, b
         out, os_ = _s._t.empty(rows, dtype=_s._BF16, device=v.device), (T * H * P, H * P, P)
     else:
         os_ = _s._bf16("out", out, rows, dev)
+    need = lib.dcconv_gated_delta_scan_workspace(n, T, H, P, G, K, int(starts is not None))
+    if workspace is None:
+        workspace = _s._t.empty(need, dtype=_s._t.uint8, device=v.device) if need else None
+    elif workspace.dtype is not _s._t.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be a contiguous uint8 tensor on v's device")
     with _b.on(dev):
         rc = lib.dcconv_gated_delta_scan(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), n, T, H, P, G, K, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2],
@@ -216,7 +230,8 @@ def gated_delta_scan(q, k, v, dt, A, beta, *, dt_bias=None, dt_softplus=False, b
             int(bool(dt_softplus)), _s._vector("A", A, _s._F32, H, dev), beta_at, beta_code, es[0], es[1],
             int(bool(beta_sigmoid)), int(bool(qk_l2norm)), l2norm_eps, K ** -0.5 if scale is None else scale, starts,
             pool, code, S, slot, _s._vector("state_indices", state_indices, _s._I32, n, dev), init, out.data_ptr(),
-            os_[0], os_[1], os_[2], _s._status(dev_status, dev), _b.stream(dev))
+            os_[0], os_[1], os_[2], None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), _s._status(dev_status, dev), _b.stream(dev))
     _b.raise_for(rc)
     return (out, final) if final is not None else out
 

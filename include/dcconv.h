@@ -426,6 +426,8 @@ int dcconv_gated_delta_update(const void *q, const void *key, const void *v, int
  *             i starts from its slot's state where has_initial_state[i] (uint8 [n],
  *             NULL: nowhere) is nonzero, from zero elsewhere, and leaves its final
  *             state there.  An empty sequence leaves its initial state or zeros.
+ * workspace   dcconv_gated_delta_scan_workspace() bytes, 16-byte aligned; its contents
+ *             need not be kept and are not read from one call to the next.
  * Returns as dcconv_gated_delta_update.
  */
 int dcconv_gated_delta_scan(const void *q, const void *key, const void *v, int64_t n, int64_t t, int64_t h, int64_t p,
@@ -437,7 +439,13 @@ int dcconv_gated_delta_scan(const void *q, const void *key, const void *v, int64
                             int qk_l2norm, float l2norm_eps, float scale, const int32_t *seq_starts,
                             void *state, int state_dtype, int64_t s, int64_t ss_s, const int32_t *state_indices,
                             const uint8_t *has_initial_state,
-                            void *out, int64_t os_n, int64_t os_t, int64_t os_h, int32_t *dev_status, void *stream);
+                            void *out, int64_t os_n, int64_t os_t, int64_t os_h,
+                            void *workspace, int64_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Bytes of workspace that dcconv_gated_delta_scan needs for these sizes (0: none, the pointer
+ * may be NULL).  `packed` is nonzero with seq_starts. */
+int64_t dcconv_gated_delta_scan_workspace(int64_t n, int64_t t, int64_t h, int64_t p, int64_t g, int64_t k,
+                                          int packed);
 
 /* ---------------------------------------------------------------------------
  * Norms of the layer: behind the recurrence, and between blocks.  All arithmetic is
