@@ -139,6 +139,11 @@ __device__ __forceinline__ void split(f32x4_t a, f32x4_t b, u32x4 (&part)[N]) {
         }
 }
 
+// acc + 0 times each of a word's two BF16 values: a NaN where one is not finite.
+__device__ __forceinline__ float add_zeros(uint32_t w, float acc) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w), __builtin_bit_cast(bf16x2_t, 0u), acc, false);
+}
+
 // The sum over the first lanes up to this one, in 64 bits.
 template <int CTRL>
 __device__ __forceinline__ double dpp_shift(double v) {
@@ -289,6 +294,21 @@ __device__ __forceinline__ Segment find_segment(const DeltaParams &p, const Scan
         s.index = u - s.seq * plan.nseg;
         s.token0 = 0;
         len = p.t;
+    } else if (!plan.split && p.n <= kWave) {
+        // whole sequences, the longest first: those that come last are short ones
+        const int lane = threadIdx.x & 63, i = min(lane, p.n - 1);
+        const int a = p.starts[i], e = p.starts[i + 1];
+        const int mine = lane < p.n ? (a >= 0 && a <= e && e <= p.t ? e - a : -1) : -2;
+        int longer = 0;  // sequences ahead of this lane's
+        for (int q = 0; q < p.n; ++q) {
+            const int other = __builtin_amdgcn_readlane(mine, q);
+            longer += other > mine || (other == mine && q < lane);
+        }
+        const uint64_t found = __ballot(lane < p.n && longer == u);  // (none at a position past the last)
+        s.seq = found != 0 ? uniform(__builtin_ctzll(found)) : 0;
+        len = found != 0 ? __builtin_amdgcn_readlane(mine, s.seq) : -1;
+        s.token0 = len >= 0 ? __builtin_amdgcn_readlane(a, s.seq) : 0;
+        s.index = 0;
     } else {
         int lo = 0, hi = p.n;  // the last i with starts[i] / seg + i <= u
         while (hi - lo > 1) {
@@ -395,17 +415,17 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         *reinterpret_cast<u32x2 *>(to + 8 * piece + 4) = u32x2{0, 0};
     }
 
-    // Where a lane reads its share of k (of q: kQuery - kKey further): row r's inner indices
-    // 32 m + 8 g .. of the state's columns, and, with tokens as the inner index, columns 16 t ..
+    // Where a lane reads its share of k or q: row r's inner indices 32 m + 8 g .. of the state's
+    // columns, and, with tokens as the inner index, columns 16 t ..
     constexpr int kAcross = KS / 8;
-    int by_row_at[kSteps < 4 ? kSteps : 4], by_column_at[kSteps < 4 ? kSteps : 4];
-#pragma unroll
-    for (int m = 0; m < kSteps && m < 4; ++m) {
-        by_row_at[m] = r * KS + 8 * ((4 * m + g) ^ swap_of<kAcross>(r));
-        by_column_at[m] = (4 * g + (r >> 2)) * KS + 8 * ((4 * m + (r & 3)) ^ swap_of<kAcross>(4 * g + (r >> 2)));
-    }
-    const auto row_at = [&](int m) { return by_row_at[m & 3] + 128 * (m >> 2); };
-    const auto column_at = [&](int t) { return by_column_at[t >> 1 & 3] + 128 * (t >> 3) + 4 * (t & 1); };
+    const auto row_place = [](int m, int r, int g) {
+        return r * KS + 8 * ((4 * (m & 3) + g) ^ swap_of<kAcross>(r)) + 128 * (m >> 2);
+    };
+    const auto column_place = [](int t, int r, int g) {
+        const int row = 4 * g + (r >> 2);
+        return row * KS + 8 * ((4 * (t >> 1 & 3) + (r & 3)) ^ swap_of<kAcross>(row)) + 128 * (t >> 3) + 4 * (t & 1);
+    };
+    const auto row_at = [&](int m) { return row_place(m, r, g); };
 
     if (wave >= kHalf) {
         // ================================================== the waves that prepare T and P
@@ -856,7 +876,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         const uint16_t *km = sk + j % 3 * C * KS, *qm = sq + j % 3 * C * KS;
         const float *tok = tokens + j % 3 * kTokenRows * C;
         f32x4_t d[kB][NT], o[kB][NT];
-        u32x4 rp[NT][PARTS];
+        u32x4 rp[NT][kTParts];
         // ---- d = S k (columns p, rows t), then R
         {
             const int lane_here = here(lane), r = lane_here & 15, g = lane_here >> 4;
@@ -868,7 +888,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             u32x4 f[2][kB], hp[2][NT][kSParts];
             auto read_rows = [&](int m) {
 #pragma unroll
-                for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(km + 16 * tt * KS + row_at(m));
+                for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(km + 16 * tt * KS + row_place(m, r, g));
             };
             auto split_state = [&](int m) {
 #pragma unroll
@@ -905,7 +925,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             u32x4 f[2][kB];
             auto read_rows = [&](int m) {
 #pragma unroll
-                for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(qm + 16 * tt * KS + row_at(m));
+                for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(qm + 16 * tt * KS + row_place(m, r, g));
             };
             read_rows(0);
 #pragma unroll
@@ -934,7 +954,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                         d[2 * m][n][i] = ((i & 1) ? hi_f32(v[i >> 1]) : lo_f32(v[i >> 1])) - w0[i] * d[2 * m][n][i];
                         d[2 * m + 1][n][i] = ((i & 1) ? hi_f32(v[2 + (i >> 1)]) : lo_f32(v[2 + (i >> 1)])) - w1[i] * d[2 * m + 1][n][i];
                     }
-                    if (m == 0) split<PARTS>(d[0][n], d[1][n], rp[n]);
+                    if (m == 0) split<kTParts>(d[0][n], d[1][n], rp[n]);
                 }
             }
         }
@@ -959,7 +979,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                     for (int a = kTParts - 1; a >= 0; --a)
 #pragma unroll
-                        for (int b = PARTS - 1; b >= 0; --b)
+                        for (int b = kTParts - 1; b >= 0; --b)
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
                                 if (a + b < kTParts) {
@@ -969,7 +989,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         if (bad && cut[n] < 32) d0[n] = d1[n] = f32x4_t{0, 0, 0, 0};
-                        split<PARTS>(d0[n], d1[n], rp[n]);
+                        split<kTParts>(d0[n], d1[n], rp[n]);
                     }
                 }
                 u32x4 tf[2][kTParts];
@@ -984,7 +1004,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                     for (int a = kTParts - 1; a >= 0; --a)
 #pragma unroll
-                        for (int b = PARTS - 1; b >= 0; --b)
+                        for (int b = kTParts - 1; b >= 0; --b)
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
                                 if (a + b < kTParts) {
@@ -993,11 +1013,13 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                                 }
                 };
                 correct();
+#pragma unroll
+                for (int n = 0; n < NT; ++n) split<kTParts>(d0[n], d1[n], up[m][n]);
                 float probe[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) probe[i] = __builtin_fmaf(d1[n][i], 0.0f, __builtin_fmaf(d0[n][i], 0.0f, probe[i]));
+                    for (int i = 0; i < 4; ++i) probe[i] = add_zeros(up[m][n][0][i], probe[i]);
                 if (__any((probe[0] + probe[1]) + (probe[2] + probe[3]) != 0.0f)) {
                     // zeros for R from the first token on where it is not finite, U anew, and the same for U
                     bad = true;
@@ -1014,7 +1036,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                         for (int i = 0; i < 8; ++i)
                             if (16 * (i >> 2) + 4 * g + (i & 3) >= at)
 #pragma unroll
-                                for (int part = 0; part < PARTS; ++part)
+                                for (int part = 0; part < kTParts; ++part)
                                     rp[n][part][i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
                         if (at < 32) cut[n] = min(cut[n], 32 * m + at);
                     }
@@ -1033,13 +1055,11 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                             if (32 * m + 4 * g + i >= cut[n]) d0[n][i] = 0.0f;
                             if (32 * m + 16 + 4 * g + i >= cut[n]) d1[n][i] = 0.0f;
                         }
+                        split<kTParts>(d0[n], d1[n], up[m][n]);
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    split<kTParts>(d0[n], d1[n], up[m][n]);
-                    split<PARTS>(d0[n] * w0, d1[n] * w1, wp[m][n]);
-                }
+                for (int n = 0; n < NT; ++n) split<PARTS>(d0[n] * w0, d1[n] * w1, wp[m][n]);
             }
         }
         block_sync();
@@ -1050,7 +1070,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             float e[kB];
             auto read_keys = [&](int t) {
 #pragma unroll
-                for (int m = 0; m < kB / 2; ++m) kt[t % 3][m] = load_columns(km + 32 * m * KS + column_at(t), KS);
+                for (int m = 0; m < kB / 2; ++m) kt[t % 3][m] = load_columns(km + 32 * m * KS + column_place(t, r, g), KS);
             };
             if constexpr (OUT)
 #pragma unroll
