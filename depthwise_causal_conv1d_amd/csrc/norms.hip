@@ -15,6 +15,7 @@ namespace dcconv {
 namespace {
 
 constexpr int kNormBlock = 256;
+constexpr bool kOnceLoads = true, kOnceStores = true;
 
 // Sums over the LANES threads that share a row, in all of them.  `part`: four floats of LDS
 // that no sum since the last barrier has used (LANES = 256 alone).
@@ -55,12 +56,26 @@ __device__ __forceinline__ float inverse_rms(const float (&v)[NV][8], int d, flo
     return scale * rsqrtf(__builtin_fmaf(sum, inv, eps * scale * scale));
 }
 
+// Sixteen bytes; ONCE: of an operand that nobody reads again soon.
+template <bool ONCE>
+__device__ __forceinline__ u32x4 load16(const void *at) {
+    const u32x4 *p = static_cast<const u32x4 *>(at);
+    return ONCE && kOnceLoads ? __builtin_nontemporal_load(p) : *p;
+}
+__device__ __forceinline__ void store16(void *at, u32x4 v) {
+    u32x4 *p = static_cast<u32x4 *>(at);
+    if (kOnceStores)
+        __builtin_nontemporal_store(v, p);
+    else
+        *p = v;
+}
+
 // Eight values from element `at` of a BF16 array, of which `count` exist (the rest: zeros).
-template <bool WIDE>
+template <bool WIDE, bool ONCE = true>
 __device__ __forceinline__ void load8(const uint16_t *base, int64_t at, int count, float (&v)[8]) {
     if (WIDE) {
         u32x4 w = {0, 0, 0, 0};
-        if (count > 0) w = *reinterpret_cast<const u32x4 *>(base + at);
+        if (count > 0) w = load16<ONCE>(base + at);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (i & 1) ? hi_f32(w[i >> 1]) : lo_f32(w[i >> 1]);
         return;
@@ -68,13 +83,13 @@ __device__ __forceinline__ void load8(const uint16_t *base, int64_t at, int coun
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < count ? bf16_bits_to_f32(base[at + i]) : 0.0f;
 }
-template <bool WIDE>
+template <bool WIDE, bool ONCE = true>
 __device__ __forceinline__ void load8(const float *base, int64_t at, int count, float (&v)[8]) {
     if (WIDE) {
         u32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
         if (count > 0) {
-            a = *reinterpret_cast<const u32x4 *>(base + at);
-            b = *reinterpret_cast<const u32x4 *>(base + at + 4);
+            a = load16<ONCE>(base + at);
+            b = load16<ONCE>(base + at + 4);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]), v[4 + i] = __uint_as_float(b[i]);
@@ -83,19 +98,19 @@ __device__ __forceinline__ void load8(const float *base, int64_t at, int count, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < count ? base[at + i] : 0.0f;
 }
-template <bool WIDE>
+template <bool WIDE, bool ONCE>
 __device__ __forceinline__ void load8(const void *base, bool f32, int64_t at, int count, float (&v)[8]) {
     if (f32)
-        load8<WIDE>(static_cast<const float *>(base), at, count, v);
+        load8<WIDE, ONCE>(static_cast<const float *>(base), at, count, v);
     else
-        load8<WIDE>(static_cast<const uint16_t *>(base), at, count, v);
+        load8<WIDE, ONCE>(static_cast<const uint16_t *>(base), at, count, v);
 }
 template <bool WIDE>
 __device__ __forceinline__ void store8(uint16_t *base, int64_t at, int count, const float (&v)[8]) {
     if (WIDE) {
         if (count > 0)
-            *reinterpret_cast<u32x4 *>(base + at) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+            store16(base + at, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                     pack_bf16x2(v[6], v[7])});
         return;
     }
 #pragma unroll
@@ -106,10 +121,8 @@ template <bool WIDE>
 __device__ __forceinline__ void store8(float *base, int64_t at, int count, const float (&v)[8]) {
     if (WIDE) {
         if (count > 0) {
-            *reinterpret_cast<u32x4 *>(base + at) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                                          __float_as_uint(v[2]), __float_as_uint(v[3])};
-            *reinterpret_cast<u32x4 *>(base + at + 4) = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                                              __float_as_uint(v[6]), __float_as_uint(v[7])};
+            store16(base + at, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+            store16(base + at + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
         }
         return;
     }
@@ -156,7 +169,7 @@ __global__ __launch_bounds__(kNormBlock) void gated_norm_kernel(const GatedNormP
         for (int i = 0; i < NV; ++i) {
             const int c = 8 * (i * LANES + sub);
             float w[8];
-            if (p.weight != nullptr) load8<WIDE>(p.weight, p.weight_f32, h * p.ws_h + c, p.d - c, w);
+            if (p.weight != nullptr) load8<WIDE, false>(p.weight, p.weight_f32, h * p.ws_h + c, p.d - c, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 x[i][j] = x[i][j] * f * (p.weight != nullptr ? w[j] + p.offset : 1.0f) * gate[i][j];
@@ -182,7 +195,7 @@ __global__ __launch_bounds__(kNormBlock) void add_norm_kernel(const AddNormParam
         for (int i = 0; i < NV; ++i) {
             const int c = 8 * (i * LANES + sub);
             load8<WIDE>(p.x, xa + c, p.d - c, y[i]);
-            load8<WIDE>(p.residual, F32, ra + c, p.d - c, r[i]);
+            load8<WIDE, true>(p.residual, F32, ra + c, p.d - c, r[i]);
             if (p.gate != nullptr) load8<WIDE>(p.gate, ga + c, p.d - c, gate[i]);
         }
         if (p.post != nullptr) {
@@ -191,7 +204,7 @@ __global__ __launch_bounds__(kNormBlock) void add_norm_kernel(const AddNormParam
             for (int i = 0; i < NV; ++i) {
                 const int c = 8 * (i * LANES + sub);
                 float w[8];
-                load8<WIDE>(p.post, p.weight_f32, c, p.d - c, w);
+                load8<WIDE, false>(p.post, p.weight_f32, c, p.d - c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[i][j] = y[i][j] * f * (w[j] + p.offset);
             }
@@ -215,7 +228,7 @@ __global__ __launch_bounds__(kNormBlock) void add_norm_kernel(const AddNormParam
         for (int i = 0; i < NV; ++i) {
             const int c = 8 * (i * LANES + sub);
             float w[8];
-            load8<WIDE>(p.weight, p.weight_f32, c, p.d - c, w);
+            load8<WIDE, false>(p.weight, p.weight_f32, c, p.d - c, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) r[i][j] = r[i][j] * f * (w[j] + p.offset);
             store8<WIDE>(p.out, oa + c, p.d - c, r[i]);

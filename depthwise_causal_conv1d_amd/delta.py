@@ -100,6 +100,11 @@ def dcconv_add_rms_norm(*args) -> int:
 # ------------------------------------------------------------ tensor front end
 
 
+def _like(t):
+    """A new contiguous tensor of t's shape and type (the shorter of torch's ways: 0.5 to 1 us a call)."""
+    return _s._t.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _per_head(name, t, shape, dev):
     """(address, dtype code, strides) of dt or beta."""
     code = _s._dtype(name, t)
@@ -151,7 +156,7 @@ def gated_delta_update(q, k, v, dt, A, beta, state, *, dt_bias=None, dt_softplus
     if A is None:
         raise ValueError("A must be given")
     if out is None:
-        out, os_ = _s._t.empty(rows, dtype=_s._BF16, device=v.device), (H * P, P)
+        out, os_ = _like(v), (H * P, P)
     else:
         os_ = _s._bf16("out", out, rows, dev)
     with _b.on(dev):
@@ -215,7 +220,7 @@ def gated_delta_scan(q, k, v, dt, A, beta, *, dt_bias=None, dt_softplus=False, b
         code, S, slot = _pool(state, H, P, K, dev)
         pool = state.data_ptr()
     if out is None:
-        out, os_ = _s._t.empty(rows, dtype=_s._BF16, device=v.device), (T * H * P, H * P, P)
+        out, os_ = _like(v), (T * H * P, H * P, P)
     else:
         os_ = _s._bf16("out", out, rows, dev)
     need = lib.dcconv_gated_delta_scan_workspace(n, T, H, P, G, K, int(starts is not None))
@@ -269,7 +274,7 @@ def gated_rms_norm(x, z, weight, *, eps=1e-6, gate_first=False, weight_offset=0.
         weight_at, code = _weight("weight", weight, ((D,), per_row), dev)
         pitch = D if weight.dim() > 1 else 0
     if out is None:
-        out = _s._t.empty(shape, dtype=_s._BF16, device=x.device)
+        out = _like(x)
         os_ = out.stride()
     else:
         os_ = _s._bf16("out", out, shape, dev)
@@ -315,7 +320,7 @@ def add_rms_norm(x, residual, weight, *, post_weight=None, gate=None, residual_s
         if post_code != code:
             raise ValueError(f"post_weight must be {weight.dtype} as weight, got {post_weight.dtype}")
     if out is None:
-        out = _s._t.empty(shape, dtype=_s._BF16, device=x.device)
+        out = _like(x)
         os_ = out.stride()
     else:
         os_ = _s._bf16("out", out, shape, dev)
