@@ -1299,9 +1299,12 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
 // How a call is cut up, by a model of its time: rounds of a block a CU, in which a chunk takes
 // kChunkNs.  Blocks have 64 or 128 rows of a head's state.  Where there are fewer blocks than CUs,
 // cutting sequences into segments may save time: it takes a pass that makes M and B, with blocks
-// for M's rows too and kStatesNs a chunk, a join of kJoinNs a segment, and two launches, kCutNs.
+// for M's rows too and kStatesNs a chunk, a join of kJoinNs a segment, and two more launches, each
+// with the latency of a block's first and last accesses, kCutNs.  (128 x 128, F32 states, cut into 5, 8
+// and 16 segments: 16381 tokens of 16 heads 530, 362 and 327 us, where the whole takes 1014; into 4
+// and 8, 4096 tokens of 32 heads 193 and 179; 1000 tokens of 32 heads into 4: 81, whole 72.)
 constexpr int64_t kCus = 256;
-constexpr int64_t kChunkNs[2] = {3900, 4500}, kStatesNs[2] = {3400, 3900}, kJoinNs = 1500, kCutNs = 12000;
+constexpr int64_t kChunkNs[2] = {4200, 5000}, kStatesNs[2] = {4000, 4700}, kJoinNs = 2200, kCutNs = 40000;
 
 ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t k, bool packed) {
     const int64_t c = k <= 128 ? 64 : 32;  // tokens of a chunk
