@@ -1157,10 +1157,13 @@ __global__ __launch_bounds__(KS / 32 * kWave) void delta_join_kernel(const Delta
     constexpr int kTiles = KS / 16, kMine = 2, kPitch = KS + 4;
     __shared__ float ss[2][16 * kPitch];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = uniform(threadIdx.x >> 6);
-    for_each_unit((int64_t)p.n * p.h * ptiles, [&](int64_t unit) {
-        const int64_t nh = unit / ptiles;
+    // Blocks are dealt to the eight XCDs in turn: a head's, which read the same M, go to one of them.
+    const int64_t heads = (int64_t)p.n * p.h;
+    for_each_unit((heads + 7) / 8 * 8 * ptiles, [&](int64_t unit) {
+        const int64_t turn = (unit >> 3) / ptiles, nh = turn * 8 + (unit & 7);
+        if (nh >= heads) return;
         const int seq = uniform((int)(nh / p.h)), head = uniform((int)(nh - (int64_t)seq * p.h));
-        const int p0 = uniform((int)(unit - nh * ptiles)) * 16;
+        const int p0 = uniform((int)((unit >> 3) - turn * ptiles)) * 16;
         int token0 = 0, len = p.t;
         if (p.starts != nullptr) {
             token0 = load_uniform(p.starts, seq);
@@ -1190,49 +1193,50 @@ __global__ __launch_bounds__(KS / 32 * kWave) void delta_join_kernel(const Delta
         for (int j = 0; j < count; ++j) {
             const Buffer buf = make_buffer(p.workspace + (place0 + j) * place_floats(p) + head * head_floats,
                                            (uint32_t)(4 * head_floats));
-            float *mat = ss[j & 1];
-            // this wave's columns of M (row k = 16 m + 4 g + i, column r of the tile), and of B
-            float mm[kMine][kTiles][4];
+            const bool more = j < count - 1;
+            // this wave's columns of B and of M (row k = 16 m + 4 g + i, column r of the tile)
             f32x4_t next[kMine];
-            const bool last = j == count - 1;
+            float mm[kMine][kTiles][4];
+            uint32_t at[kMine];
+            int left[kMine];
 #pragma unroll
             for (int t = 0; t < kMine; ++t) {
                 const int c = 16 * (wave * kMine + t);
-                const int count4 = mine && !last ? p.k - c - 4 * g : 0;
-                const uint32_t at = 4u * ((uint32_t)(p0 + r) * (uint32_t)p.k + (uint32_t)(c + 4 * g));
-                next[t] = p.k % 4 == 0 ? load_state4<true, true>(buf, at, count4) : load_state4<true, false>(buf, at, count4);
+                at[t] = 4u * ((uint32_t)(p0 + r) * (uint32_t)p.k + (uint32_t)(c + 4 * g));
+                left[t] = mine ? p.k - c - 4 * g : 0;
+                next[t] = p.k % 4 == 0 ? load_state4<true, true>(buf, at[t], more ? left[t] : 0)
+                                       : load_state4<true, false>(buf, at[t], more ? left[t] : 0);
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int row = 16 * m + 4 * g + i;
-                        const uint32_t from = !last && row < p.k && c + r < p.k
+                        const uint32_t from = more && row < p.k && c + r < p.k
                                                   ? 4u * ((uint32_t)(p.p + row) * (uint32_t)p.k + (uint32_t)(c + r)) : kNowhere;
                         mm[t][m][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buf, from, 0, kCached));
                     }
-                *reinterpret_cast<f32x4_t *>(mat + r * kPitch + c + 4 * g) = now[t];
             }
-            __syncthreads();
-            // (every wave has read its share of B, whose place S takes)
+            float *mat = ss[j & 1];
 #pragma unroll
-            for (int t = 0; t < kMine; ++t) {
-                const int c = 16 * (wave * kMine + t);
-                const int count4 = mine ? p.k - c - 4 * g : 0;
-                const uint32_t at = 4u * ((uint32_t)(p0 + r) * (uint32_t)p.k + (uint32_t)(c + 4 * g));
-                if (p.k % 4 == 0)
-                    store_state4<true, true>(buf, at, count4, now[t]);
-                else
-                    store_state4<true, false>(buf, at, count4, now[t]);
-            }
-            if (last) break;
+            for (int t = 0; t < kMine; ++t)
+                *reinterpret_cast<f32x4_t *>(mat + r * kPitch + 16 * (wave * kMine + t) + 4 * g) = now[t];
+            __syncthreads();
 #pragma unroll
             for (int m = 0; m < kTiles; ++m) {
                 const f32x4_t s = lds4f(mat + r * kPitch + 16 * m + 4 * g);
 #pragma unroll
-                for (int t = 0; t < kMine; ++t) next[t] = mfma_f32(f32x4_t{mm[t][m][0], mm[t][m][1], mm[t][m][2], mm[t][m][3]}, s, next[t]);
+                for (int t = 0; t < kMine; ++t)
+                    next[t] = mfma_f32(f32x4_t{mm[t][m][0], mm[t][m][1], mm[t][m][2], mm[t][m][3]}, s, next[t]);
             }
+            // (in the place of B's columns, which this wave alone has read)
 #pragma unroll
-            for (int t = 0; t < kMine; ++t) now[t] = next[t];
+            for (int t = 0; t < kMine; ++t) {
+                if (p.k % 4 == 0)
+                    store_state4<true, true>(buf, at[t], left[t], now[t]);
+                else
+                    store_state4<true, false>(buf, at[t], left[t], now[t]);
+                now[t] = next[t];
+            }
         }
         __syncthreads();  // the next unit reuses the LDS arrays
     });
@@ -1281,7 +1285,7 @@ hipError_t launch_passes(const DeltaParams &p, const ScanPlan &plan, hipStream_t
         hipError_t err = launch<KS, C, NT, 3, false, WIDE>(p, plan, stream);
         if (err != hipSuccess) return err;
         const int ptiles = (p.p + 15) / 16;
-        const int64_t units = (int64_t)p.n * p.h * ptiles;
+        const int64_t units = ((int64_t)p.n * p.h + 7) / 8 * 8 * ptiles;
         delta_join_kernel<KS><<<dim3((unsigned)(units < kMaxBlocks ? units : kMaxBlocks)), KS / 32 * kWave, 0, stream>>>(p, plan, ptiles);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
