@@ -14,7 +14,10 @@
 //     out = scale (e^{c_t} S q_t + sum_{u <= t} e^{c_t - c_u} q_t.k_u U_u)
 //     S'  = e^{c_C} S + sum_u e^{c_C - c_u} U_u k_u^T
 //
-// T and P = e^{c_t - c_u} q_t.k_u do not depend on the state: a block's second four waves
+// (I + A)^-1 is taken 32 tokens at a time: U_0 = T_0 R_0 for the chunk's first half, and then
+// U_1 = T_1 (R_1 - A_10 U_0), so that T needs no products over the whole chunk.
+//
+// T, A_10 and P = e^{c_t - c_u} q_t.k_u do not depend on the state: a block's second four waves
 // prepare them for the next chunk while its first four, which hold the state, run the
 // chain S -> R -> U -> S'.
 //
@@ -25,10 +28,25 @@
 // matrix instructions (a series in A would need terms that grow like binomials where keys
 // repeat; substitution does not).
 //
-// Three barriers a chunk.  While the first four waves form R (1), U (2) and then the outputs
-// and S' (3) of chunk j, the second put chunk j + 1's q and k into LDS, request chunk j + 2's
-// and join T of chunk j (1); form A of chunk j + 1 and P of chunk j (2); and invert A's
-// diagonal blocks (3).
+// Three phases a chunk, a barrier behind each.  Chunk j:
+//
+//     waves with the state                      the other four
+//     1  S k, S q, R                            request q and k of j + 2; A of j + 1
+//     2  U                                      request v of j + 1; invert A of j + 1 (one wave)
+//                                               and form P of j (three); wait for the tiles
+//     3  outputs, S'                            T of j + 1; factors of j + 1; gates and key
+//                                               lengths of j + 2
+//
+// q, k and v go from memory to LDS without passing registers, q and k into one of three places
+// each, in pieces of 16 bytes whose order within a row differs from row to row so that the rows
+// and the transposing loads both find their banks free.  64-token chunks of 128-value keys take
+// 150 to 157 KiB of LDS: one block a CU.
+//
+// Few heads leave CUs idle.  Then sequences are cut into segments: what a segment does to a
+// state is S' = S M + B, with M and B from the same kernel (OUT = false), which takes the
+// identity's rows without v for M; a join passes over the segments' M and B, and the output pass
+// starts each segment from its state.  It is three times the work, and taken where a model of the
+// times says so (make_plan).  Packed sequences that are not cut are started longest first.
 //
 // Layouts.  v_mfma_f32_16x16x32_bf16 takes, in lane l with r = l & 15 and g = l >> 4, row
 // (column) r of an operand at inner indices 8 g .. 8 g + 7, and leaves column r, rows
@@ -41,17 +59,33 @@
 //
 // Precision.  q, k and v are BF16 as given: a key's length enters as an FP32 factor.  Sums,
 // states, A and its inverse are FP32, prefix sums 64 bits and their differences 48.  An
-// operand that is no BF16 value is split into PARTS BF16 values, whose products are added
-// up: with an F32 state, S, R, T and U are (PARTS = 3: all 24 bits); with a BF16 state S, R and
-// the U that enters the state are rounded, T has two parts.  P, and the copy of the state that q reads, are
-// rounded to BF16, and the U that P multiplies has two parts, in every case: what is left is about the
-// output's own rounding.
+// operand that is no BF16 value is split into parts, BF16 values whose products are added
+// up, the smallest first.  With an F32 state (PARTS = 3): R, T, A_10 and U in three parts (all
+// 24 bits), S for S k in two; the state is within 1e-6 of its size of 64 bits.  (Two parts of
+// everything: packed sequences 1.2 times as fast, 2.8e-6.)  With a BF16 state (PARTS = 1): R, T
+// and A_10 in two, S for S k and the U that enters the state in one, since the state is rounded to
+// BF16 again when it is stored; it is up to 0.0028 of its size off then (S in two parts: 0.0025, and
+// the case below 161 us beside 151; U too: 173).  A call without states runs as one with BF16
+// states.  In every case P, and the copy of the state that q reads, are one BF16 value, and the U
+// that P multiplies two: outputs are 0.0023 to 0.0028 of their size off where the rounding of an
+// exact result is 0.0017 off.
 //
 // What is not finite.  An infinity or NaN of a later token must not meet the zeros above T's
 // and P's diagonals.  A key, decay or weight that is not finite leaves A's entries out and
 // makes R's factor NaN from there on; a channel of R or U with a value that is not finite is
 // cut at its first such token: U is zero from there, and those outputs and the channel's
 // state become NaN.
+//
+// What bounds it, at 8 x 2048 tokens, 32 heads of 128 x 128 in 16 groups, BF16 states (one block a CU, 32
+// chunks): 148 to 161 us, 2.2 times its bytes' time.  A chunk takes about 10000 cycles, 3200, 3000
+// and 2900 of them in the three phases of the waves that prepare, and 2900, 2350 and 2650 in those of the
+// waves with the state: both kinds wait for their own chain of reads, products and conversions, with two
+// waves a SIMD to cover for each other (matrix units 27 % busy, vector instructions 45 % of the issue
+// slots).  What did not help there: 64 rows a block, twice the blocks (273 us, since T and P
+// are prepared twice); loads of q and k by the waves with the state (147 to 158); a higher priority for
+// the waves that prepare (161); reading all of A's columns ahead of the substitution (spills).
+// What did: chunks in two halves rather than T over all 64 tokens, tiles straight to LDS, and no
+// spilled register (238 us to 150).
 #include <type_traits>
 
 #include "delta_common.h"
@@ -1301,7 +1335,8 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
 }
 
 // How a call is cut up, by a model of its time: rounds of a block a CU, in which a chunk takes
-// kChunkNs.  Blocks have 64 or 128 rows of a head's state.  Where there are fewer blocks than CUs,
+// kChunkNs.  Blocks have 64 or 128 rows of a head's state (8 x 2048 tokens of 32 heads of 128: 273 us and 150;
+// few heads fill more CUs with 64).  Where there are fewer blocks than CUs,
 // cutting sequences into segments may save time: it takes a pass that makes M and B, with blocks
 // for M's rows too and kStatesNs a chunk, a join of kJoinNs a segment, and two more launches, each
 // with the latency of a block's first and last accesses, kCutNs.  (128 x 128, F32 states, cut into 5, 8
@@ -1311,7 +1346,7 @@ constexpr int64_t kCus = 256;
 constexpr int64_t kChunkNs[2] = {4200, 5000}, kStatesNs[2] = {4000, 4700}, kJoinNs = 2200, kCutNs = 40000;
 
 ScanPlan make_plan(int64_t n, int64_t t, int64_t h, int64_t p, int64_t k, bool packed) {
-    const int64_t c = k <= 128 ? 64 : 32;  // tokens of a chunk
+    const int64_t c = k <= 128 ? 64 : 32;  // tokens of a chunk (64 of longer keys would take 192 KiB of LDS for q and k)
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     // (packed: of more than two sequences, the longest is taken for twice the mean)
     const int64_t whole = up(t, c) > 0 ? up(t, c) : 1, longest = packed && n > 2 ? up(2 * t, n * c) : up(t, c);

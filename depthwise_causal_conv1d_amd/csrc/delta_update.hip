@@ -15,6 +15,10 @@
 // are four DPP steps each.  q, k (as F32, made to length one once for all of the block's
 // heads), v and the heads' factors pass through LDS.  All arithmetic is FP32; a BF16 state
 // is rounded when it is stored, after q has read the unrounded value.
+//
+// 256 rows, 32 heads of 128 x 128, F32 states: 176 us, 6.1 TB/s of state, where a large copy
+// reaches 5.9.  61 rows, 9 heads of 80 x 72, BF16 states: 8.5 us for 11 MB; rows of 144
+// bytes fill nine of sixteen lanes.  4 rows, 8 heads: 5.0 us, launch and one item's latency.
 #include "delta_common.h"
 #include "state_vec.h"
 

@@ -427,7 +427,20 @@ int dcconv_gated_delta_update(const void *q, const void *key, const void *v, int
  *             NULL: nowhere) is nonzero, from zero elsewhere, and leaves its final
  *             state there.  An empty sequence leaves its initial state or zeros.
  * workspace   dcconv_gated_delta_scan_workspace() bytes, 16-byte aligned; its contents
- *             need not be kept and are not read from one call to the next.
+ *             need not be kept and are not read from one call to the next.  Calls that
+ *             may run at the same time need one each.
+ * Precision.  Tokens are taken 32 or 64 at a time as matrix products with BF16 operands
+ * and FP32 sums.  An F32 state is kept as exactly as FP32 products keep it.  What is
+ * rounded to BF16 once on the way to out is the copy of the state that q reads, and the
+ * products of q and key under their decays; a BF16 state takes u (times its decay) as one
+ * BF16 value, too.  Outputs are 0.0023 to 0.0028 of their size off, where the rounding of
+ * an exact result is 0.0017 off.  A decay below 2^-65536 counts as that.
+ * What is not finite.  A NaN or infinity reaches what the recurrence lets it reach and
+ * nothing else: no earlier token, no other sequence, and for v no other channel.  An
+ * infinity may arrive as a NaN, and stays one.  The same holds where states or u pass FP32's
+ * range, or where positive dt * a let decays grow past 2^127 within 32 tokens.
+ * Results do not depend on the run.  They may differ in their last bits between forms of the
+ * same call: batched or packed, cut into segments or not (which the sizes decide).
  * Returns as dcconv_gated_delta_update.
  */
 int dcconv_gated_delta_scan(const void *q, const void *key, const void *v, int64_t n, int64_t t, int64_t h, int64_t p,
