@@ -438,7 +438,8 @@ int dcconv_gated_delta_update(const void *q, const void *key, const void *v, int
  * What is not finite.  A NaN or infinity reaches what the recurrence lets it reach and
  * nothing else: no earlier token, no other sequence, and for v no other channel.  An
  * infinity may arrive as a NaN, and stays one.  The same holds where states or u pass FP32's
- * range, or where positive dt * a let decays grow past 2^127 within 32 tokens.
+ * range, or the factors that several tokens together multiply a state by, exp(d * a) (1 - b key
+ * key^T), do (with positive d * a, say, or b above 2), also where they would meet a state of zeros.
  * Results do not depend on the run.  They may differ in their last bits between forms of the
  * same call: batched or packed, cut into segments or not (which the sizes decide).
  * Returns as dcconv_gated_delta_update.

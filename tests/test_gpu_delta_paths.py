@@ -45,6 +45,33 @@ def test_cut_packed_sequences():
     Case(43, [1800, 1500], 2, 64, 1, 64, packed=True, state=torch.float32, table=[-1, 0], init=[True, True]).check()
 
 
+@pytest.mark.parametrize("what", ["q", "k", "v", "beta", "dt"])
+def test_cut_sequences_not_finite(what):
+    """A NaN in the middle of a segment reaches what is behind it, and no earlier token, other head or
+    channel of v, through the segments' matrices either."""
+    t0 = 700
+    case = Case(45, [1601], 2, 32, 2, 64, state=torch.float32, init=[True], logit=False, soft=False, f32=True)
+    clean = case.call()
+    assert dc.dcconv_last_kernel().startswith("delta_scan_split")
+    clean_pool = case.pool
+    at = {"q": (0, t0, 1, 5), "k": (0, t0, 1, 5), "v": (0, t0, 1, 7), "beta": (0, t0, 1), "dt": (0, t0, 1)}[what]
+    getattr(case, what)[at] = float("nan")
+    out, pool = case.call(), case.pool
+    fine = torch.isfinite(out)
+    assert torch.equal(out[0, :, 0], clean[0, :, 0]) and torch.equal(out[0, :t0], clean[0, :t0])
+    assert torch.equal(pool[0, 0], clean_pool[0, 0])
+    if what == "q":
+        assert not fine[0, t0, 1].any() and torch.equal(out[0, t0 + 1:], clean[0, t0 + 1:])
+        assert torch.equal(pool, clean_pool)
+        return
+    if what == "v":
+        others = [p for p in range(32) if p != 7]
+        assert not fine[0, t0:, 1, 7].any() and torch.equal(out[..., others], clean[..., others])
+        assert not torch.isfinite(pool[0, 1, 7]).any() and torch.equal(pool[:, :, others], clean_pool[:, :, others])
+        return
+    assert not fine[0, t0:, 1].any() and not torch.isfinite(pool[0, 1]).any()
+
+
 def test_cut_sequences_do_not_read_the_workspace_before_they_write_it():
     case = Case(44, [1601], 2, 64, 1, 64, state=torch.float32, init=[True])
     need = dc.dcconv_gated_delta_scan_workspace(1, 1601, 2, 64, 1, 64, 0)
