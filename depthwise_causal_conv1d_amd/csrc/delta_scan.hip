@@ -71,8 +71,11 @@
 // exact result is 0.0017 off.
 //
 // What is not finite.  An infinity or NaN of a later token must not meet the zeros above T's
-// and P's diagonals.  A key, decay or weight that is not finite leaves A's entries out and
-// makes R's factor NaN from there on; a channel of R or U with a value that is not finite is
+// and P's diagonals.  An entry of A that is not finite, from operands that are not or from finite
+// ones (decays that rise between two tokens, large weights and keys), makes its row of T so, and
+// with it U at that token: the substitution takes a row from those ahead of it alone; between a
+// half's two tiles the entry is left out of the product with T_11, and NaN put in its row of T; and
+// A_10 between halves enters R row by row.  A channel of R or U with a value that is not finite is
 // cut at its first such token: U is zero from there, and those outputs and the channel's
 // state become NaN.
 //
@@ -657,15 +660,12 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[i] = self[i] * (tw[i] * tu[i]) * uu * Log{tl.high[i], tl.low[i]}.to(ul);
-                if (!(r < 4 * g + i && is_finite(v[i]))) v[i] = 0.0f;
+                if (!(r < 4 * g + i)) v[i] = 0.0f;
             }
             *reinterpret_cast<f32x4_t *>(tile) = v;
             if (kSide) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[i] = a0[i] * (sw[i] * su[i]) * vu * Log{sl.high[i], sl.low[i]}.to(vl);
-                    if (!is_finite(v[i])) v[i] = 0.0f;
-                }
+                for (int i = 0; i < 4; ++i) v[i] = a0[i] * (sw[i] * su[i]) * vu * Log{sl.high[i], sl.low[i]}.to(vl);
                 *reinterpret_cast<f32x4_t *>(sa + (3 * (S >> 1) + 2) * 16 * kAPitch + r * kAPitch + 4 * g) = v;
             }
             if (kOff) {  // decays by way of the second half's start
@@ -677,8 +677,6 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     v0[i] = a0[i] * fx * fu[i], v1[i] = a1[i] * fy * fu[i];
-                    if (!is_finite(v0[i])) v0[i] = 0.0f;
-                    if (!is_finite(v1[i])) v1[i] = 0.0f;
                 }
                 to_parts(v0, off[0]);
                 to_parts(v1, off[1]);
@@ -744,7 +742,20 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                 a = lds4f(half + (2 * 16 + r) * kAPitch + 4 * g), t = lds4f(half + r * kAPitch + 4 * g);
                 w1 = lds4f(weight + 16);
                 const f32x4_t zero = {0, 0, 0, 0};
-                const f32x4_t x = mfma_f32(t, mfma_f32(a, y, zero), zero) * w0;
+                // a row of A_10 that is not finite: left out of the product, where it would meet T_11's
+                // zeros in the rows ahead, and NaN in T
+                bool lost = false;
+                if (__any(!is_finite((a[0] + a[1]) + (a[2] + a[3])))) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const bool bad = !is_finite(a[s]);
+                        const uint64_t rows = __ballot(bad);  // that of row 4 q + s: in the lanes g = q
+                        if (bad) a[s] = 0.0f;
+                        if ((r & 3) == s) lost = (rows >> (16 * (r >> 2)) & 0xffff) != 0;
+                    }
+                }
+                f32x4_t x = mfma_f32(t, mfma_f32(a, y, zero), zero) * w0;
+                if (lost) x[0] = __builtin_nanf("");
                 y *= w1;
                 float v0[4] = {-x[0], -x[1], -x[2], -x[3]}, v1[4] = {y[0], y[1], y[2], y[3]};
                 put_parts(v1, to + 4, C * TP);

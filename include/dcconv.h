@@ -434,12 +434,15 @@ int dcconv_gated_delta_update(const void *q, const void *key, const void *v, int
  * rounded to BF16 once on the way to out is the copy of the state that q reads, and the
  * products of q and key under their decays; a BF16 state takes u (times its decay) as one
  * BF16 value, too.  Outputs are 0.0023 to 0.0028 of their size off, where the rounding of
- * an exact result is 0.0017 off.  A decay below 2^-65536 counts as that.
+ * an exact result is 0.0017 off.  Decays below 2^-126, a token's or several tokens' together, count
+ * as zero.
  * What is not finite.  A NaN or infinity reaches what the recurrence lets it reach and
  * nothing else: no earlier token, no other sequence, and for v no other channel.  An
- * infinity may arrive as a NaN, and stays one.  The same holds where states or u pass FP32's
- * range, or the factors that several tokens together multiply a state by, exp(d * a) (1 - b key
- * key^T), do (with positive d * a, say, or b above 2), also where they would meet a state of zeros.
+ * infinity may arrive as a NaN, and stays one.  The same holds where the factors that a token or
+ * several together multiply a state by, exp(d * a) (1 - b key key^T), pass FP32's range (with positive
+ * d * a, say, or b above 2), also where they would meet a state of zeros or others take the growth
+ * back.  Where states or u pass that range by themselves, a result that is finite all the same is as
+ * right as any other.
  * Results do not depend on the run.  They may differ in their last bits between forms of the
  * same call: batched or packed, cut into segments or not (which the sizes decide).
  * Returns as dcconv_gated_delta_update.
