@@ -438,11 +438,10 @@ int dcconv_gated_delta_update(const void *q, const void *key, const void *v, int
  * as zero.
  * What is not finite.  A NaN or infinity reaches what the recurrence lets it reach and
  * nothing else: no earlier token, no other sequence, and for v no other channel.  An
- * infinity may arrive as a NaN, and stays one.  The same holds where the factors that a token or
+ * infinity may arrive as a NaN, and stays one.  Where states, u, or the factors that a token or
  * several together multiply a state by, exp(d * a) (1 - b key key^T), pass FP32's range (with positive
- * d * a, say, or b above 2), also where they would meet a state of zeros or others take the growth
- * back.  Where states or u pass that range by themselves, a result that is finite all the same is as
- * right as any other.
+ * d * a, say, or b above 2), also where those would meet a state of zeros or later tokens take the
+ * growth back, what follows is not finite either, or finite and as right as any other result.
  * Results do not depend on the run.  They may differ in their last bits between forms of the
  * same call: batched or packed, cut into segments or not (which the sizes decide).
  * Returns as dcconv_gated_delta_update.
