@@ -218,6 +218,8 @@ def gated_delta_scan(q, k, v, dt, A, beta, *, dt_bias=None, dt_softplus=False, b
     code, S, slot, pool = _s.DCCONV_DTYPE_F32, 0, 0, None
     if state is not None:
         code, S, slot = _pool(state, H, P, K, dev)
+        if S == 0 and n > 0:  # (its address is NULL, which would mean no state)
+            raise ValueError(f"state has no slots for {n} sequences")
         pool = state.data_ptr()
     if out is None:
         out, os_ = _like(v), (T * H * P, H * P, P)
