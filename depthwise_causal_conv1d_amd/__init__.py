@@ -379,6 +379,8 @@ def causal_conv1d(x, weight, bias=None, activation=None, *, conv_state=None, con
         state_out = conv_state
     if conv_state is not None and (conv_state.dim() != 3 or conv_state.shape[1] != D):
         raise ValueError(f"conv_state must be [S, D, L] with D={D}, got {tuple(conv_state.shape)}")
+    if conv_state is not None and conv_state.shape[0] == 0 and n > 0:  # (its address is NULL, which would mean no state)
+        raise ValueError(f"conv_state has no slots for {n} sequences")
     if out is None:
         out = torch.empty(B, T, D, dtype=torch.bfloat16, device=dev).permute(0, 2, 1)
     elif out.shape != (B, D, T) or out.dtype != torch.bfloat16 or out.device != dev:

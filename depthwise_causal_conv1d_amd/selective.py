@@ -365,6 +365,8 @@ def selective_scan(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus=
         if ssm_state.dim() != 4:
             raise ValueError(f"ssm_state must be [S, H, P, K], got shape {tuple(ssm_state.shape)}")
         code, S, slot = _pool(ssm_state, H, P, K, dev)
+        if S == 0 and n > 0:  # (its address is NULL, which would mean no state)
+            raise ValueError(f"ssm_state has no slots for {n} sequences")
         pool = ssm_state.data_ptr()
     if out is None:
         out, os_ = _t.empty(rows, dtype=_BF16, device=x.device), (T * H * P, H * P, P)
