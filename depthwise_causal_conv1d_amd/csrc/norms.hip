@@ -38,9 +38,10 @@ __device__ __forceinline__ float sum_lanes(float v, float *part) {
 
 // 1 / sqrt(mean of the row's squares + eps).  A sum of squares that leaves FP32's range is
 // formed again from values scaled by a power of two; under 2^-80 only where eps is not far
-// above the mean anyway.  part: eight floats of LDS.
+// above the mean anyway.  Then the values are below 2^-40, and v is left scaled by 2^100, the result
+// being for the scaled values: their own may be up to 2^149.  part: eight floats of LDS.
 template <int LANES, int NV>
-__device__ __forceinline__ float inverse_rms(const float (&v)[NV][8], int d, float eps, float *part) {
+__device__ __forceinline__ float inverse_rms(float (&v)[NV][8], int d, float eps, float *part) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -50,14 +51,19 @@ __device__ __forceinline__ float inverse_rms(const float (&v)[NV][8], int d, flo
     const float inv = 1.0f / (float)d;
     const bool large = !(sum < 0x1p+126f), small = sum < 0x1p-80f && eps < 0x1p-100f;
     if (!large && !small) return rsqrtf(__builtin_fmaf(sum, inv, eps));
-    const float scale = large ? 0x1p-80f : 0x1p+64f;
+    const float scale = large ? 0x1p-80f : 0x1p+100f;
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += (v[i][j] * scale) * (v[i][j] * scale);
+        for (int j = 0; j < 8; ++j) {
+            const float scaled = v[i][j] * scale;
+            sum = __builtin_fmaf(scaled, scaled, sum);
+            if (small) v[i][j] = scaled;
+        }
     sum = sum_lanes<LANES>(sum, part + 4);
-    return scale * rsqrtf(__builtin_fmaf(sum, inv, eps * scale * scale));
+    const float f = rsqrtf(__builtin_fmaf(sum, inv, eps * scale * scale));
+    return small ? f : scale * f;
 }
 
 // Sixteen bytes; ONCE: of an operand that nobody reads again soon, as streaming accesses, which leave

@@ -469,7 +469,8 @@ int64_t dcconv_gated_delta_scan_workspace(int64_t n, int64_t t, int64_t h, int64
  * same) is BF16 or F32; weight_offset is added to every weight (1 for weights that
  * are kept as their difference from one).  rms(v) = sqrt(mean of v^2 + eps) over the
  * d values of a row; the squares of all finite values are served, also where their
- * sum is not finite or zero in FP32.  1 <= d <= 16384.  x, z, gate and out are BF16 with
+ * sum is not finite or zero in FP32 (what is normed is an FP32 value each, a sum or a
+ * product x SiLU(z) too).  A row of zeros with eps 0 gives NaN.  1 <= d <= 16384.  x, z, gate and out are BF16 with
  * d unit-stride values of a row and other strides >= 0, in elements.  Nothing that a
  * call writes may lie within the range another operand spans.
  * ------------------------------------------------------------------------ */
