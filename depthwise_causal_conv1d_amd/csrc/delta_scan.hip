@@ -204,16 +204,24 @@ __device__ __forceinline__ double prefix_sum(double v, int lane) {
     return v + (lane >= 48 ? r0 + r1 + r2 : lane >= 32 ? r0 + r1 : lane >= 16 ? r0 : 0.0);
 }
 
-// log(1 + e^v) and 1 / (1 + e^-v) with the hardware's exponential, logarithm and reciprocal,
-// each within about 2^-21 of itself: a series where the logarithm's argument is near one.
+// log(1 + e^v) and 1 / (1 + e^-v) with the hardware's exponential, logarithm and reciprocal, each within
+// 2^-21 of itself (down to 2^-126): by way of t = e^-|v|, whose exponent's rounding is made good, and with what
+// 1 + t loses of t put back behind the logarithm; a series where t is small.
+__device__ __forceinline__ float exp_minus_abs(float v) {
+    const float a = __builtin_fabsf(v) > 128.0f ? 128.0f : __builtin_fabsf(v);  // (a NaN stays one)
+    const float h = -a * kLog2e, low = __builtin_fmaf(-a, kLog2e, -h) - a * 1.9259629911266175e-8f;  // log2 e - kLog2e
+    const float t = __builtin_amdgcn_exp2f(h);
+    return __builtin_fmaf(t, low * 0.6931471805599453f, t);
+}
 __device__ __forceinline__ float softplus_near(float v) {
-    const float t = __builtin_amdgcn_exp2f(-__builtin_fabsf(v) * kLog2e);
+    const float t = exp_minus_abs(v), w = 1.0f + t;
     const float series = t * (1.0f + t * (-0.5f + t * (1.0f / 3.0f + t * (-0.25f + t * 0.2f))));
-    const float far = __builtin_amdgcn_logf(1.0f + t) * 0.6931471805599453f;
+    const float far = __builtin_fmaf(__builtin_amdgcn_logf(w), 0.6931471805599453f, (t - (w - 1.0f)) * __builtin_amdgcn_rcpf(w));
     return (v > 0.0f ? v : 0.0f) + (t > 0x1p-5f ? far : series);
 }
 __device__ __forceinline__ float sigmoid_near(float v) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
+    const float t = exp_minus_abs(v), s = __builtin_amdgcn_rcpf(1.0f + t);
+    return v < 0.0f ? t * s : s;
 }
 
 // The place of 16-byte piece i of row `row` in a tile of rows of ACROSS pieces is i ^ swap: what

@@ -435,7 +435,7 @@ int dcconv_gated_delta_update(const void *q, const void *key, const void *v, int
  * products of q and key under their decays; a BF16 state takes u (times its decay) as one
  * BF16 value, too.  Outputs are 0.0023 to 0.0028 of their size off, where the rounding of
  * an exact result is 0.0017 off.  Decays below 2^-126, a token's or several tokens' together, count
- * as zero.
+ * as zero, and u and b are held to multiples of 2^-133 at best.
  * What is not finite.  A NaN or infinity reaches what the recurrence lets it reach and
  * nothing else: no earlier token, no other sequence, and for v no other channel.  An
  * infinity may arrive as a NaN, and stays one.  Where states, u, or the factors that a token or
