@@ -60,15 +60,16 @@
 // Precision.  q, k and v are BF16 as given: a key's length enters as an FP32 factor.  Sums,
 // states, A and its inverse are FP32, prefix sums 64 bits and their differences 48.  An
 // operand that is no BF16 value is split into parts, BF16 values whose products are added
-// up, the smallest first.  With an F32 state (PARTS = 3): R, T, A_10 and U in three parts (all
-// 24 bits), S for S k in two; the state is within 1e-6 of its size of 64 bits.  (Two parts of
-// everything: packed sequences 1.2 times as fast, 2.8e-6.)  With a BF16 state (PARTS = 1): R, T
-// and A_10 in two, S for S k and the U that enters the state in one, since the state is rounded to
-// BF16 again when it is stored; it is up to 0.0028 of its size off then (S in two parts: 0.0025, and
-// the case below 161 us beside 151; U too: 173).  A call without states runs as one with BF16
-// states.  In every case P, and the copy of the state that q reads, are one BF16 value, and the U
-// that P multiplies two: outputs are 0.0023 to 0.0028 of their size off where the rounding of an
-// exact result is 0.0017 off.
+// up, the smallest first.  With an F32 state (PARTS = 3): R, T, A_10, U and S for S k in three parts, all
+// 24 bits; the state is off by what token-by-token FP32 is off by, 1e-7 to 7e-7 of its size over thousands of tokens.
+// (S in two parts: packed sequences 179 us beside 188, one long sequence 299 beside 319, but 1.4e-6 to
+// 3e-6 where decay is slow; two parts of everything: 1.2 times as fast again, 2.8e-6 with decay.)  With a BF16
+// state (PARTS = 1): R, T and A_10 in two, S for S k and the U that enters the state in one, since the state
+// is rounded to BF16 again when it is stored; it is 0.0021 to 0.0042 of its size off then, the most without decay
+// and with weights up to two (U in two parts: 0.0017 to 0.0026, the case below 162 us beside 151; S too: 0.0017,
+// 174).  A call without states runs as one with BF16 states.  In every case P, and the copy of the state that
+// q reads, are one BF16 value, and the U that P multiplies two: outputs are 0.0023 to 0.0029 of their size off
+// with F32 states and 0.0024 to 0.004 with others, where the rounding of an exact result is 0.0017 off.
 //
 // What is not finite.  An infinity or NaN of a later token must not meet the zeros above T's
 // and P's diagonals.  An entry of A that is not finite, from operands that are not or from finite
@@ -401,12 +402,13 @@ struct Sizes {
 
 // OUT: the outputs and final states.  Otherwise what a segment (any but a sequence's last) does
 // to a state: S' = S M + B, with B from no state and M, row by row, from the unit rows and no v.
-template <int KS, int C, int NT, int PARTS, bool OUT, bool WIDE>
+// SPARTS: parts of the state that k reads.
+template <int KS, int C, int NT, int PARTS, int SPARTS, bool OUT, bool WIDE>
 __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaParams p, const ScanPlan plan,
                                                                    const ScanGrid grid) {
     using Z = Sizes<KS, C, NT, PARTS>;
     constexpr int kB = Z::kBlocks, VP = Z::kRowsP, TP = Z::kTPitch, PP = Z::kPPitch, kSteps = KS / 32;
-    constexpr int kTParts = Z::kTParts, kSParts = PARTS == 1 ? 1 : 2;
+    constexpr int kTParts = Z::kTParts, kSParts = SPARTS;
     extern __shared__ u32x4 smem[];
     char *lds = reinterpret_cast<char *>(smem);
     uint16_t *sk = reinterpret_cast<uint16_t *>(lds + Z::kKey), *sq = reinterpret_cast<uint16_t *>(lds + Z::kQuery);
@@ -1308,10 +1310,10 @@ hipError_t allow_lds(const void *kernel, uint64_t *done) {
     return set;
 }
 
-template <int KS, int C, int NT, int PARTS, bool OUT, bool WIDE>
+template <int KS, int C, int NT, int PARTS, int SPARTS, bool OUT, bool WIDE>
 uint64_t lds_allowed = 0;
 
-template <int KS, int C, int NT, int PARTS, bool OUT, bool WIDE>
+template <int KS, int C, int NT, int PARTS, int SPARTS, bool OUT, bool WIDE>
 hipError_t launch(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream) {
     using Z = Sizes<KS, C, NT, PARTS>;
     const auto tiles = [](int64_t rows) { return (rows + Z::kRowsP - 1) / Z::kRowsP; };
@@ -1321,9 +1323,9 @@ hipError_t launch(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream
     const int64_t groups = (int64_t)plan.slots * p.g;
     grid.runs = groups >= 32;
     const int64_t units = (grid.runs ? (groups + 7) / 8 * 8 : groups) * grid.each;
-    auto kernel = delta_scan_kernel<KS, C, NT, PARTS, OUT, WIDE>;
+    auto kernel = delta_scan_kernel<KS, C, NT, PARTS, SPARTS, OUT, WIDE>;
     const hipError_t allowed =
-        allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, C, NT, PARTS, OUT, WIDE>);
+        allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, C, NT, PARTS, SPARTS, OUT, WIDE>);
     if (allowed != hipSuccess) return allowed;
     const int64_t across = units < kMaxBlocks ? units : kMaxBlocks, deep = (units + across - 1) / across;
     if (deep > 65535) return hipErrorInvalidConfiguration;
@@ -1333,9 +1335,11 @@ hipError_t launch(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream
 
 template <int KS, int C, int NT, bool WIDE>
 hipError_t launch_passes(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream) {
+    const bool f32 = p.state != nullptr && p.state_f32;
     if (plan.split) {
-        // (all 24 bits of M and B, whatever the state's type: their errors meet those of the state)
-        hipError_t err = launch<KS, C, NT, 3, false, WIDE>(p, plan, stream);
+        // (three parts of all but S, whatever the state's type; S, whose errors are 2^-18 with two, for F32 states)
+        hipError_t err = f32 ? launch<KS, C, NT, 3, 3, false, WIDE>(p, plan, stream)
+                             : launch<KS, C, NT, 3, 2, false, WIDE>(p, plan, stream);
         if (err != hipSuccess) return err;
         const int ptiles = (p.p + 15) / 16;
         const int64_t units = ((int64_t)p.n * p.h + 7) / 8 * 8 * ptiles;
@@ -1343,8 +1347,7 @@ hipError_t launch_passes(const DeltaParams &p, const ScanPlan &plan, hipStream_t
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
-    return p.state != nullptr && p.state_f32 ? launch<KS, C, NT, 3, true, WIDE>(p, plan, stream)
-                                             : launch<KS, C, NT, 1, true, WIDE>(p, plan, stream);
+    return f32 ? launch<KS, C, NT, 3, 3, true, WIDE>(p, plan, stream) : launch<KS, C, NT, 1, 1, true, WIDE>(p, plan, stream);
 }
 
 // Whether rows at p with the given element strides start on 16 bytes, and a chunk's rows
