@@ -38,9 +38,10 @@
 //                                               lengths of j + 2
 //
 // q, k and v go from memory to LDS without passing registers, q and k into one of three places
-// each, in pieces of 16 bytes whose order within a row differs from row to row so that the rows
-// and the transposing loads both find their banks free.  64-token chunks of 128-value keys take
-// 150 to 157 KiB of LDS: one block a CU.
+// each, in pieces of 16 bytes whose order within a row differs from row to row so that neither the rows
+// nor the transposing loads meet on a bank by their layout.  (Some accesses do: conflicts take 15.4e6 of the 82.3e6
+// cycles in which CUs are busy, in the case below.)  64-token chunks of 128-value keys take 150 to 157 KiB of
+// LDS: one block a CU.
 //
 // Few heads leave CUs idle.  Then sequences are cut into segments: what a segment does to a
 // state is S' = S M + B, with M and B from the same kernel (OUT = false), which takes the
@@ -81,15 +82,16 @@
 // state become NaN.
 //
 // What bounds it, at 8 x 2048 tokens, 32 heads of 128 x 128 in 16 groups, BF16 states (one block a CU, 32
-// chunks): 148 to 161 us, 2.2 times its bytes' time.  A chunk takes about 10000 cycles, 3200, 3000
+// chunks): 146 to 161 us, 2.2 times its bytes' time.  A chunk takes about 10000 cycles, 3200, 3000
 // and 2900 of them in the three phases of the waves that prepare, and 2900, 2350 and 2650 in those of the
 // waves with the state: both kinds wait for their own chain of reads, products and conversions, with two
 // waves a SIMD to cover for each other (matrix units 27 % busy, vector instructions 45 % of the issue
-// slots).  What did not help there: 64 rows a block, twice the blocks (273 us, since T and P
+// slots).  What did not help there: 64 rows a block, twice the blocks (239 us, since T and P
 // are prepared twice); loads of q and k by the waves with the state (147 to 158); a higher priority for
 // the waves that prepare (161); reading all of A's columns ahead of the substitution (spills).
 // What did: chunks in two halves rather than T over all 64 tokens, tiles straight to LDS, and no
-// spilled register (238 us to 150).
+// spilled register (238 us to 150).  (Kernels for F32 states whose rows are no whole 16 bytes spill two to seven of 256,
+// and the join for keys above 128 fifty: a wave holds 2 x 64 of M's values there.)
 #include <type_traits>
 
 #include "delta_common.h"
@@ -1357,13 +1359,13 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
 }
 
 // How a call is cut up, by a model of its time: rounds of a block a CU, in which a chunk takes
-// kChunkNs.  Blocks have 64 or 128 rows of a head's state (8 x 2048 tokens of 32 heads of 128: 273 us and 150;
+// kChunkNs.  Blocks have 64 or 128 rows of a head's state (8 x 2048 tokens of 32 heads of 128: 239 us and 156;
 // few heads fill more CUs with 64).  Where there are fewer blocks than CUs,
 // cutting sequences into segments may save time: it takes a pass that makes M and B, with blocks
 // for M's rows too and kStatesNs a chunk, a join of kJoinNs a segment, and two more launches, each
 // with the latency of a block's first and last accesses, kCutNs.  (128 x 128, F32 states, cut into 5, 8
-// and 16 segments: 16381 tokens of 16 heads 530, 362 and 327 us, where the whole takes 1014; into 4
-// and 8, 4096 tokens of 32 heads 193 and 179; 1000 tokens of 32 heads into 4: 81, whole 72.)
+// and 16 segments, 128 rows a block: 16381 tokens of 16 heads 566, 373 and 317 us, where the whole takes 1009 with 64 rows;
+// into 4 and 8, 4096 tokens of 32 heads 203 and 181, whole 256; 1000 tokens of 32 heads into 4: 83, whole 70.)
 constexpr int64_t kCus = 256;
 constexpr int64_t kChunkNs[2] = {4200, 5000}, kStatesNs[2] = {4000, 4700}, kJoinNs = 2200, kCutNs = 40000;
 

@@ -60,8 +60,8 @@ enum { DCCONV_DTYPE_BF16 = 0, DCCONV_DTYPE_F32 = 1 };
 enum {
     DCCONV_DEV_BAD_INDEX = 1, /* an index below -1, or not below S           */
     DCCONV_DEV_DUP_INDEX = 2, /* two rows of the batch select one real slot  */
-    DCCONV_DEV_BAD_SEQ = 4,   /* dcconv_prefill, dcconv_selective_scan: seq_starts is not
-                                 0 = starts[0] <= starts[1] <= ... <= starts[n] = t */
+    DCCONV_DEV_BAD_SEQ = 4,   /* dcconv_prefill, dcconv_selective_scan, dcconv_gated_delta_scan:
+                                 seq_starts is not 0 = starts[0] <= starts[1] <= ... <= starts[n] = t */
     DCCONV_DEV_BAD_SEQLEN = 8 /* dcconv_update, dcconv_update_tokens and
                                  dcconv_conv_selective_update: a cache_seqlens entry below 0 */
 };
