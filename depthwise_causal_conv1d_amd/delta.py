@@ -164,7 +164,7 @@ def gated_delta_update(q, k, v, dt, A, beta, state, *, dt_bias=None, dt_softplus
             q.data_ptr(), k.data_ptr(), v.data_ptr(), N, H, P, G, K, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
             dt_at, dt_code, ds[0], _s._vector("dt_bias", dt_bias, _s._F32, H, dev), int(bool(dt_softplus)),
             _s._vector("A", A, _s._F32, H, dev), beta_at, beta_code, es[0], int(bool(beta_sigmoid)),
-            int(bool(qk_l2norm)), l2norm_eps, K ** -0.5 if scale is None else scale, state.data_ptr(), code, S, slot,
+            int(bool(qk_l2norm)), l2norm_eps, max(K, 1) ** -0.5 if scale is None else scale, state.data_ptr(), code, S, slot,
             _s._vector("state_indices", state_indices, _s._I32, N, dev), out.data_ptr(), os_[0], os_[1],
             _s._status(dev_status, dev), _b.stream(dev))
     _b.raise_for(rc)
@@ -239,7 +239,7 @@ def gated_delta_scan(q, k, v, dt, A, beta, *, dt_bias=None, dt_softplus=False, b
             q.data_ptr(), k.data_ptr(), v.data_ptr(), n, T, H, P, G, K, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2],
             vs[0], vs[1], vs[2], dt_at, dt_code, ds[0], ds[1], _s._vector("dt_bias", dt_bias, _s._F32, H, dev),
             int(bool(dt_softplus)), _s._vector("A", A, _s._F32, H, dev), beta_at, beta_code, es[0], es[1],
-            int(bool(beta_sigmoid)), int(bool(qk_l2norm)), l2norm_eps, K ** -0.5 if scale is None else scale, starts,
+            int(bool(beta_sigmoid)), int(bool(qk_l2norm)), l2norm_eps, max(K, 1) ** -0.5 if scale is None else scale, starts,
             pool, code, S, slot, _s._vector("state_indices", state_indices, _s._I32, n, dev), init, out.data_ptr(),
             os_[0], os_[1], os_[2], None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel(), _s._status(dev_status, dev), _b.stream(dev))

@@ -155,3 +155,17 @@ def test_scan_of_a_broken_table_of_cut_or_many_sequences(n, seed):
                         has_initial_state=torch.ones(n, dtype=torch.bool, device="cuda"),
                         seq_starts=table.to(torch.int32).cuda())
     assert int(status) == dc.DCCONV_DEV_BAD_SEQ and pool_kept() and out_kept() and work_kept()
+
+
+@pytest.mark.parametrize("sizes", [(0, 8, 1, 8), (2, 0, 1, 8), (2, 8, 0, 8), (2, 8, 1, 0)])
+def test_sizes_of_zero_are_refused(sizes):
+    """Heads, channels, groups and keys: as any other size that the entry points refuse."""
+    H, P, G, K = sizes
+    z = torch.zeros(2, 3, 8, 8, dtype=torch.bfloat16, device="cuda")
+    k, v = z[:, :, :G, :K], z[:, :, :H, :P]
+    A, state = torch.zeros(H, device="cuda"), torch.zeros(2, H, P, K, device="cuda")
+    dt = torch.zeros(2, 3, H, device="cuda")
+    with pytest.raises(ValueError, match=">= 1"):
+        dc.gated_delta_scan(k, k, v, dt, A, dt)
+    with pytest.raises(ValueError, match=">= 1"):
+        dc.gated_delta_update(k[:, 0], k[:, 0], v[:, 0], dt[:, 0], A, dt[:, 0], state)
