@@ -39,7 +39,7 @@
 //
 // q, k and v go from memory to LDS without passing registers, q and k into one of three places
 // each, in pieces of 16 bytes whose order within a row differs from row to row so that neither the rows
-// nor the transposing loads meet on a bank by their layout.  (Some accesses do: conflicts take 15.4e6 of the 82.3e6
+// nor the transposing loads meet on a bank by their layout.  (Some accesses do: conflicts take 15.4e6 of the 96.3e6
 // cycles in which CUs are busy, in the case below.)  64-token chunks of 128-value keys take 150 to 157 KiB of
 // LDS: one block a CU.
 //
@@ -61,16 +61,15 @@
 // Precision.  q, k and v are BF16 as given: a key's length enters as an FP32 factor.  Sums,
 // states, A and its inverse are FP32, prefix sums 64 bits and their differences 48.  An
 // operand that is no BF16 value is split into parts, BF16 values whose products are added
-// up, the smallest first.  With an F32 state (PARTS = 3): R, T, A_10, U and S for S k in three parts, all
-// 24 bits; the state is off by what token-by-token FP32 is off by, 1e-7 to 7e-7 of its size over thousands of tokens.
-// (S in two parts: packed sequences 179 us beside 188, one long sequence 299 beside 319, but 1.4e-6 to
-// 3e-6 where decay is slow; two parts of everything: 1.2 times as fast again, 2.8e-6 with decay.)  With a BF16
-// state (PARTS = 1): R, T and A_10 in two, S for S k and the U that enters the state in one, since the state
-// is rounded to BF16 again when it is stored; it is 0.0021 to 0.0042 of its size off then, the most without decay
-// and with weights up to two (U in two parts: 0.0017 to 0.0026, the case below 162 us beside 151; S too: 0.0017,
-// 174).  A call without states runs as one with BF16 states.  In every case P, and the copy of the state that
-// q reads, are one BF16 value, and the U that P multiplies two: outputs are 0.0023 to 0.0029 of their size off
-// with F32 states and 0.0024 to 0.004 with others, where the rounding of an exact result is 0.0017 off.
+// up, the smallest first.  With an F32 state R, T, A_10, U and S for S k have three parts (PARTS = 3), all 24
+// bits: the state is off by what token-by-token FP32 is off by, 1e-7 to 7e-7 of its size over thousands of tokens.
+// (S in two parts: packed sequences 179 us beside 188, but 1.4e-6 to 3e-6 where decay is slow.)  With a BF16
+// state, or none, they have two (PARTS = 2), and the state is off by its own rounding.  (S and the U that enters
+// the state in one: states 0.0021 to 0.0042 of their size off, the most without decay and with weights up to two,
+// where the rounding is 0.0017 off.)  S for S q has two, as the U that P multiplies, and P is one BF16 value: outputs
+// are 0.0017 to 0.0023 of their size off where the rounding of an exact result is 0.0017 off.  (S for S q in one:
+// 0.0023 to 0.0029 with F32 states, 0.0024 to 0.004 with the fewer parts for others.  The case below takes 180 us, with
+// S for S k in one part 171, S for S q too 162, and U for the state too 151; packed sequences 194, with S for S q in one 188.)
 //
 // What is not finite.  An infinity or NaN of a later token must not meet the zeros above T's
 // and P's diagonals.  An entry of A that is not finite, from operands that are not or from finite
@@ -82,15 +81,14 @@
 // state become NaN.
 //
 // What bounds it, at 8 x 2048 tokens, 32 heads of 128 x 128 in 16 groups, BF16 states (one block a CU, 32
-// chunks): 146 to 161 us, 2.2 times its bytes' time.  A chunk takes about 10000 cycles, 3200, 3000
-// and 2900 of them in the three phases of the waves that prepare, and 2900, 2350 and 2650 in those of the
-// waves with the state: both kinds wait for their own chain of reads, products and conversions, with two
-// waves a SIMD to cover for each other (matrix units 27 % busy, vector instructions 45 % of the issue
-// slots).  What did not help there: 64 rows a block, twice the blocks (239 us, since T and P
-// are prepared twice); loads of q and k by the waves with the state (147 to 158); a higher priority for
-// the waves that prepare (161); reading all of A's columns ahead of the substitution (spills).
-// What did: chunks in two halves rather than T over all 64 tokens, tiles straight to LDS, and no
-// spilled register (238 us to 150).  (Kernels for F32 states whose rows are no whole 16 bytes spill two to seven of 256,
+// chunks): 180 to 189 us, 2.6 times its bytes' time.  A chunk takes about 12000 cycles.  Both kinds of waves wait for their
+// own chain of reads, products and conversions, with two waves a SIMD to cover for each other (matrix units 36 % busy,
+// vector instructions 51 % of the issue slots); 32 more matrix
+// instructions a wave and chunk (512 cycles) add 9 to 12 us.  What did not help there: 64 rows a block, twice the
+// blocks (255 us, since T and P are prepared twice); S k and S q in one loop that splits S once (180), a part of S q
+// in the second phase (178 to 180, or spills); loads of q and k by the waves with the state, a higher priority for the
+// waves that prepare (both slower by 7 %); reading all of A's columns ahead of the substitution (spills).
+// What did: chunks in two halves rather than T over all 64 tokens, tiles straight to LDS, and no spilled register.  (Kernels for F32 states whose rows are no whole 16 bytes spill two to seven of 256,
 // and the join for keys above 128 fifty: a wave holds 2 x 64 of M's values there.)
 #include <type_traits>
 
@@ -388,14 +386,13 @@ template <int KS, int C, int NT, int PARTS>
 struct Sizes {
     static constexpr int kRowsP = kHalf * 16 * NT;  // state rows of a block
     static constexpr int kPPitch = C + 8, kTPitch = 40;  // rows of 16 lanes' 16-byte reads on banks of their own
-    static constexpr int kTParts = PARTS == 1 ? 2 : PARTS;
     static constexpr int kBlocks = C / 16, kHalves = C / 32;
     static constexpr int kKey = 0;                                   // [3][C][KS]
     static constexpr int kQuery = kKey + 3 * C * KS * 2;             // [3][C][KS]
     static constexpr int kV = kQuery + 3 * C * KS * 2;               // [C][kRowsP]
-    static constexpr int kT = kV + C * kRowsP * 2;                   // [kTParts][C][kTPitch]
-    static constexpr int kOff = kT + kTParts * C * kTPitch * 2;      // [kTParts][C - 32][kTPitch]
-    static constexpr int kP = kOff + kTParts * (C - 32) * kTPitch * 2;  // [C][kPPitch]
+    static constexpr int kT = kV + C * kRowsP * 2;                   // [PARTS][C][kTPitch]
+    static constexpr int kOff = kT + PARTS * C * kTPitch * 2;      // [PARTS][C - 32][kTPitch]
+    static constexpr int kP = kOff + PARTS * (C - 32) * kTPitch * 2;  // [C][kPPitch]
     static constexpr int kA = kP + C * kPPitch * 2;                  // [3 kHalves][16][kAPitch] floats
     static constexpr int kToken = kA + 3 * kHalves * 16 * kAPitch * 4;  // [3][kTokenRows][C] floats
     static constexpr int kBytes = kToken + 3 * kTokenRows * C * 4;
@@ -404,13 +401,11 @@ struct Sizes {
 
 // OUT: the outputs and final states.  Otherwise what a segment (any but a sequence's last) does
 // to a state: S' = S M + B, with B from no state and M, row by row, from the unit rows and no v.
-// SPARTS: parts of the state that k reads.
-template <int KS, int C, int NT, int PARTS, int SPARTS, bool OUT, bool WIDE>
+template <int KS, int C, int NT, int PARTS, bool OUT, bool WIDE>
 __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaParams p, const ScanPlan plan,
                                                                    const ScanGrid grid) {
     using Z = Sizes<KS, C, NT, PARTS>;
     constexpr int kB = Z::kBlocks, VP = Z::kRowsP, TP = Z::kTPitch, PP = Z::kPPitch, kSteps = KS / 32;
-    constexpr int kTParts = Z::kTParts, kSParts = SPARTS;
     extern __shared__ u32x4 smem[];
     char *lds = reinterpret_cast<char *>(smem);
     uint16_t *sk = reinterpret_cast<uint16_t *>(lds + Z::kKey), *sq = reinterpret_cast<uint16_t *>(lds + Z::kQuery);
@@ -458,9 +453,9 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
     const int chunks = (len + C - 1) / C;
 
     // the tiles of T and P above the diagonal that products over 32 tokens read: zeros for good
-    for (int i = tid; i < (kTParts + 1) * (kB / 2) * 16 * 4; i += kScanBlock) {
+    for (int i = tid; i < (PARTS + 1) * (kB / 2) * 16 * 4; i += kScanBlock) {
         const int piece = i & 3, row = (i >> 2) & 15, m = (i >> 6) % (kB / 2), part = (i >> 6) / (kB / 2);
-        uint16_t *to = part < kTParts ? st + (part * C + 32 * m + row) * TP : sp + (32 * m + row) * PP + 32 * m;
+        uint16_t *to = part < PARTS ? st + (part * C + 32 * m + row) * TP : sp + (32 * m + row) * PP + 32 * m;
         *reinterpret_cast<u32x2 *>(to + 8 * piece + 4) = u32x2{0, 0};
     }
 
@@ -548,20 +543,20 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                 tok[kUnitQ * C] = p.scale * unit_factor(p, qq);
             }
         };
-        // Four values as kTParts parts, and put `apart` values apart.
-        auto to_parts = [&](float (&v)[4], u32x2 (&parts)[kTParts]) {
+        // Four values as PARTS parts, and put `apart` values apart.
+        auto to_parts = [&](float (&v)[4], u32x2 (&parts)[PARTS]) {
 #pragma unroll
-            for (int part = 0; part < kTParts; ++part) {
+            for (int part = 0; part < PARTS; ++part) {
                 const uint32_t h0 = pack_bf16x2(v[0], v[1]), h1 = pack_bf16x2(v[2], v[3]);
                 parts[part] = u32x2{h0, h1};
                 v[0] -= lo_f32(h0), v[1] -= hi_f32(h0), v[2] -= lo_f32(h1), v[3] -= hi_f32(h1);
             }
         };
         auto put_parts = [&](float (&v)[4], uint16_t *to, int apart) {
-            u32x2 parts[kTParts];
+            u32x2 parts[PARTS];
             to_parts(v, parts);
 #pragma unroll
-            for (int part = 0; part < kTParts; ++part) *reinterpret_cast<u32x2 *>(to + part * apart) = parts[part];
+            for (int part = 0; part < PARTS; ++part) *reinterpret_cast<u32x2 *>(to + part * apart) = parts[part];
         };
         // ---- block row I of P of chunk j
         auto form_p = [&](auto row_constant, int j) {
@@ -625,7 +620,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         auto logs_at = [&](const float *tok, int t) {
             return Logs{lds4f(tok + kSumHigh * C + t), lds4f(tok + kSumLow * C + t)};
         };
-        u32x2 off[2][kTParts];  // what this wave has formed of the tiles between halves
+        u32x2 off[2][PARTS];  // what this wave has formed of the tiles between halves
         auto form_a = [&](auto wave_constant, int j) {
             // wave W's tiles: diagonal block W, and: blocks (2, W) and (3, W) for W = 0, 1, block
             // (1, 0) for W = 2 and (3, 2) for W = 3.  (Two blocks: (0, 0), and (1, 1) and (1, 0).)
@@ -698,7 +693,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         auto put_off = [&](int w) {
             if (kB == 2 || w >= 2) return;
 #pragma unroll
-            for (int part = 0; part < kTParts; ++part) {
+            for (int part = 0; part < PARTS; ++part) {
                 uint16_t *to = so + (part * (C - 32) + r) * TP + 8 * g + 4 * w;
                 *reinterpret_cast<u32x2 *>(to) = off[0][part];
                 *reinterpret_cast<u32x2 *>(to + 16 * TP) = off[1][part];
@@ -882,7 +877,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         for (int n = 0; n < NT; ++n) hs[m][n] = f32x4_t{0, 0, 0, 0};
     // Where the state is from and where it goes: the pool's slot, or the workspace's place.
     // body(a tile's four values, their byte offset in the head's state, how many there are)
-    constexpr bool kF32 = PARTS > 1;  // the pool's type, where there is a pool
+    constexpr bool kF32 = PARTS == 3;  // the pool's type, where there is a pool
     const bool wide_pool = p.k % 4 == 0 && p.ss_s % 4 == 0 && reinterpret_cast<uintptr_t>(p.state) % 16 == 0;
     const bool wide_place = p.k % 4 == 0;
     const auto in_pool = [&]() {
@@ -933,7 +928,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         const uint16_t *km = sk + j % 3 * C * KS, *qm = sq + j % 3 * C * KS;
         const float *tok = tokens + j % 3 * kTokenRows * C;
         f32x4_t d[kB][NT], o[kB][NT];
-        u32x4 rp[NT][kTParts];
+        u32x4 rp[NT][PARTS];
         // ---- d = S k (columns p, rows t), then R
         {
             const int lane_here = here(lane), r = lane_here & 15, g = lane_here >> 4;
@@ -942,14 +937,14 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                 for (int n = 0; n < NT; ++n) d[tt][n] = f32x4_t{0, 0, 0, 0};
             // Rows of k, read ahead of their products; the next 32 columns of the state are split meanwhile.
-            u32x4 f[2][kB], hp[2][NT][kSParts];
+            u32x4 f[2][kB], hp[2][NT][PARTS];
             auto read_rows = [&](int m) {
 #pragma unroll
                 for (int tt = 0; tt < kB; ++tt) f[m & 1][tt] = lds16(km + 16 * tt * KS + row_place(m, r, g));
             };
             auto split_state = [&](int m) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) split<kSParts>(hs[2 * m][n], hs[2 * m + 1][n], hp[m & 1][n]);
+                for (int n = 0; n < NT; ++n) split<PARTS>(hs[2 * m][n], hs[2 * m + 1][n], hp[m & 1][n]);
             };
             read_rows(0);
             split_state(0);
@@ -958,7 +953,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                 if (m + 1 < kSteps) read_rows(m + 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int part = kSParts - 1; part >= 0; --part)
+                for (int part = PARTS - 1; part >= 0; --part)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -967,9 +962,9 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                     split_state(m + 1);
                     // a product, and what the vector units do meanwhile
 #pragma unroll
-                    for (int i = 0; i < kSParts * NT * kB; ++i) {
+                    for (int i = 0; i < PARTS * NT * kB; ++i) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, PARTS == 1 ? 2 : 3, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
                     }
                 }
             }
@@ -991,10 +986,12 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    u32x4 hp[1];
-                    split<1>(hs[2 * m][n], hs[2 * m + 1][n], hp);
+                    u32x4 hp[2];
+                    split<2>(hs[2 * m][n], hs[2 * m + 1][n], hp);
 #pragma unroll
-                    for (int tt = 0; tt < kB; ++tt) o[tt][n] = mfma(hp[0], f[m & 1][tt], o[tt][n]);
+                    for (int part = 1; part >= 0; --part)
+#pragma unroll
+                        for (int tt = 0; tt < kB; ++tt) o[tt][n] = mfma(hp[part], f[m & 1][tt], o[tt][n]);
                 }
             }
             }
@@ -1011,7 +1008,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                         d[2 * m][n][i] = ((i & 1) ? hi_f32(v[i >> 1]) : lo_f32(v[i >> 1])) - w0[i] * d[2 * m][n][i];
                         d[2 * m + 1][n][i] = ((i & 1) ? hi_f32(v[2 + (i >> 1)]) : lo_f32(v[2 + (i >> 1)])) - w1[i] * d[2 * m + 1][n][i];
                     }
-                    if (m == 0) split<kTParts>(d[0][n], d[1][n], rp[n]);
+                    if (m == 0) split<PARTS>(d[0][n], d[1][n], rp[n]);
                 }
             }
         }
@@ -1019,7 +1016,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         // ---- d = U, half by half: U_0 = T_0 R_0, U_1 = T_1 (R_1 - A_10 U_0)
         int cut[NT];  // the first token whose R or U is not finite
         bool bad = false;
-        u32x4 up[kB / 2][NT][kTParts], wp[kB / 2][NT][PARTS];
+        u32x4 up[kB / 2][NT][PARTS], wp[kB / 2][NT][PARTS];
         {
             const int lane_here = here(lane), r = lane_here & 15, g = lane_here >> 4;
 #pragma unroll
@@ -1028,30 +1025,30 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             for (int m = 0; m < kB / 2; ++m) {
                 f32x4_t(&d0)[NT] = d[2 * m], (&d1)[NT] = d[2 * m + 1];
                 if (m > 0) {
-                    u32x4 af[2][kTParts];
+                    u32x4 af[2][PARTS];
 #pragma unroll
-                    for (int a = kTParts - 1; a >= 0; --a)
+                    for (int a = PARTS - 1; a >= 0; --a)
 #pragma unroll
                         for (int tt = 0; tt < 2; ++tt) af[tt][a] = lds16(so + (a * (C - 32) + 16 * tt + r) * TP + 8 * g);
 #pragma unroll
-                    for (int a = kTParts - 1; a >= 0; --a)
+                    for (int a = PARTS - 1; a >= 0; --a)
 #pragma unroll
-                        for (int b = kTParts - 1; b >= 0; --b)
+                        for (int b = PARTS - 1; b >= 0; --b)
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                if (a + b < kTParts) {
+                                if (a + b < PARTS) {
                                     d0[n] = mfma(af[0][a], up[0][n][b], d0[n]);
                                     d1[n] = mfma(af[1][a], up[0][n][b], d1[n]);
                                 }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         if (bad && cut[n] < 32) d0[n] = d1[n] = f32x4_t{0, 0, 0, 0};
-                        split<kTParts>(d0[n], d1[n], rp[n]);
+                        split<PARTS>(d0[n], d1[n], rp[n]);
                     }
                 }
-                u32x4 tf[2][kTParts];
+                u32x4 tf[2][PARTS];
 #pragma unroll
-                for (int a = kTParts - 1; a >= 0; --a)
+                for (int a = PARTS - 1; a >= 0; --a)
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt) tf[tt][a] = lds16(st + (a * C + 32 * m + 16 * tt + r) * TP + 8 * g);
                 const f32x4_t w0 = lds4f(tok + kForU * C + 32 * m + 4 * g), w1 = lds4f(tok + kForU * C + 32 * m + 16 + 4 * g);
@@ -1059,19 +1056,19 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                     for (int n = 0; n < NT; ++n) d0[n] = d1[n] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-                    for (int a = kTParts - 1; a >= 0; --a)
+                    for (int a = PARTS - 1; a >= 0; --a)
 #pragma unroll
-                        for (int b = kTParts - 1; b >= 0; --b)
+                        for (int b = PARTS - 1; b >= 0; --b)
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                if (a + b < kTParts) {
+                                if (a + b < PARTS) {
                                     d0[n] = mfma(tf[0][a], rp[n][b], d0[n]);
                                     d1[n] = mfma(tf[1][a], rp[n][b], d1[n]);
                                 }
                 };
                 correct();
 #pragma unroll
-                for (int n = 0; n < NT; ++n) split<kTParts>(d0[n], d1[n], up[m][n]);
+                for (int n = 0; n < NT; ++n) split<PARTS>(d0[n], d1[n], up[m][n]);
                 float probe[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -1093,7 +1090,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                         for (int i = 0; i < 8; ++i)
                             if (16 * (i >> 2) + 4 * g + (i & 3) >= at)
 #pragma unroll
-                                for (int part = 0; part < kTParts; ++part)
+                                for (int part = 0; part < PARTS; ++part)
                                     rp[n][part][i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
                         if (at < 32) cut[n] = min(cut[n], 32 * m + at);
                     }
@@ -1112,7 +1109,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                             if (32 * m + 4 * g + i >= cut[n]) d0[n][i] = 0.0f;
                             if (32 * m + 16 + 4 * g + i >= cut[n]) d1[n][i] = 0.0f;
                         }
-                        split<kTParts>(d0[n], d1[n], up[m][n]);
+                        split<PARTS>(d0[n], d1[n], up[m][n]);
                     }
                 }
 #pragma unroll
@@ -1312,10 +1309,10 @@ hipError_t allow_lds(const void *kernel, uint64_t *done) {
     return set;
 }
 
-template <int KS, int C, int NT, int PARTS, int SPARTS, bool OUT, bool WIDE>
+template <int KS, int C, int NT, int PARTS, bool OUT, bool WIDE>
 uint64_t lds_allowed = 0;
 
-template <int KS, int C, int NT, int PARTS, int SPARTS, bool OUT, bool WIDE>
+template <int KS, int C, int NT, int PARTS, bool OUT, bool WIDE>
 hipError_t launch(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream) {
     using Z = Sizes<KS, C, NT, PARTS>;
     const auto tiles = [](int64_t rows) { return (rows + Z::kRowsP - 1) / Z::kRowsP; };
@@ -1325,9 +1322,9 @@ hipError_t launch(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream
     const int64_t groups = (int64_t)plan.slots * p.g;
     grid.runs = groups >= 32;
     const int64_t units = (grid.runs ? (groups + 7) / 8 * 8 : groups) * grid.each;
-    auto kernel = delta_scan_kernel<KS, C, NT, PARTS, SPARTS, OUT, WIDE>;
+    auto kernel = delta_scan_kernel<KS, C, NT, PARTS, OUT, WIDE>;
     const hipError_t allowed =
-        allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, C, NT, PARTS, SPARTS, OUT, WIDE>);
+        allow_lds(reinterpret_cast<const void *>(kernel), &lds_allowed<KS, C, NT, PARTS, OUT, WIDE>);
     if (allowed != hipSuccess) return allowed;
     const int64_t across = units < kMaxBlocks ? units : kMaxBlocks, deep = (units + across - 1) / across;
     if (deep > 65535) return hipErrorInvalidConfiguration;
@@ -1335,13 +1332,10 @@ hipError_t launch(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream
     return hipGetLastError();
 }
 
-template <int KS, int C, int NT, bool WIDE>
+template <int KS, int C, int NT, int PARTS, bool WIDE>
 hipError_t launch_passes(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream) {
-    const bool f32 = p.state != nullptr && p.state_f32;
     if (plan.split) {
-        // (three parts of all but S, whatever the state's type; S, whose errors are 2^-18 with two, for F32 states)
-        hipError_t err = f32 ? launch<KS, C, NT, 3, 3, false, WIDE>(p, plan, stream)
-                             : launch<KS, C, NT, 3, 2, false, WIDE>(p, plan, stream);
+        hipError_t err = launch<KS, C, NT, PARTS, false, WIDE>(p, plan, stream);
         if (err != hipSuccess) return err;
         const int ptiles = (p.p + 15) / 16;
         const int64_t units = ((int64_t)p.n * p.h + 7) / 8 * 8 * ptiles;
@@ -1349,7 +1343,13 @@ hipError_t launch_passes(const DeltaParams &p, const ScanPlan &plan, hipStream_t
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
-    return f32 ? launch<KS, C, NT, 3, 3, true, WIDE>(p, plan, stream) : launch<KS, C, NT, 1, 1, true, WIDE>(p, plan, stream);
+    return launch<KS, C, NT, PARTS, true, WIDE>(p, plan, stream);
+}
+
+template <int KS, int C, int NT, bool WIDE>
+hipError_t launch_state(const DeltaParams &p, const ScanPlan &plan, hipStream_t stream) {
+    return p.state != nullptr && p.state_f32 ? launch_passes<KS, C, NT, 3, WIDE>(p, plan, stream)
+                                             : launch_passes<KS, C, NT, 2, WIDE>(p, plan, stream);
 }
 
 // Whether rows at p with the given element strides start on 16 bytes, and a chunk's rows
@@ -1359,13 +1359,13 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
 }
 
 // How a call is cut up, by a model of its time: rounds of a block a CU, in which a chunk takes
-// kChunkNs.  Blocks have 64 or 128 rows of a head's state (8 x 2048 tokens of 32 heads of 128: 239 us and 156;
+// kChunkNs.  Blocks have 64 or 128 rows of a head's state (8 x 2048 tokens of 32 heads of 128: 255 us and 178;
 // few heads fill more CUs with 64).  Where there are fewer blocks than CUs,
 // cutting sequences into segments may save time: it takes a pass that makes M and B, with blocks
 // for M's rows too and kStatesNs a chunk, a join of kJoinNs a segment, and two more launches, each
 // with the latency of a block's first and last accesses, kCutNs.  (128 x 128, F32 states, cut into 5, 8
-// and 16 segments, 128 rows a block: 16381 tokens of 16 heads 566, 373 and 317 us, where the whole takes 1009 with 64 rows;
-// into 4 and 8, 4096 tokens of 32 heads 203 and 181, whole 256; 1000 tokens of 32 heads into 4: 83, whole 70.)
+// and 16 segments, 128 rows a block: 16381 tokens of 16 heads 577, 380 and 322 us, where the whole takes 1012 with 64 rows;
+// into 4 and 8, 4096 tokens of 32 heads 207 and 183, whole 258; 1000 tokens of 32 heads into 4: 84, whole 71.)
 constexpr int64_t kCus = 256;
 constexpr int64_t kChunkNs[2] = {4200, 5000}, kStatesNs[2] = {4000, 4700}, kJoinNs = 2200, kCutNs = 40000;
 
@@ -1412,14 +1412,14 @@ hipError_t launch_delta_scan(const DeltaParams &p, hipStream_t stream, const cha
                               : (wide ? "delta_scan" : "delta_scan_scalar");
     const bool two = plan.two;
     if (p.k <= 64) {
-        if (two) return wide ? launch_passes<64, 64, 2, true>(p, plan, stream) : launch_passes<64, 64, 2, false>(p, plan, stream);
-        return wide ? launch_passes<64, 64, 1, true>(p, plan, stream) : launch_passes<64, 64, 1, false>(p, plan, stream);
+        if (two) return wide ? launch_state<64, 64, 2, true>(p, plan, stream) : launch_state<64, 64, 2, false>(p, plan, stream);
+        return wide ? launch_state<64, 64, 1, true>(p, plan, stream) : launch_state<64, 64, 1, false>(p, plan, stream);
     }
     if (p.k <= 128) {
-        if (two) return wide ? launch_passes<128, 64, 2, true>(p, plan, stream) : launch_passes<128, 64, 2, false>(p, plan, stream);
-        return wide ? launch_passes<128, 64, 1, true>(p, plan, stream) : launch_passes<128, 64, 1, false>(p, plan, stream);
+        if (two) return wide ? launch_state<128, 64, 2, true>(p, plan, stream) : launch_state<128, 64, 2, false>(p, plan, stream);
+        return wide ? launch_state<128, 64, 1, true>(p, plan, stream) : launch_state<128, 64, 1, false>(p, plan, stream);
     }
-    return wide ? launch_passes<256, 32, 1, true>(p, plan, stream) : launch_passes<256, 32, 1, false>(p, plan, stream);
+    return wide ? launch_state<256, 32, 1, true>(p, plan, stream) : launch_state<256, 32, 1, false>(p, plan, stream);
 }
 
 }  // namespace dcconv

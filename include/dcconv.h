@@ -430,14 +430,12 @@ int dcconv_gated_delta_update(const void *q, const void *key, const void *v, int
  *             need not be kept and are not read from one call to the next.  Calls that
  *             may run at the same time need one each.
  * Precision.  Tokens are taken 32 or 64 at a time as matrix products with BF16 operands
- * and FP32 sums.  An F32 state is kept as exactly as FP32 products keep it (over thousands of
- * tokens 1e-7 to 7e-7 of its size off).  On the way to out, the copy of the state that q reads
- * and the products of q and key under their decays are rounded to BF16 once.  With a BF16 state, or
- * none (the final state is dropped), so are the copy of the state that key reads and the u, times its
- * decay, that enters the state.  Outputs are 0.0023 to 0.0029 of their size off with an F32 state,
- * 0.0024 to 0.004 with a BF16 one or none, and a BF16 state 0.0021 to 0.0042 (the most without decay and
- * with b up to 2), where the rounding of an exact result is 0.0017 off.  Decays below 2^-126, a token's
- * or several tokens' together, count as zero, and u and b are held to multiples of 2^-133 at best.
+ * and FP32 sums; operands that are no BF16 values are split into two or three.  An F32 state is
+ * kept as exactly as FP32 products keep it (over thousands of tokens 1e-7 to 7e-7 of its size off),
+ * a BF16 one is rounded when it is stored and nowhere else.  What is rounded to BF16 once on the way to
+ * out are the products of q and key under their decays: outputs are 0.0017 to 0.0023 of their size off, where
+ * the rounding of an exact result is 0.0017 off.  Decays below 2^-126, a token's or several tokens' together,
+ * count as zero, and u and b are held to multiples of 2^-133 at best.
  * What is not finite.  A NaN or infinity reaches what the recurrence lets it reach and
  * nothing else: no earlier token, no other sequence, and for v no other channel.  An
  * infinity may arrive as a NaN, and stays one.  Where states, u, or the factors that a token or

@@ -5,22 +5,14 @@ Rounding to BF16 is off by e = 0.00166 in the mean (uniform within half a step o
 
 F32 states: sums of 64 tokens make about a dozen roundings of 2^-24 a chunk, 0.29 of that each in the mean; over
 128 chunks without any forgetting sqrt(12 * 128) * 0.29 * 2^-24 = 7e-7.  At most 2^-20.  (S in two parts where
-k reads it: 2^-18 for every token's correction, 1.4e-6 to 3e-6.)
+k reads it: 2^-18 for every token's correction, 1.4e-6 to 3e-6.)  BF16 states: their one rounding, e.
 
-The others, for random keys of length one, without decay (with it, less is carried on), in units of the channel's
-v^2 and of e^2, with b1 = mean of b, b2 = mean of b^2, f = 2 b1 - b2:
-
-* |S k|^2 = |S|^2 / K = b2 / f, and u^2 = b2 (1 + b2 / f) a token: the state's steady size.  A chunk of C tokens
-  leaves e^(-f C / K) of an error's square and turns it to e^(-b1 C / K) of itself.
-* u in one part: C u^2 / K a chunk, in the steady state U = (C / K) u^2 / (1 - e^(-f C / K)).  S in one part where k
-  reads it: a chunk adds the rounding's part that it changes, V = b2 / f (e^(-f C / K) - 2 e^(-b1 C / K) + 1) /
-  (1 - e^(-f C / K)).  States, rounded once more: sqrt(1 + (U + V) f / b2) e.
-* Outputs: their own rounding, 1; P's, C u^2 f / (2 K b2); with F32 states that of the S that q reads, 1; with others
-  that one through the chunk's tokens, of which m = (1 - e^(-f C / K)) K / (f C) is left in the mean, and the states' m (U + V) f / b2.
-
-With K = C = 64, where they are largest: b = sigmoid of a normal number (b1 = 0.5, b2 = 0.293) gives outputs 1.58 e =
-0.0026 with F32 states and 2.01 e = 0.0033 with others, whose states are 1.88 e = 0.0031; b uniform up to 1.9 (b1 = 0.95,
-b2 = 1.203) gives 1.72 e = 0.0029, 2.54 e = 0.0042 and 2.50 e = 0.0042.  The draw is left 5 %.
+Outputs: their own rounding and that of the products of q and k, P.  P's is of the size of the terms P u: at most that of
+the output, sqrt(2) e in all, where they do not cancel.  Without decay, for random keys of length one, in units of v^2, with
+b1 = mean of b, b2 = mean of b^2, f = 2 b1 - b2: the state's steady size is |S k|^2 = b2 / f, as that of an
+output, and u^2 = b2 (1 + b2 / f), of which the C / 2 tokens that a chunk has behind it in the mean give P's terms
+C u^2 / (2 K): sqrt(1 + C u^2 f / (2 K b2)) e.  With K = C = 64, where that is largest, b = sigmoid of a normal
+number (b1 = 0.5, b2 = 0.293) gives 1.23 e, and b uniform up to 1.9 (b1 = 0.95, b2 = 1.203) 1.40 e.  The draw is left 5 %.
 """
 import pytest
 import torch
@@ -95,10 +87,10 @@ def test_errors_in_the_mean(N, T, H, P, K, cut, rate, sigmoid):
     y, s = case.exact()
     out, pool = case.call(torch.float32)
     assert dc.dcconv_last_kernel().startswith("delta_scan_split") == cut
-    errors = {"out, F32 states": (off(out, y), 1.05 * E * (1.58 if sigmoid else 1.72)), "F32 states": (off(pool, s), 2.0 ** -20)}
+    most = 1.05 * E * (1.23 if sigmoid and rate < 1 else 2 ** 0.5)
+    errors = {"out, F32 states": (off(out, y), most), "F32 states": (off(pool, s), 2.0 ** -20)}
     out, pool = case.call(torch.bfloat16)
-    errors["out, BF16 states"] = off(out, y), 1.05 * E * (2.01 if sigmoid else 2.54)
-    errors["BF16 states"] = off(pool, s), 1.05 * E * (1.88 if sigmoid else 2.50)
+    errors["out, BF16 states"], errors["BF16 states"] = (off(out, y), most), (off(pool, s), 1.05 * E)
     y, s = case.exact(init=False)
-    errors["out, no states"] = off(case.call(None)[0], y), 1.05 * E * (2.01 if sigmoid else 2.54)
+    errors["out, no states"] = off(case.call(None)[0], y), most
     assert all(v <= most for v, most in errors.values()), errors
