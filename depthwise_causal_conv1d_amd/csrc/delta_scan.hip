@@ -39,8 +39,8 @@
 //
 // q, k and v go from memory to LDS without passing registers, q and k into one of three places
 // each, in pieces of 16 bytes whose order within a row differs from row to row so that neither the rows
-// nor the transposing loads meet on a bank by their layout.  (Some accesses do: conflicts take 15.4e6 of the 96.3e6
-// cycles in which CUs are busy, in the case below.)  64-token chunks of 128-value keys take 150 to 157 KiB of
+// nor the transposing loads meet on a bank by their layout.  (Some accesses do: conflicts take 15.4e6 of the 98.3e6
+// cycles in which CUs are busy, in the case below.)  64-token chunks of 128-value keys take 154 to 160 KiB of
 // LDS: one block a CU.
 //
 // Few heads leave CUs idle.  Then sequences are cut into segments: what a segment does to a
@@ -64,12 +64,11 @@
 // up, the smallest first.  With an F32 state R, T, A_10, U and S for S k have three parts (PARTS = 3), all 24
 // bits: the state is off by what token-by-token FP32 is off by, 1e-7 to 7e-7 of its size over thousands of tokens.
 // (S in two parts: packed sequences 179 us beside 188, but 1.4e-6 to 3e-6 where decay is slow.)  With a BF16
-// state, or none, they have two (PARTS = 2), and the state is off by its own rounding.  (S and the U that enters
-// the state in one: states 0.0021 to 0.0042 of their size off, the most without decay and with weights up to two,
-// where the rounding is 0.0017 off.)  S for S q has two, as the U that P multiplies, and P is one BF16 value: outputs
-// are 0.0017 to 0.0023 of their size off where the rounding of an exact result is 0.0017 off.  (S for S q in one:
-// 0.0023 to 0.0029 with F32 states, 0.0024 to 0.004 with the fewer parts for others.  The case below takes 180 us, with
-// S for S k in one part 171, S for S q too 162, and U for the state too 151; packed sequences 194, with S for S q in one 188.)
+// state, or none, they have two (PARTS = 2), as S for S q, P and the U that P multiplies have in every case: outputs
+// and BF16 states are off by their one rounding, 0.0017 of their size.  What fewer parts take and lose: P in one
+// 180 us in the case below beside 184, packed sequences 195 beside 199, outputs 0.0017 to 0.0023; S for S q in one as well,
+// packed 188, outputs 0.0023 to 0.0029; S for S k and the U that enters the state in one too, where states are BF16 or
+// not given, 151 us, outputs 0.0024 to 0.004, states 0.0021 to 0.0042, the most without decay and with weights up to two.
 //
 // What is not finite.  An infinity or NaN of a later token must not meet the zeros above T's
 // and P's diagonals.  An entry of A that is not finite, from operands that are not or from finite
@@ -81,15 +80,15 @@
 // state become NaN.
 //
 // What bounds it, at 8 x 2048 tokens, 32 heads of 128 x 128 in 16 groups, BF16 states (one block a CU, 32
-// chunks): 180 to 189 us, 2.6 times its bytes' time.  A chunk takes about 12000 cycles.  Both kinds of waves wait for their
-// own chain of reads, products and conversions, with two waves a SIMD to cover for each other (matrix units 36 % busy,
-// vector instructions 51 % of the issue slots); 32 more matrix
-// instructions a wave and chunk (512 cycles) add 9 to 12 us.  What did not help there: 64 rows a block, twice the
-// blocks (255 us, since T and P are prepared twice); S k and S q in one loop that splits S once (180), a part of S q
-// in the second phase (178 to 180, or spills); loads of q and k by the waves with the state, a higher priority for the
-// waves that prepare (both slower by 7 %); reading all of A's columns ahead of the substitution (spills).
-// What did: chunks in two halves rather than T over all 64 tokens, tiles straight to LDS, and no spilled register.  (Kernels for F32 states whose rows are no whole 16 bytes spill two to seven of 256,
-// and the join for keys above 128 fifty: a wave holds 2 x 64 of M's values there.)
+// chunks): 183 to 190 us, 2.7 times its bytes' time.  A chunk takes about 12000 cycles.  Both kinds of waves wait
+// for their own chain of reads, products and conversions, with two waves a SIMD to cover for each other (matrix
+// units 37 % busy, vector instructions 52 % of the issue slots); 32 more matrix instructions a wave and chunk (512
+// cycles) add 9 to 12 us.  What did not help there: 64 rows a block, twice the blocks (255 us, since T and P are
+// prepared twice); S k and S q in one loop that splits S once (180), a part of S q in the second phase (178 to 180,
+// or spills); loads of q and k by the waves with the state, a higher priority for the waves that prepare (both slower
+// by 7 %); reading all of A's columns ahead of the substitution (spills).  What did: chunks in two halves rather
+// than T over all 64 tokens, tiles straight to LDS, and no spilled register.  (Kernels whose rows are no whole 16
+// bytes spill up to 16 of 256, and the join for keys above 128 fifty: a wave holds 2 x 64 of M's values there.)
 #include <type_traits>
 
 #include "delta_common.h"
@@ -385,15 +384,15 @@ __device__ __forceinline__ int64_t place_floats(const DeltaParams &p) { return (
 template <int KS, int C, int NT, int PARTS>
 struct Sizes {
     static constexpr int kRowsP = kHalf * 16 * NT;  // state rows of a block
-    static constexpr int kPPitch = C + 8, kTPitch = 40;  // rows of 16 lanes' 16-byte reads on banks of their own
+    static constexpr int kPPitch = C, kTPitch = 32;
     static constexpr int kBlocks = C / 16, kHalves = C / 32;
     static constexpr int kKey = 0;                                   // [3][C][KS]
     static constexpr int kQuery = kKey + 3 * C * KS * 2;             // [3][C][KS]
     static constexpr int kV = kQuery + 3 * C * KS * 2;               // [C][kRowsP]
     static constexpr int kT = kV + C * kRowsP * 2;                   // [PARTS][C][kTPitch]
     static constexpr int kOff = kT + PARTS * C * kTPitch * 2;      // [PARTS][C - 32][kTPitch]
-    static constexpr int kP = kOff + PARTS * (C - 32) * kTPitch * 2;  // [C][kPPitch]
-    static constexpr int kA = kP + C * kPPitch * 2;                  // [3 kHalves][16][kAPitch] floats
+    static constexpr int kP = kOff + PARTS * (C - 32) * kTPitch * 2;  // [2][C][kPPitch]
+    static constexpr int kA = kP + 2 * C * kPPitch * 2;              // [3 kHalves][16][kAPitch] floats
     static constexpr int kToken = kA + 3 * kHalves * 16 * kAPitch * 4;  // [3][kTokenRows][C] floats
     static constexpr int kBytes = kToken + 3 * kTokenRows * C * 4;
     static_assert(kBytes <= 160 * 1024, "more LDS than a CU has");
@@ -452,11 +451,17 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
     }
     const int chunks = (len + C - 1) / C;
 
+    // Where piece i of row r of a 16-row tile of T or A_10 (four pieces of eight inner indices), and of P, begins: sixteen
+    // lanes that read a piece of 16 rows find banks of their own.
+    const auto t_place = [](int r, int i) { return r * TP + 8 * (i ^ (r >> 2 & 3)); };
+    const auto p_place = [](int r, int i) { return r * PP + 8 * (i ^ (C == 64 ? r >> 1 & 7 : r >> 2 & 3)); };
+
     // the tiles of T and P above the diagonal that products over 32 tokens read: zeros for good
-    for (int i = tid; i < (PARTS + 1) * (kB / 2) * 16 * 4; i += kScanBlock) {
+    for (int i = tid; i < (PARTS + 2) * (kB / 2) * 16 * 4; i += kScanBlock) {
         const int piece = i & 3, row = (i >> 2) & 15, m = (i >> 6) % (kB / 2), part = (i >> 6) / (kB / 2);
-        uint16_t *to = part < PARTS ? st + (part * C + 32 * m + row) * TP : sp + (32 * m + row) * PP + 32 * m;
-        *reinterpret_cast<u32x2 *>(to + 8 * piece + 4) = u32x2{0, 0};
+        uint16_t *to = part < PARTS ? st + (part * C + 32 * m) * TP + t_place(row, piece)
+                                    : sp + ((part - PARTS) * C + 32 * m) * PP + p_place(row, 4 * m + piece);
+        *reinterpret_cast<u32x2 *>(to + 4) = u32x2{0, 0};
     }
 
     // Where a lane reads its share of k or q: row r's inner indices 32 m + 8 g .. of the state's
@@ -601,8 +606,13 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
                                                     __builtin_amdgcn_exp2f((th - uh[b][i]) + (tl - ul[b][i]))
                                               : 0.0f;
                 }
-                *reinterpret_cast<u32x2 *>(sp + t * PP + 32 * (b >> 1) + 8 * g + 4 * (b & 1)) =
-                    u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                uint16_t *to = sp + 16 * I * PP + p_place(r, 4 * (b >> 1) + g) + 4 * (b & 1);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const uint32_t h0 = pack_bf16x2(v[0], v[1]), h1 = pack_bf16x2(v[2], v[3]);
+                    *reinterpret_cast<u32x2 *>(to + part * C * PP) = u32x2{h0, h1};
+                    v[0] -= lo_f32(h0), v[1] -= hi_f32(h0), v[2] -= lo_f32(h1), v[3] -= hi_f32(h1);
+                }
             }
         };
         // ---- A of chunk j, tile by tile.  Tiles inside a half of 32 tokens are kept in FP32,
@@ -694,7 +704,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             if (kB == 2 || w >= 2) return;
 #pragma unroll
             for (int part = 0; part < PARTS; ++part) {
-                uint16_t *to = so + (part * (C - 32) + r) * TP + 8 * g + 4 * w;
+                uint16_t *to = so + part * (C - 32) * TP + t_place(r, g) + 4 * w;
                 *reinterpret_cast<u32x2 *>(to) = off[0][part];
                 *reinterpret_cast<u32x2 *>(to + 16 * TP) = off[1][part];
             }
@@ -736,7 +746,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             constexpr int I = decltype(row_constant)::value;
             const float *weight = tokens + (j % 3 * kTokenRows + kWeight) * C + 16 * (I & ~1) + 4 * g;
             const float *half = sa + 3 * (I >> 1) * 16 * kAPitch;
-            uint16_t *to = st + (16 * I + r) * TP + 8 * g;
+            uint16_t *to = st + 16 * I * TP + t_place(r, g);
             const float *diag = half + (I & 1) * 16 * kAPitch;
             f32x4_t y, a, t, w0 = lds4f(weight), w1;
 #pragma unroll
@@ -1029,7 +1039,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                     for (int a = PARTS - 1; a >= 0; --a)
 #pragma unroll
-                        for (int tt = 0; tt < 2; ++tt) af[tt][a] = lds16(so + (a * (C - 32) + 16 * tt + r) * TP + 8 * g);
+                        for (int tt = 0; tt < 2; ++tt) af[tt][a] = lds16(so + (a * (C - 32) + 16 * tt) * TP + t_place(r, g));
 #pragma unroll
                     for (int a = PARTS - 1; a >= 0; --a)
 #pragma unroll
@@ -1050,7 +1060,7 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
 #pragma unroll
                 for (int a = PARTS - 1; a >= 0; --a)
 #pragma unroll
-                    for (int tt = 0; tt < 2; ++tt) tf[tt][a] = lds16(st + (a * C + 32 * m + 16 * tt + r) * TP + 8 * g);
+                    for (int tt = 0; tt < 2; ++tt) tf[tt][a] = lds16(st + (a * C + 32 * m + 16 * tt) * TP + t_place(r, g));
                 const f32x4_t w0 = lds4f(tok + kForU * C + 32 * m + 4 * g), w1 = lds4f(tok + kForU * C + 32 * m + 16 + 4 * g);
                 auto correct = [&]() {
 #pragma unroll
@@ -1120,19 +1130,29 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
         // ---- the outputs, and the state behind the chunk
         {
             const int lane_here = here(lane), r = lane_here & 15, g = lane_here >> 4;
-            u32x4 pf[kB][kB / 2], kt[3][kB / 2];
+            u32x4 pf[2][kB][kB / 2], kt[3][kB / 2];
             float e[kB];
             auto read_keys = [&](int t) {
 #pragma unroll
                 for (int m = 0; m < kB / 2; ++m) kt[t % 3][m] = load_columns(km + 32 * m * KS + column_place(t, r, g), KS);
             };
-            if constexpr (OUT)
+            // a part of P's columns 32 m ..
+            auto read_p = [&](int m, int part) {
 #pragma unroll
-                for (int tt = 0; tt < kB; ++tt) {
-                    e[tt] = tok[kForQ * C + 16 * tt + r];
+                for (int tt = 2 * m; tt < kB; ++tt) pf[part][tt][m] = lds16(sp + (part * C + 16 * tt) * PP + p_place(r, 4 * m + g));
+            };
+            auto add_p = [&](int m, int u_part, int p_part) {
 #pragma unroll
-                    for (int m = 0; m <= tt / 2; ++m) pf[tt][m] = lds16(sp + (16 * tt + r) * PP + 32 * m + 8 * g);
-                }
+                for (int tt = 2 * m; tt < kB; ++tt)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) o[tt][n] = mfma(up[m][n][u_part], pf[p_part][tt][m], o[tt][n]);
+            };
+            if constexpr (OUT) {
+#pragma unroll
+                for (int tt = 0; tt < kB; ++tt) e[tt] = tok[kForQ * C + 16 * tt + r];
+#pragma unroll
+                for (int m = 0; m < kB / 2; ++m) read_p(m, 1);
+            }
             const float dec = __builtin_amdgcn_exp2f(tok[kSumHigh * C + C - 1] + tok[kSumLow * C + C - 1]);
             read_keys(0);
             read_keys(1);
@@ -1142,14 +1162,17 @@ __global__ __launch_bounds__(kScanBlock, 2) void delta_scan_kernel(const DeltaPa
             for (int tt = 0; tt < kB; ++tt)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) o[tt][n] *= e[tt];
+            // U's first part with P's second, whose places P's first then takes; and U's two with that
+            add_p(0, 0, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            read_p(0, 0);
+            if constexpr (kB > 2) {
+                add_p(1, 0, 1);
+                __builtin_amdgcn_sched_barrier(0);
+                read_p(1, 0);
+            }
 #pragma unroll
-            for (int m = 0; m < kB / 2; ++m)
-#pragma unroll
-                for (int part = 1; part >= 0; --part)
-#pragma unroll
-                    for (int tt = 2 * m; tt < kB; ++tt)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) o[tt][n] = mfma(up[m][n][part], pf[tt][m], o[tt][n]);
+            for (int m = 0; m < kB / 2; ++m) add_p(m, 1, 0), add_p(m, 0, 0);
             }
 #pragma unroll
             for (int t = 0; t < KS / 16; ++t) {
@@ -1364,7 +1387,7 @@ bool rows16(const void *p, int64_t a, int64_t b, int64_t c) {
 // cutting sequences into segments may save time: it takes a pass that makes M and B, with blocks
 // for M's rows too and kStatesNs a chunk, a join of kJoinNs a segment, and two more launches, each
 // with the latency of a block's first and last accesses, kCutNs.  (128 x 128, F32 states, cut into 5, 8
-// and 16 segments, 128 rows a block: 16381 tokens of 16 heads 577, 380 and 322 us, where the whole takes 1012 with 64 rows;
+// and 16 segments, 128 rows a block: 16381 tokens of 16 heads 577, 380 and 322 us, where the whole took 1012 with 64 rows;
 // into 4 and 8, 4096 tokens of 32 heads 207 and 183, whole 258; 1000 tokens of 32 heads into 4: 84, whole 71.)
 constexpr int64_t kCus = 256;
 constexpr int64_t kChunkNs[2] = {4200, 5000}, kStatesNs[2] = {4000, 4700}, kJoinNs = 2200, kCutNs = 40000;

@@ -186,8 +186,8 @@ def gated_delta_scan(q, k, v, dt, A, beta, *, dt_bias=None, dt_softplus=False, b
     [n, H, P, K] state.  ``workspace``: a uint8 buffer of ``dcconv_gated_delta_scan_workspace``
     bytes (allocated here if None).  The rest as for ``gated_delta_update``.
 
-    Sums and states are 32 bits; of the operands of the matrix products, the products of q and
-    k are rounded to bf16, and the others keep 16 bits or more."""
+    Sums and states are 32 bits, the operands of the matrix products keep 16 bits or more, and
+    the output (and a bf16 state) is rounded once."""
     lib = _s._lib()
     if v.dim() != 4 or k.dim() != 4:
         raise ValueError(f"v must be [N, T, H, P] and k [N, T, G, K], got {tuple(v.shape)} and {tuple(k.shape)}")

@@ -380,7 +380,7 @@ int64_t dcconv_selective_scan_workspace(int64_t n, int64_t t, int64_t h, int64_t
  * With qk_l2norm, q and key are first multiplied by 1 / sqrt(sum of squares +
  * l2norm_eps).  Sums, exponentials and the recurrence are FP32.  The one-token entry
  * point rounds out, and a BF16 state, once and nothing else; dcconv_gated_delta_scan
- * rounds some operands of its matrix products besides (see there).
+ * keeps 16 bits or more of the operands of its matrix products besides (see there).
  *
  * Operands of both entry points:
  *  q, key      BF16, k unit-stride values of a group.  1 <= k <= 256.
@@ -430,12 +430,12 @@ int dcconv_gated_delta_update(const void *q, const void *key, const void *v, int
  *             need not be kept and are not read from one call to the next.  Calls that
  *             may run at the same time need one each.
  * Precision.  Tokens are taken 32 or 64 at a time as matrix products with BF16 operands
- * and FP32 sums; operands that are no BF16 values are split into two or three.  An F32 state is
- * kept as exactly as FP32 products keep it (over thousands of tokens 1e-7 to 7e-7 of its size off),
- * a BF16 one is rounded when it is stored and nowhere else.  What is rounded to BF16 once on the way to
- * out are the products of q and key under their decays: outputs are 0.0017 to 0.0023 of their size off, where
- * the rounding of an exact result is 0.0017 off.  Decays below 2^-126, a token's or several tokens' together,
- * count as zero, and u and b are held to multiples of 2^-133 at best.
+ * and FP32 sums; operands that are no BF16 values are split into two or three, 16 bits or more.
+ * An F32 state is kept as exactly as FP32 products keep it (over thousands of tokens 1e-7 to 7e-7 of
+ * its size off); out, and a BF16 state, are rounded when they are stored (0.0017 of their size in the
+ * mean), and what they are off by besides is some 2^-16 of the terms they are sums of.  Decays below
+ * 2^-126, a token's or several tokens' together, count as zero, and u and b are held to multiples of
+ * 2^-133 at best.
  * What is not finite.  A NaN or infinity reaches what the recurrence lets it reach and
  * nothing else: no earlier token, no other sequence, and for v no other channel.  An
  * infinity may arrive as a NaN, and stays one.  Where states, u, or the factors that a token or
